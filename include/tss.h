@@ -50,7 +50,10 @@ enum {
 };
 
 /* ---- element types ------------------------------------------------------- */
-enum { TSS_F16 = 1, TSS_BF16 = 2, TSS_F32 = 3 };
+enum {
+  TSS_F16 = 1, TSS_BF16 = 2, TSS_F32 = 3,
+  TSS_E4M3 = 4, TSS_E5M2 = 5  /* 8 bits, OCP: largest finite values 448 and 57344 */
+};
 
 /* ---- instruction shapes (C3) -------------------------------------------- */
 enum {
@@ -576,6 +579,112 @@ enum {
 };
 int32_t tss_lds_probe(int32_t pattern, int32_t stride_words, int32_t iters, int32_t blocks, int64_t *cycles,
                       void *stream);
+
+/* ---- row operators ---------------------------------------------------------
+ * Rows of d elements, contiguous; d a multiple of 8; dtype TSS_F16, TSS_BF16
+ * or TSS_F32; sums and statistics in fp32, each output rounded once, to
+ * nearest even.  8-bit outputs carry one fp32 scale for each block of 1 or
+ * 128 rows x 128 columns: scale = max(largest |value| of the block, 1e-30) /
+ * largest value of the type, stored column-block-major, scale[col / 128][row]
+ * or scale[col / 128][row / 128] (the last block of a row or column may be
+ * short).  A NaN in a block makes its scale and all its values NaN.
+ */
+
+/*
+ * h = x + residual; y = h / sqrt(mean(h^2) + eps) * weight, row by row.
+ * residual may be NULL (h = x).  y: out_dtype dtype, or TSS_E4M3 with
+ * scale[ceil(d / 128)][rows] (NULL otherwise).  residual_out (may be NULL):
+ * h rounded to dtype; it may be residual or x itself.  y may be x when
+ * out_dtype is dtype.  rstd (may be NULL): rows fp32, 1 / sqrt(...).
+ * weight: d elements of dtype.  d <= 32768.  x, residual, weight, y and
+ * residual_out 16-byte aligned.  rows == 0: nothing to do.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_UNSUPPORTED (d),
+ * TSS_E_HIP.
+ */
+int32_t tss_rms_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, const void *residual, const void *weight,
+                     float eps, int32_t out_dtype, void *y, float *scale, void *residual_out, float *rstd,
+                     void *stream);
+
+/*
+ * Gradients of tss_rms_norm from dy, its h and rstd:
+ *   dx = dh + rstd (dy weight - xhat mean(dy weight xhat)),  xhat = h rstd
+ * (the gradient of x and of residual; dh, which may be NULL, is what arrives
+ * through residual_out), and dweight[d] (fp32) = sum over rows of dy xhat,
+ * added in a fixed order.  dx may be dy or dh.  workspace: device memory of
+ * at least tss_rms_norm_backward_workspace_size(rows, d) bytes, 16-byte
+ * aligned, scratch.  rows == 0: dweight is zero-filled.
+ * Errors: as tss_rms_norm; TSS_E_ARG for a missing or small workspace.
+ */
+int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
+                              const void *weight, const float *rstd, const void *dh, void *dx, float *dweight,
+                              void *workspace, int64_t workspace_bytes, void *stream);
+int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d);
+
+/*
+ * q (rows x d in fp8 = TSS_E4M3 or TSS_E5M2) and its scales from x, with
+ * blocks of block_rows (1 or 128) x 128.  gated: x has rows of 2 d elements,
+ * gate then up, and silu(gate) * up is quantised.  x and q 16-byte aligned.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, int32_t fp8,
+                         int32_t block_rows, void *q, float *scale, void *stream);
+
+/* ---- 8-bit and grouped products -------------------------------------------- */
+
+/*
+ * C = (A sa) (B sb)^T: A is M x K (a_dtype TSS_E4M3 or TSS_E5M2) with
+ * sa[ceil(K / 128)][M]; B is N x K (TSS_E4M3) with sb[ceil(K / 128)][N]
+ * (b_block_rows 1) or sb[ceil(K / 128)][ceil(N / 128)] (128); C is M x N,
+ * out_dtype TSS_F16, TSS_BF16 or TSS_F32.  Within a block of 128 of K the
+ * products are summed by the matrix cores in fp32, the blocks' sums are
+ * scaled and added in fp32.
+ * workspace: tss_gemm_fp8_workspace_size(M, N, K) bytes of device memory
+ * (the partial sums of a product whose K is split over workgroups; may be
+ * NULL when that is 0), 16-byte aligned, scratch.
+ * K a multiple of 16 and below 2^22, N a multiple of 8; A, B, C 16-byte
+ * aligned, sa and sb 4-byte; each operand below 2 GiB.  M == 0 or N == 0: nothing to do.  K == 0: C is
+ * zero-filled (A, B, sa and sb may then be NULL).
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const void *A, const void *B, const float *sa,
+                     const float *sb, int32_t b_block_rows, void *C, int32_t out_dtype, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * Products grouped by expert: the T rows of A (and C) are sorted by group,
+ * sizes[E] (int32, device memory) says how many belong to each, and the rows
+ * past their sum belong to none.  A negative size counts as 0, and groups
+ * end at row T.  The sizes are read on the device: no host synchronisation,
+ * and a captured graph follows them from replay to replay.  1 <= E <= 4096.
+ *
+ * tss_gemm_grouped: C[rows of e] = A[rows of e] B[e], A T x K, B E x K x N,
+ * C T x N (rows of no group: zero); dtype TSS_F16 or TSS_BF16, out_dtype
+ * dtype or TSS_F32, fp32 accumulation.
+ *
+ * tss_gemm_grouped_backward: dA[rows of e] = dC[rows of e] B[e]^T (dtype;
+ * rows of no group: zero) and dB[e] = A[rows of e]^T dC[rows of e] (db_dtype
+ * dtype or TSS_F32; groups without rows: zero).  dA or dB may be NULL: that
+ * one is not computed (and B, or A, may then be NULL too).
+ *
+ * tss_gemm_grouped_fp8: C[rows of e] = (A sa)[rows of e] (B[e] sb[e])^T, A
+ * T x K (a_dtype TSS_E4M3 or TSS_E5M2) with sa[ceil(K / 128)][T], B E x N x K
+ * (TSS_E4M3) with sb[e][ceil(K / 128)][ceil(N / 128)]; out_dtype TSS_F16,
+ * TSS_BF16 or TSS_F32; K a multiple of 16 below 2^22.
+ *
+ * K and N multiples of 8; every tensor 16-byte aligned (sizes, sa, sb
+ * 4-byte); A, C and one group's B below 2 GiB each.  T == 0 or N == 0: C is
+ * empty; K == 0: C is zero-filled.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_gemm_grouped(int64_t T, int64_t E, int64_t K, int64_t N, int32_t dtype, const void *A, const void *B,
+                         const int32_t *sizes, void *C, int32_t out_dtype, void *stream);
+int32_t tss_gemm_grouped_backward(int64_t T, int64_t E, int64_t K, int64_t N, int32_t dtype, const void *dC,
+                                  const void *A, const void *B, const int32_t *sizes, void *dA, void *dB,
+                                  int32_t db_dtype, void *stream);
+int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t a_dtype, const void *A,
+                             const void *B, const float *sa, const float *sb, const int32_t *sizes, void *C,
+                             int32_t out_dtype, void *stream);
 
 /* The configuration tss_gemm / tss_conv2d would take for a NULL cfg. */
 int32_t tss_gemm_default_config(int64_t batch, int64_t M, int64_t N, int64_t K, int32_t dtype,

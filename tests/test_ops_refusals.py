@@ -1,0 +1,172 @@
+"""What the row operators and the 8-bit and grouped products refuse, before
+any device work: through the C ABI with addresses that are never touched, and
+through the Python calls with host tensors."""
+import pytest
+import torch
+
+import tile_size_selection_amd as tss
+from tile_size_selection_amd import _capi as C
+
+P = 1 << 20       # a 16-byte aligned address
+ODD = P + 8       # not 16-byte aligned
+ARG, DTYPE, ALIGN, UNSUP = C.TSS_E_ARG, C.TSS_E_DTYPE, C.TSS_E_ALIGN, C.TSS_E_UNSUPPORTED
+F16, BF16, F32, E4M3, E5M2 = C.TSS_F16, C.TSS_BF16, C.TSS_F32, C.TSS_E4M3, C.TSS_E5M2
+
+
+def _with(base, **changes):
+    return list({**base, **changes}.values())
+
+
+NORM = dict(rows=4, d=64, dtype=BF16, x=P, residual=P, weight=P, eps=1e-6, out_dtype=BF16, y=P, scale=None, h=P, rstd=P,
+            stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(rows=1 << 31), ARG), (dict(rows=1 << 23), ARG), (dict(d=12), ALIGN),
+    (dict(d=32776), UNSUP), (dict(dtype=9), DTYPE), (dict(dtype=E4M3), DTYPE), (dict(out_dtype=F16), DTYPE),
+    (dict(out_dtype=E5M2), DTYPE), (dict(out_dtype=E4M3), ARG), (dict(x=None), ARG), (dict(weight=None), ARG),
+    (dict(y=None), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG), (dict(x=ODD), ALIGN),
+    (dict(residual=ODD), ALIGN), (dict(weight=ODD), ALIGN), (dict(y=ODD), ALIGN), (dict(h=ODD), ALIGN)])
+def test_norm_refuses(change, status):
+    assert C.lib().tss_rms_norm(*_with(NORM, **change)) == status
+
+
+BACK = dict(rows=4, d=64, dtype=F32, dy=P, h=P, weight=P, rstd=P, dh=None, dx=P, dweight=P, ws=P, ws_bytes=1 << 20,
+            stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), ARG), (dict(d=20), ALIGN), (dict(d=40000), UNSUP), (dict(dtype=E4M3), DTYPE), (dict(dy=None), ARG),
+    (dict(h=None), ARG), (dict(rstd=None), ARG), (dict(dx=None), ARG), (dict(dweight=None), ARG), (dict(ws=None), ARG),
+    (dict(ws_bytes=4 * 64 * 4 - 1), ARG), (dict(ws=ODD), ALIGN), (dict(dh=ODD), ALIGN), (dict(dx=ODD), ALIGN)])
+def test_norm_backward_refuses(change, status):
+    assert C.lib().tss_rms_norm_backward(*_with(BACK, **change)) == status
+
+
+def test_norm_backward_workspace():
+    size = C.lib().tss_rms_norm_backward_workspace_size
+    assert size(0, 64) == 0 and size(4, 64) >= 4 * 64 * 4
+    assert size(-1, 64) == ARG and size(4, 12) == ALIGN and size(4, 40000) == UNSUP
+
+
+QUANT = dict(rows=4, d=64, dtype=BF16, x=P, gated=0, fp8=E4M3, block_rows=1, q=P, scale=P, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(d=4), ALIGN), (dict(dtype=E4M3), DTYPE), (dict(fp8=BF16), DTYPE),
+    (dict(block_rows=64), ARG), (dict(x=None), ARG), (dict(q=None), ARG), (dict(scale=None), ARG), (dict(x=ODD), ALIGN),
+    (dict(q=ODD), ALIGN), (dict(rows=(1 << 31) - 1, d=1 << 20), ARG)])
+def test_quantize_refuses(change, status):
+    assert C.lib().tss_quantize_fp8(*_with(QUANT, **change)) == status
+
+
+GEMM = dict(M=4, N=64, K=128, a_dtype=E4M3, A=P, B=P, sa=P, sb=P, b_rows=128, C=P, out=BF16, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(M=-1), ARG), (dict(N=-8), ARG), (dict(K=-16), ARG), (dict(K=136), ALIGN), (dict(N=12), ALIGN),
+    (dict(a_dtype=BF16), DTYPE), (dict(out=E4M3), DTYPE), (dict(b_rows=64), ARG), (dict(A=None), ARG), (dict(B=None), ARG),
+    (dict(sa=None), ARG), (dict(sb=None), ARG), (dict(C=None), ARG), (dict(A=ODD), ALIGN), (dict(B=ODD), ALIGN),
+    (dict(C=ODD), ALIGN), (dict(sa=P + 2), ALIGN), (dict(sb=P + 2), ALIGN), (dict(M=1 << 20, K=2048), ARG),
+    (dict(N=1 << 20, K=2048), ARG), (dict(M=1 << 31), ARG)])
+def test_gemm_fp8_refuses(change, status):
+    assert C.lib().tss_gemm_fp8(*_with(GEMM, **change)) == status
+
+
+def test_gemm_fp8_wants_its_workspace():
+    need = tss.gemm_fp8_workspace_size(100, 128, 8192)
+    assert need > 0 and need % (100 * 128 * 4) == 0
+    big = dict(GEMM, M=100, N=128, K=8192)
+    assert C.lib().tss_gemm_fp8(*big.values()) == ARG
+    assert C.lib().tss_gemm_fp8(*_with(big, ws=P, ws_bytes=need - 1)) == ARG
+    assert C.lib().tss_gemm_fp8(*_with(big, ws=ODD, ws_bytes=need)) == ALIGN
+    assert tss.gemm_fp8_workspace_size(0, 128, 8192) == 0
+    with pytest.raises(tss.TssError):
+        tss.gemm_fp8_workspace_size(100, 128, 8190)
+
+
+GROUPED = dict(T=4, E=2, K=64, N=64, dtype=BF16, A=P, B=P, sizes=P, C=P, out=BF16, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), ARG), (dict(E=0), ARG), (dict(E=4097), ARG), (dict(K=12), ALIGN), (dict(N=12), ALIGN),
+    (dict(dtype=F32), DTYPE), (dict(out=F16), DTYPE), (dict(A=None), ARG), (dict(B=None), ARG), (dict(sizes=None), ARG),
+    (dict(C=None), ARG), (dict(A=ODD), ALIGN), (dict(B=ODD), ALIGN), (dict(C=ODD), ALIGN), (dict(sizes=P + 2), ALIGN),
+    (dict(T=1 << 24), ARG), (dict(K=1 << 15, N=1 << 15), ARG)])
+def test_gemm_grouped_refuses(change, status):
+    assert C.lib().tss_gemm_grouped(*_with(GROUPED, **change)) == status
+
+
+GROUPED_BACK = dict(T=4, E=2, K=64, N=64, dtype=F16, dC=P, A=P, B=P, sizes=P, dA=P, dB=P, db=F32, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(E=0), ARG), (dict(K=4), ALIGN), (dict(dtype=E4M3), DTYPE), (dict(db=BF16), DTYPE), (dict(dC=None), ARG),
+    (dict(A=None), ARG), (dict(B=None), ARG), (dict(sizes=None), ARG), (dict(dA=ODD), ALIGN), (dict(dB=ODD), ALIGN),
+    (dict(dA=None, dB=None, sizes=None), C.TSS_OK)])
+def test_gemm_grouped_backward_refuses(change, status):
+    assert C.lib().tss_gemm_grouped_backward(*_with(GROUPED_BACK, **change)) == status
+
+
+GROUPED8 = dict(T=4, E=2, K=64, N=64, a_dtype=E4M3, A=P, B=P, sa=P, sb=P, sizes=P, C=P, out=BF16, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=-1), ARG), (dict(E=0), ARG), (dict(K=24), ALIGN), (dict(a_dtype=F16), DTYPE), (dict(out=E5M2), DTYPE),
+    (dict(sa=None), ARG), (dict(sb=None), ARG), (dict(sizes=None), ARG), (dict(B=ODD), ALIGN), (dict(sa=P + 1), ALIGN)])
+def test_gemm_grouped_fp8_refuses(change, status):
+    assert C.lib().tss_gemm_grouped_fp8(*_with(GROUPED8, **change)) == status
+
+
+def z(*shape, t=torch.bfloat16):
+    return torch.zeros(*shape, dtype=t)
+
+
+F8, S = torch.float8_e4m3fn, torch.float32
+CALLS = {
+    "norm: host tensors": lambda: tss.rms_norm(z(4, 64), z(64)),
+    "norm: one dimension": lambda: tss.rms_norm(z(64), z(64)),
+    "norm: integers": lambda: tss.rms_norm(z(4, 64, t=torch.int32), z(64)),
+    "norm: strided rows": lambda: tss.rms_norm(z(4, 128)[:, :64], z(64)),
+    "norm: weight's length": lambda: tss.rms_norm(z(4, 64), z(32)),
+    "norm: weight's type": lambda: tss.rms_norm(z(4, 64), z(64, t=torch.float32)),
+    "norm: output type": lambda: tss.rms_norm(z(4, 64), z(64), out_dtype="e5m2"),
+    "norm: scale without 8 bits": lambda: tss.rms_norm(z(4, 64), z(64), scale=z(1, 4, t=S)),
+    "norm: residual_out alone": lambda: tss.rms_norm(z(4, 64), z(64), residual_out=z(4, 64)),
+    "norm: rstd's length": lambda: tss.rms_norm(z(4, 64), z(64), rstd=z(3, t=S)),
+    "backward: rstd's type": lambda: tss.rms_norm_backward(z(4, 64), z(4, 64), z(64), z(4)),
+    "backward: dh's shape": lambda: tss.rms_norm_backward(z(4, 64), z(4, 64), z(64), z(4, t=S), z(4, 32)),
+    "backward: host tensors": lambda: tss.rms_norm_backward(z(4, 64), z(4, 64), z(64), z(4, t=S)),
+    "quantize: type": lambda: tss.quantize_fp8(z(4, 64), "bf16"),
+    "quantize: block_rows": lambda: tss.quantize_fp8(z(4, 64), block_rows=2),
+    "quantize: odd gated row": lambda: tss.quantize_fp8(z(4, 65), gated=True),
+    "quantize: scale's shape": lambda: tss.quantize_fp8(z(4, 256), scale=z(4, 2, t=S)),
+    "quantize: host tensors": lambda: tss.quantize_fp8(z(4, 64)),
+    "gemm_fp8: A's type": lambda: tss.gemm_fp8(z(4, 128), z(8, 128, t=F8), z(1, 4, t=S), z(1, 1, t=S)),
+    "gemm_fp8: B's type": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 128, t=torch.float8_e5m2), z(1, 4, t=S), z(1, 1, t=S)),
+    "gemm_fp8: inner sizes": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 256, t=F8), z(1, 4, t=S), z(1, 1, t=S)),
+    "gemm_fp8: sa's order": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 128, t=F8), z(4, 1, t=S), z(1, 1, t=S)),
+    "gemm_fp8: sb's shape": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 128, t=F8), z(1, 4, t=S), z(1, 2, t=S)),
+    "gemm_fp8: out type": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 128, t=F8), z(1, 4, t=S), z(1, 1, t=S), "e4m3"),
+    "gemm_fp8: host tensors": lambda: tss.gemm_fp8(z(4, 128, t=F8), z(8, 128, t=F8), z(1, 4, t=S), z(1, 1, t=S)),
+    "grouped: sizes' type": lambda: tss.gemm_grouped(z(4, 64), z(2, 64, 8), z(2, t=torch.int64)),
+    "grouped: groups": lambda: tss.gemm_grouped(z(4, 64), z(2, 64, 8), z(3, t=torch.int32)),
+    "grouped: inner sizes": lambda: tss.gemm_grouped(z(4, 64), z(2, 32, 8), z(2, t=torch.int32)),
+    "grouped: types differ": lambda: tss.gemm_grouped(z(4, 64), z(2, 64, 8, t=torch.float16), z(2, t=torch.int32)),
+    "grouped: strided B": lambda: tss.gemm_grouped(z(4, 64), z(2, 8, 64).transpose(1, 2), z(2, t=torch.int32)),
+    "grouped: host tensors": lambda: tss.gemm_grouped(z(4, 64), z(2, 64, 8), z(2, t=torch.int32)),
+    "grouped backward: unneeded output": lambda: tss.gemm_grouped_backward(
+        z(4, 8), z(4, 64), z(2, 64, 8), z(2, t=torch.int32), dA=z(4, 64), need_dA=False),
+    "grouped backward: dC's shape": lambda: tss.gemm_grouped_backward(
+        z(4, 16), z(4, 64), z(2, 64, 8), z(2, t=torch.int32)),
+    "grouped fp8: sb's shape": lambda: tss.gemm_grouped_fp8(
+        z(4, 128, t=F8), z(2, 8, 128, t=F8), z(1, 4, t=S), z(2, 1, 8, t=S), z(2, t=torch.int32)),
+    "grouped fp8: host tensors": lambda: tss.gemm_grouped_fp8(
+        z(4, 128, t=F8), z(2, 8, 128, t=F8), z(1, 4, t=S), z(2, 1, 1, t=S), z(2, t=torch.int32)),
+}
+
+
+@pytest.mark.parametrize("call", CALLS.values(), ids=CALLS.keys())
+def test_python_calls_refuse(call):
+    with pytest.raises(ValueError):
+        call()

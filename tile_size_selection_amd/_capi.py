@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_HERE, "libtss.so")
 TSS_OK, TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_INFEASIBLE, TSS_E_HIP, TSS_E_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 TSS_E_SCRATCH = -7
 TSS_SCRATCH_BYTES = 64 << 20
-TSS_F16, TSS_BF16, TSS_F32 = 1, 2, 3
+TSS_F16, TSS_BF16, TSS_F32, TSS_E4M3, TSS_E5M2 = 1, 2, 3, 4, 5
 LDS_PATTERN = {"b32": 1, "b128": 2, "tr_b64": 3, "gemm_a": 4, "gemm_a_plain": 5, "gemm_b": 6, "gemm_b_plain": 7}
 INSTR = {"mfma32": 1, "mfma16": 2, "mma": 16, "wgmma": 17, "simt": 18}
 INSTR_NAME = {v: k for k, v in INSTR.items()}
@@ -66,7 +66,10 @@ EXPORTS = ["tss_device_gfx950", "tss_device_pages", "tss_device_query", "tss_eva
            "tss_lds_probe", "tss_gemm_default_config", "tss_status_string", "tss_instr_shape", "tss_gemm_splitk",
            "tss_gemm_splitk_workspace_size", "tss_conv2d_splitk", "tss_conv2d_splitk_workspace_size",
            "tss_conv2d_nhwc", "tss_conv2d_nhwc_workspace_size", "tss_gemm_autotune",
-           "tss_splitk_plan", "tss_conv_splitk_plan", "tss_conv2d_splitk_noalloc"]
+           "tss_splitk_plan", "tss_conv_splitk_plan", "tss_conv2d_splitk_noalloc",
+           "tss_rms_norm", "tss_rms_norm_backward", "tss_rms_norm_backward_workspace_size", "tss_quantize_fp8",
+           "tss_gemm_fp8", "tss_gemm_fp8_workspace_size", "tss_gemm_grouped", "tss_gemm_grouped_backward",
+           "tss_gemm_grouped_fp8"]
 
 _lib = None
 
@@ -111,6 +114,15 @@ def lib():
     L.tss_conv2d_splitk_noalloc.argtypes = [i64] * 16 + [i32, i32, vp, vp, vp, i32, P(TileConfig), vp]
     L.tss_splitk_plan.argtypes = [i64, i64, i64, i64, i32, P(Device), P(Verdict), P(i32)]
     L.tss_conv_splitk_plan.argtypes = [i64, i64, i64, i64, i32, P(Device), P(Verdict), P(i32)]
+    L.tss_rms_norm.argtypes = [i64, i64, i32, vp, vp, vp, ctypes.c_float, i32, vp, vp, vp, vp, vp]
+    L.tss_rms_norm_backward.argtypes = [i64, i64, i32] + [vp] * 8 + [i64, vp]
+    L.tss_rms_norm_backward_workspace_size.argtypes = [i64, i64]
+    L.tss_quantize_fp8.argtypes = [i64, i64, i32, vp, i32, i32, i32, vp, vp, vp]
+    L.tss_gemm_fp8.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, i32, vp, i32, vp, i64, vp]
+    L.tss_gemm_fp8_workspace_size.argtypes = [i64, i64, i64]
+    L.tss_gemm_grouped.argtypes = [i64] * 4 + [i32, vp, vp, vp, vp, i32, vp]
+    L.tss_gemm_grouped_backward.argtypes = [i64] * 4 + [i32] + [vp] * 6 + [i32, vp]
+    L.tss_gemm_grouped_fp8.argtypes = [i64] * 4 + [i32] + [vp] * 6 + [i32, vp]
     L.tss_status_string.argtypes = [i32]
     L.tss_status_string.restype = ctypes.c_char_p
     for n in EXPORTS:
@@ -120,6 +132,8 @@ def lib():
     L.tss_gemm_splitk_workspace_size.restype = i64
     L.tss_conv2d_splitk_workspace_size.restype = i64
     L.tss_conv2d_nhwc_workspace_size.restype = i64
+    L.tss_rms_norm_backward_workspace_size.restype = i64
+    L.tss_gemm_fp8_workspace_size.restype = i64
     _lib = L
     return L
 

@@ -44,6 +44,7 @@ FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++20", "-fPIC", "-Wall", "-Wno-u
 def sources():
     return ([os.path.join(CSRC, "planner.cpp"), os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "lds_probe.hip"),
              os.path.join(CSRC, "noalloc.cpp")]
+            + [os.path.join(CSRC, f) for f in ("norm.hip", "quantize.hip", "gemm_fp8.hip", "gemm_grouped.hip")]
             + sorted(glob.glob(os.path.join(CSRC, "inst", "*.hip"))))
 
 

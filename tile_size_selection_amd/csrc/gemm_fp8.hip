@@ -1,0 +1,221 @@
+// Host side of the 8-bit products: tss_gemm_fp8, tss_gemm_grouped_fp8.
+#include <atomic>
+
+#include "gemm_fp8_kernel.h"
+#include "splitk_reduce.h"
+
+using namespace tss;
+
+namespace {
+
+constexpr int64_t kTwoGiB = int64_t(1) << 31;
+
+bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+
+using Tile256 = Fp8Geometry<256, 256, 2, 8, 2>;
+using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;
+using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;
+
+// How a product is run: by tiles of bm x bn (K in `splits` ranges), or
+// (bn == 16) by the kernel for few rows.
+struct Plan {
+  int bm, bn, splits;
+};
+
+constexpr int kCUs = 256;
+
+Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
+  if (M <= 16) return {16, 16, 1};
+  if (M <= 32) return {32, 16, 1};
+  auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
+  if (!exact && blocks(256, 256) >= kCUs) return {256, 256, 1};
+  if (blocks(128, 128) >= kCUs) return {128, 128, 1};
+  const int64_t b = blocks(64, 128), kb = (K + 127) / 128;
+  int64_t s = b >= kCUs ? 1 : kCUs / b;
+  if (s > kb / 4) s = kb / 4;  // at least four steps of K a range
+  if (s < 1) s = 1;
+  return {64, 128, int(s)};
+}
+
+Plan plan_grouped(int64_t T, int64_t E, bool exact) {
+  const int64_t rows = T / E;  // of an average group
+  if (rows <= 16) return {16, 16, 1};
+  if (rows <= 32) return {32, 16, 1};
+  if (rows <= 64) return {64, 128, 1};
+  if (rows <= 256 || exact) return {128, 128, 1};
+  return {256, 256, 1};
+}
+
+template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+hipError_t launch_tile(const Fp8Args &a, int64_t blocks, hipStream_t s) {
+  // dynamic LDS above 64 KiB needs an attribute per kernel and device, set on the first launch there
+  static std::atomic<uint64_t> attr_set{0};
+  auto kernel = gemm_fp8_tile_kernel<G, A_E5M2, B_ROWS, GROUPED, EXACT>;
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (!bit || !(attr_set.load(std::memory_order_acquire) & bit)) {
+    e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
+    if (e != hipSuccess) return e;
+    attr_set.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(G::THREADS), G::LDS_BYTES, s, a);
+  return hipGetLastError();
+}
+
+template <int MT, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+hipError_t launch_rows(const Fp8Args &a, int64_t blocks, hipStream_t s) {
+  const int nk = (a.K + 127) / 128;
+  int nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
+  nw = nw < 1 ? 1 : nw > 16 ? 16 : nw;
+  hipLaunchKernelGGL((gemm_fp8_rows_kernel<MT, A_E5M2, B_ROWS, GROUPED, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64),
+                     nw * MT * 1024, s, a);
+  return hipGetLastError();
+}
+
+template <bool A_E5M2, bool B_ROWS, bool GROUPED>
+hipError_t launch(Fp8Args &a, const Plan &pl, bool exact, hipStream_t s, int32_t *status) {
+  a.tiles_n = int32_t((a.N + pl.bn - 1) / pl.bn);
+  const int64_t tiles_m = GROUPED ? max_group_tiles(a.M, a.groups, pl.bm) : (int64_t(a.M) + pl.bm - 1) / pl.bm;
+  a.tiles_m = int32_t(tiles_m);
+  const int64_t blocks = tiles_m * a.tiles_n * a.splits;
+  if (blocks * 1024 > int64_t(UINT32_MAX)) {  // the launch's thread count is 32 bits
+    *status = TSS_E_ARG;
+    return hipSuccess;
+  }
+  auto go = [&](auto exact) {
+    constexpr bool X = decltype(exact)::value;
+    if (pl.bn == 16)
+      return pl.bm == 16 ? launch_rows<1, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s)
+                         : launch_rows<2, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+    if constexpr (!X)
+      if (pl.bm == 256) return launch_tile<Tile256, A_E5M2, B_ROWS, GROUPED, false>(a, blocks, s);
+    if (pl.bm == 128) return launch_tile<Tile128, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+    return launch_tile<Tile64, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+  };
+  return exact ? go(std::true_type{}) : go(std::false_type{});
+}
+
+int32_t check_types(int32_t a_dtype, int32_t out_dtype) {
+  if (a_dtype != TSS_E4M3 && a_dtype != TSS_E5M2) return TSS_E_DTYPE;
+  if (out_dtype != TSS_F16 && out_dtype != TSS_BF16 && out_dtype != TSS_F32) return TSS_E_DTYPE;
+  return TSS_OK;
+}
+
+int32_t check_sizes(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return TSS_E_ARG;
+  if (K % 16 || N % 8) return TSS_E_ALIGN;
+  if (M * K >= kTwoGiB || N * K >= kTwoGiB || M * N * 2 >= kTwoGiB * 4) return TSS_E_ARG;
+  // the kernels' byte offsets are 32 bits: 256 rows of K, and a row of scales for each 128 of K
+  if (K >= int64_t(1) << 22) return TSS_E_ARG;
+  if ((K + 127) / 128 * 4 * (M > N ? M : N) >= kTwoGiB) return TSS_E_ARG;
+  return TSS_OK;
+}
+
+// K of a range: a multiple of 128; the ranges that hold any.
+void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
+  const int64_t kb = (K + 127) / 128, per = (kb + splits - 1) / splits;
+  *k_split = int32_t(per * 128);
+  *n = int32_t((kb + per - 1) / per);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
+  const int32_t st = check_sizes(M, N, K);
+  if (st != TSS_OK) return st;
+  if (M == 0 || N == 0 || K == 0) return 0;
+  // the larger of what a 16-bit and an fp32 output take
+  int32_t n, ks, most = 1;
+  for (bool exact : {false, true}) {
+    split_ranges(K, plan_product(M, N, K, exact).splits, &n, &ks);
+    most = n > most ? n : most;
+  }
+  return most > 1 ? most * M * N * 4 : 0;
+}
+
+int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const void *A, const void *B, const float *sa,
+                     const float *sb, int32_t b_block_rows, void *C, int32_t out_dtype, void *workspace,
+                     int64_t workspace_bytes, void *stream) {
+  int32_t st = check_types(a_dtype, out_dtype);
+  if (st == TSS_OK) st = check_sizes(M, N, K);
+  if (st != TSS_OK) return st;
+  if (b_block_rows != 1 && b_block_rows != 128) return TSS_E_ARG;
+  if (M == 0 || N == 0) return TSS_OK;
+  if (!C || (K > 0 && (!A || !B || !sa || !sb))) return TSS_E_ARG;
+  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(sa, 4) || misaligned(sb, 4))
+    return TSS_E_ALIGN;
+  const bool exact = out_dtype == TSS_F32;
+  const Plan pl = K ? plan_product(M, N, K, exact) : Plan{64, 128, 1};
+  Fp8Args a{};
+  a.A = static_cast<const uint8_t *>(A);
+  a.B = static_cast<const uint8_t *>(B);
+  a.sa = sa;
+  a.sb = sb;
+  a.M = int32_t(M);
+  a.N = int32_t(N);
+  a.K = int32_t(K);
+  a.groups = 1;
+  a.sb_cols = int32_t(b_block_rows == 1 ? N : (N + 127) / 128);
+  a.splits = 1;
+  a.k_split = a.K;
+  if (K) split_ranges(K, pl.splits, &a.splits, &a.k_split);
+  const bool split = a.splits > 1;
+  if (split) {
+    if (!workspace || workspace_bytes < a.splits * M * N * 4) return TSS_E_ARG;
+    if (misaligned(workspace, 16)) return TSS_E_ALIGN;
+  }
+  a.C = split ? workspace : C;
+  a.out_dtype = split ? TSS_F32 : out_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t err;
+  if (a_dtype == TSS_E5M2)
+    err = b_block_rows == 1 ? launch<true, true, false>(a, pl, exact, s, &st) : launch<true, false, false>(a, pl, exact, s, &st);
+  else
+    err = b_block_rows == 1 ? launch<false, true, false>(a, pl, exact, s, &st) : launch<false, false, false>(a, pl, exact, s, &st);
+  if (st != TSS_OK) return st;
+  if (err == hipSuccess && split)
+    err = launch_splitk_reduce(static_cast<const float *>(workspace), C, out_dtype, 1, M * N, a.splits, s);
+  return err == hipSuccess ? TSS_OK : TSS_E_HIP;
+}
+
+int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t a_dtype, const void *A,
+                             const void *B, const float *sa, const float *sb, const int32_t *sizes, void *C,
+                             int32_t out_dtype, void *stream) {
+  int32_t st = check_types(a_dtype, out_dtype);
+  if (st == TSS_OK) st = check_sizes(T, N, K);
+  if (st != TSS_OK) return st;
+  if (E < 1 || E > kMaxGroups) return TSS_E_ARG;
+  if (T == 0 || N == 0) return TSS_OK;
+  if (!C || !sizes || (K > 0 && (!A || !B || !sa || !sb))) return TSS_E_ARG;
+  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(sa, 4) || misaligned(sb, 4) ||
+      misaligned(sizes, 4))
+    return TSS_E_ALIGN;
+  Fp8Args a{};
+  a.A = static_cast<const uint8_t *>(A);
+  a.B = static_cast<const uint8_t *>(B);
+  a.sa = sa;
+  a.sb = sb;
+  a.C = C;
+  a.sizes = sizes;
+  a.M = int32_t(T);
+  a.N = int32_t(N);
+  a.K = int32_t(K);
+  a.groups = int32_t(E);
+  a.sb_cols = int32_t((N + 127) / 128);
+  a.splits = 1;
+  a.k_split = a.K;
+  a.out_dtype = out_dtype;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool exact = out_dtype == TSS_F32;
+  const Plan pl = plan_grouped(T, E, exact);
+  const hipError_t err = a_dtype == TSS_E5M2 ? launch<true, false, true>(a, pl, exact, s, &st)
+                                             : launch<false, false, true>(a, pl, exact, s, &st);
+  if (st != TSS_OK) return st;
+  return err == hipSuccess ? TSS_OK : TSS_E_HIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,437 @@
+// C = (A sa) (B sb)^T on 8-bit operands, A M x K and B N x K, both
+// K-contiguous, with fp32 scales for each 128 of K (of a row of A; of a row
+// or of 128 rows of B):
+//
+//   C[m][n] = sum over blocks j of 128:  sa[j][m] sb[j][n] sum_{k in j} A[m][k] B[n][k]
+//
+// One v_mfma_f32_16x16x128_f8f6f4 sums exactly one block of 128 of a 16 x 16
+// tile, so a block's sum leaves the matrix core in 4 registers, and 4 fp32
+// FMAs scale it into the accumulators: 16 vector cycles beside the MFMA's 32.
+// (The MFMA's own block scales are powers of two over 32 elements; these are
+// any fp32 over 128, hence the unscaled form.)  As in the fp16 kernel the B
+// fragment is the MFMA's row operand: a lane holds 4 consecutive columns of
+// one row of C.
+//
+// The 8-bit MFMA adds its products in groups with fewer bits than fp32: a
+// product 2^-14 of the largest beside it is lost (measured), which leaves the
+// result 1.7e-5 of its norm off, far below the rounding of a 16-bit output
+// (2^-9) but not of an fp32 one (plain fp32 sums: 8e-7).  With EXACT, taken
+// for fp32 outputs, the fragments are widened to fp16 (exactly: e4m3 and e5m2
+// are subsets of it) and multiplied by v_mfma_f32_16x16x32_f16, which adds in
+// fp32, at half the rate.
+//
+// Two kernels: gemm_fp8_tile_kernel stages BM x 128 and BN x 128 tiles of the
+// operands through LDS; gemm_fp8_rows_kernel, for few rows, streams B from
+// memory straight into registers.
+#pragma once
+#include "gemm_kernel.h"
+
+namespace tss {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+struct Fp8Args {
+  const uint8_t *A;   // [M][K]
+  const uint8_t *B;   // [groups][N][K]
+  const float *sa;    // [ceil(K / 128)][M]
+  const float *sb;    // [groups][ceil(K / 128)][sb_cols]
+  void *C;            // [M][N]; split K: [splits][M][N] fp32
+  const int32_t *sizes;  // grouped: rows of each group
+  int32_t M, N, K, groups;
+  int32_t sb_cols;    // N, or ceil(N / 128)
+  int32_t tiles_m, tiles_n, splits;
+  int32_t k_split;    // K of a range, a multiple of 128
+  int32_t out_dtype;
+};
+
+// A fragment: the 32 bytes that a lane holds of a block of 128 of K, as they
+// are or widened to fp16.
+template <bool EXACT>
+struct Fragment;
+
+template <>
+struct Fragment<false> {
+  i32x8 v;
+  template <bool E5M2>
+  __device__ __forceinline__ void set(i32x8 x) { v = x; }
+};
+
+template <>
+struct Fragment<true> {
+  f16x8 v[4];
+  template <bool E5M2>
+  __device__ __forceinline__ void set(i32x8 x) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      i32x4 w;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int s = x[q * 2 + h / 2];
+        if constexpr (E5M2)  // e5m2 is the upper byte of an fp16
+          w[h] = int(__builtin_amdgcn_perm(0, uint32_t(s), h % 2 ? 0x030c020cu : 0x010c000cu));
+        else if (h % 2)
+          w[h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s, 1.0f, true));
+        else
+          w[h] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s, 1.0f, false));
+      }
+      v[q] = __builtin_bit_cast(f16x8, w);
+    }
+  }
+};
+
+// A block's sum of a 16 x 16 tile; A_E5M2 is the type of `a` (b: e4m3).
+template <bool A_E5M2>
+__device__ __forceinline__ f32x4 mfma_block(const Fragment<false> &b, const Fragment<false> &a) {
+  // formats: 0 = e4m3, 1 = e5m2; zero scale operands select the unscaled instruction
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, f32x4{0, 0, 0, 0}, 0, A_E5M2 ? 1 : 0, 0, 0, 0, 0);
+}
+template <bool A_E5M2>
+__device__ __forceinline__ f32x4 mfma_block(const Fragment<true> &b, const Fragment<true> &a) {
+  f32x4 c = {0, 0, 0, 0};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) c = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[q], a.v[q], c, 0, 0, 0);
+  return c;
+}
+
+// 4 bytes per lane from memory to LDS: lane i's word lands at dst + 4 i (as copy_to_lds16).
+__device__ __forceinline__ void copy_to_lds4(i32x4 rs, uint32_t voff, uint32_t soff, const lds_void *dst) {
+  const uint32_t m0 = uint32_t(reinterpret_cast<uintptr_t>(dst));
+  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds" ::"v"(voff), "s"(rs), "s"(soff),
+               "s"(m0)
+               : "memory", "m0");
+}
+
+template <int BM_, int BN_, int ST_, int NW_, int WM_>
+struct Fp8Geometry {
+  static constexpr int BM = BM_, BN = BN_, ST = ST_, NW = NW_, MF = 16, BK = 128;
+  static constexpr int THREADS = NW * 64, WM = WM_, WN = NW / WM;
+  static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 16, TN = WTN / 16;
+  static constexpr int CA = BK / 16;  // 16-byte chunks of a row
+  static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK;
+  static constexpr int S_LOADS = (BM + BN + 64 * NW - 1) / (64 * NW);  // 256-byte wave loads of scales
+  static constexpr int S_BYTES = S_LOADS * NW * 256;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + S_BYTES;
+  static constexpr int A_LOADS = A_BYTES / 1024 / NW, B_LOADS = B_BYTES / 1024 / NW;
+  static constexpr int LPW = A_LOADS + B_LOADS + S_LOADS;
+  static constexpr int LDS_BYTES = ST * STAGE_BYTES;
+  static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0,
+                "whole wave loads");
+  static_assert(WTM % 64 == 0 && WTN % 16 == 0 && 128 % WTN == 0, "a wave's columns lie in one block of 128");
+  static_assert(8 * NW % 16 == 0, "the swizzle is the same for every load of a lane");
+  static_assert(LDS_BYTES <= 163840 && (ST - 2) * LPW < 64, "LDS, vmcnt");
+  // chunk c of row r lives at c ^ swz(r): 16 consecutive rows read at one
+  // logical chunk land in 16 distinct 16-byte bank groups
+  static __device__ __forceinline__ int swz(int r) { return (r / 2) % CA; }
+};
+
+// The tile of a workgroup.
+struct Fp8Tile {
+  int group, row0, row_end, n0, split;
+  bool any;
+};
+
+template <int BM, int BN, bool GROUPED>
+__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
+  Fp8Tile t;
+  int id, n_ids, tm, tn;
+  if constexpr (GROUPED) {
+    // only the tiles there are take part in the XCD order; the launch's spare workgroups end here
+    n_ids = int(count_group_tiles<BM>(p.sizes, p.groups, p.M, lane)) * p.tiles_n;
+    if (int(blockIdx.x) >= n_ids) return {0, 0, 0, 0, 0, false};
+  } else {
+    n_ids = gridDim.x;
+  }
+  const int bid = blockIdx.x, xcd = bid & 7, local = bid >> 3, per = n_ids >> 3, extra = n_ids & 7;
+  id = xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
+  if constexpr (GROUPED) {
+    tm = id / p.tiles_n;
+    tn = id - tm * p.tiles_n;
+    const GroupTile g = find_group_tile<BM>(p.sizes, p.groups, p.M, tm, lane);
+    t = {g.group, g.row0, g.row_end, tn * BN, 0, true};
+  } else {
+    const int mn = p.tiles_m * p.tiles_n;
+    t.split = id / mn;
+    const int in = id - t.split * mn;
+    constexpr int GM = 4;  // tile rows that share an XCD's run of tiles (as in the fp16 kernel)
+    const int span = GM * p.tiles_n, first = in / span * GM, gm = min(p.tiles_m - first, GM), r = in % span;
+    t.group = 0;
+    t.row0 = (first + r % gm) * BM;
+    t.row_end = min(t.row0 + BM, p.M);
+    t.n0 = r / gm * BN;
+    t.any = true;
+  }
+  return t;
+}
+
+template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+__global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / G::WN, wc = wave % G::WN;
+  const Fp8Tile t = fp8_tile<G::BM, G::BN, GROUPED>(p, lane);
+  if (!t.any) return;
+  const int rows = t.row_end - t.row0, cols = min(G::BN, p.N - t.n0);
+  const int kbeg = t.split * p.k_split;
+  // rows of no group: no product, zeros are written
+  const int K = GROUPED && t.group == p.groups ? 0 : max(0, min(p.k_split, p.K - kbeg));
+  const int nk = (K + 127) / 128;
+  const int kb0 = kbeg / 128, kblocks = (p.K + 127) / 128;
+  const int group = GROUPED ? (K ? t.group : 0) : 0;
+
+  const i32x4 rsA = buffer_rsrc(p.A + int64_t(t.row0) * p.K + kbeg, K ? uint32_t(rows - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
+  const i32x4 rsB = buffer_rsrc(p.B + (int64_t(group) * p.N + t.n0) * p.K + kbeg,
+                                K ? uint32_t(cols - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
+  const i32x4 rsSA = buffer_rsrc(p.sa + int64_t(kb0) * p.M + t.row0, nk ? (uint32_t(nk - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u : 0u);
+  const i32x4 rsSB = buffer_rsrc(p.sb + (int64_t(group) * kblocks + kb0) * p.sb_cols, uint32_t(nk) * uint32_t(p.sb_cols) * 4u);
+
+  // Copy plan: wave load j of an operand covers LDS chunks (j*NW + wave)*64 +
+  // lane, so a lane's loads are 8*NW rows apart and at one place in their
+  // rows (the swizzle repeats every 16 rows).  Rows past the operand's last
+  // lie past its range, and read as zero; so does K past its end (kOOB).
+  const int cr = (wave * 64 + lane) / G::CA, cc = ((lane % G::CA) ^ G::swz(cr)) * 16;
+  const uint32_t off0 = uint32_t(cr) * uint32_t(p.K) + uint32_t(cc);
+  const uint32_t jstep = uint32_t(8 * G::NW) * uint32_t(p.K);
+  // scales: LDS words 0 .. BM-1 hold sa, ordered so that a lane's TM rows
+  // (16 apart) are neighbours; BM .. BM+BN-1 hold sb per column
+  // (words past them fill up the last wave's load)
+  uint32_t soff[G::S_LOADS];
+#pragma unroll
+  for (int j = 0; j < G::S_LOADS; ++j) {
+    const int w0 = (j * G::NW + wave) * 64;
+    if (w0 < G::BM) {
+      const int w = w0 + lane, in = w % G::WTM;
+      const int r = w - in + (in % G::TM) * 16 + in / G::TM;
+      soff[j] = r < rows ? uint32_t(r) * 4u : kOOB;
+    } else {
+      const int c = w0 - G::BM + lane;
+      soff[j] = c < cols ? uint32_t(B_ROWS ? t.n0 + c : (t.n0 + c) / 128) * 4u : kOOB;
+    }
+  }
+  // copy j of K tile kt (past the last one: zeros) into `slot`
+  auto issue = [&](int kt, int slot, int j) __attribute__((always_inline)) {
+    char *st = smem + slot * G::STAGE_BYTES;
+    if (j < G::A_LOADS + G::B_LOADS) {
+      const bool a = j < G::A_LOADS;
+      const int jj = a ? j : j - G::A_LOADS, k0 = kt * 128;
+      const lds_void *dst = (lds_void *)(st + (a ? 0 : G::A_BYTES) + (jj * G::NW + wave) * 1024);
+      copy_to_lds16(a ? rsA : rsB, (k0 + cc < K ? off0 : kOOB) + uint32_t(jj) * jstep, uint32_t(k0), dst);
+    } else {
+      const int js = j - G::A_LOADS - G::B_LOADS, w0 = (js * G::NW + wave) * 64;
+      const lds_void *dst = (lds_void *)(st + G::A_BYTES + G::B_BYTES + w0 * 4);
+      const bool sa = w0 < G::BM;
+      const uint32_t row = uint32_t(sa ? p.M : p.sb_cols) * 4u;
+      copy_to_lds4(sa ? rsSA : rsSB, kt < nk ? soff[js] : kOOB, kt < nk ? uint32_t(kt) * row : 0u, dst);
+    }
+  };
+
+  // fragments: lane's row lane % 16, chunks lane / 16 and 4 + lane / 16 (any
+  // order of K serves, being the same for both operands)
+  const int fr = lane % 16;
+  uint32_t f0 = uint32_t(fr * 128 + ((lane / 16) ^ G::swz(fr)) * 16);
+  uint32_t f1 = uint32_t(fr * 128 + ((4 + lane / 16) ^ G::swz(fr)) * 16);
+  auto frag = [&](const char *base) __attribute__((always_inline)) -> i32x8 {
+    const i32x4 lo = *(const __attribute__((address_space(3))) i32x4 *)(base + f0);
+    const i32x4 hi = *(const __attribute__((address_space(3))) i32x4 *)(base + f1);
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  f32x4 acc[G::TM][G::TN];
+#pragma unroll
+  for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < G::TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  asm volatile("s_nop 4" ::: "memory");  // descriptors written by v_readfirstlane, before the first copy
+#pragma unroll
+  for (int s = 0; s < G::ST - 1; ++s)
+#pragma unroll
+    for (int j = 0; j < G::LPW; ++j) issue(s, s, j);
+
+  int slot = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    // tile kt has landed and every wave is done with tile kt - 1, whose slot is refilled
+    wait_vmcnt_lgkm0<(G::ST - 2) * G::LPW>();
+    block_barrier();
+    const int free_slot = slot == 0 ? G::ST - 1 : slot - 1;
+    const char *st = smem + slot * G::STAGE_BYTES;
+    const char *sta = st + wr * G::WTM * 128, *stb = st + G::A_BYTES + wc * G::WTN * 128;
+    const float *ss = reinterpret_cast<const float *>(st + G::A_BYTES + G::B_BYTES);
+    float sav[G::TM], sbv[G::TN][4];
+#pragma unroll
+    for (int i = 0; i < G::TM; i += 4) {
+      const f32x4 v = *(const __attribute__((address_space(3))) f32x4 *)(ss + wr * G::WTM + fr * G::TM + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sav[i + e] = v[e];
+    }
+    if constexpr (B_ROWS) {
+#pragma unroll
+      for (int j = 0; j < G::TN; ++j) {
+        const f32x4 v = *(const __attribute__((address_space(3))) f32x4 *)(ss + G::BM + wc * G::WTN + j * 16 + lane / 16 * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sbv[j][e] = v[e];
+      }
+    } else {
+      const float v = *(const __attribute__((address_space(3))) float *)(ss + G::BM + wc * G::WTN);
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i) sav[i] *= v;
+    }
+    i32x8 fa[2];
+    Fragment<EXACT> fb[G::TN];
+    fa[0] = frag(sta);
+#pragma unroll
+    for (int j = 0; j < G::TN; ++j) fb[j].template set<false>(frag(stb + j * 16 * 128));
+    // Row i's block sums are scaled while row i + 1's MFMAs run.  The fences
+    // keep the compiler from reading fragments further ahead than one row,
+    // which would not fit the registers beside the accumulators.
+    f32x4 part[2][G::TN];
+#pragma unroll
+    for (int i = 0; i <= G::TM; ++i) {
+      if (i < G::TM) {
+        if (i + 1 < G::TM) fa[(i + 1) % 2] = frag(sta + (i + 1) * 16 * 128);
+        Fragment<EXACT> a;
+        a.template set<A_E5M2>(fa[i % 2]);
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j) part[i % 2][j] = mfma_block<A_E5M2>(fb[j], a);
+      }
+      if (i > 0) {
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float v = part[(i - 1) % 2][j][e];
+            acc[i - 1][j][e] = __builtin_fmaf(B_ROWS ? v * sbv[j][e] : v, sav[i - 1], acc[i - 1][j][e]);
+          }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (i < G::TM) {
+#pragma unroll
+        for (int c = i * G::LPW / G::TM; c < (i + 1) * G::LPW / G::TM; ++c) issue(kt + G::ST - 1, free_slot, c);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    slot = slot + 1 == G::ST ? 0 : slot + 1;
+  }
+  wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
+
+  const int64_t base = int64_t(t.split) * p.M * p.N;
+  if (p.out_dtype == TSS_F32)
+    store_tile<G, float>(acc, static_cast<float *>(p.C) + base, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+  else if (p.out_dtype == TSS_F16)
+    store_tile<G, _Float16>(acc, static_cast<_Float16 *>(p.C), smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+  else
+    store_tile<G, __bf16>(acc, static_cast<__bf16 *>(p.C), smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+}
+
+// Few rows: B's bytes are the cost, and each is used by one wave only, so it
+// goes from memory straight into MFMA fragments.  A workgroup takes 16 * MT
+// rows and 16 columns; its NW waves share K, block by block of 128, and their
+// sums are joined through LDS in the order of the waves.  A (a few rows, read
+// by every workgroup) comes from L2.
+constexpr int kRowsUnroll = 4;  // blocks of K whose loads a wave has in flight
+
+template <int MT, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+__global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const Fp8Tile t = fp8_tile<16 * MT, 16, GROUPED>(p, lane);
+  if (!t.any) return;
+  const int rows = t.row_end - t.row0, cols = min(16, p.N - t.n0);
+  const int K = GROUPED && t.group == p.groups ? 0 : p.K;
+  const int nk = (K + 127) / 128;
+  const int group = K ? t.group : 0;
+  auto rsrc = [](const void *base, uint32_t range) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
+  };
+  const auto rsA = rsrc(p.A + int64_t(t.row0) * p.K, K ? uint32_t(rows) * uint32_t(K) : 0u);
+  const auto rsB = rsrc(p.B + (int64_t(group) * p.N + t.n0) * p.K, K ? uint32_t(cols) * uint32_t(K) : 0u);
+  const auto rsSA = rsrc(p.sa + t.row0, nk ? (uint32_t(nk - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u : 0u);
+  const auto rsSB = rsrc(p.sb + int64_t(group) * nk * p.sb_cols, uint32_t(nk) * uint32_t(p.sb_cols) * 4u);
+  const int fr = lane % 16, ch = lane / 16 * 16;
+  const uint32_t b_off = fr < cols ? uint32_t(fr) * uint32_t(p.K) + uint32_t(ch) : kOOB;
+  uint32_t a_off[MT], sa_off[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int r = m * 16 + fr;
+    a_off[m] = r < rows ? uint32_t(r) * uint32_t(p.K) + uint32_t(ch) : kOOB;
+    sa_off[m] = r < rows ? uint32_t(r) * 4u : kOOB;
+  }
+  // a lane's 16 bytes at k (kOOB from K on); `ch` is its place within 64
+  auto load = [&](auto rs, uint32_t off, int k) __attribute__((always_inline)) -> i32x4 {
+    const uint32_t o = k + ch < K && off != kOOB ? off + uint32_t(k) : kOOB;
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+  };
+  auto loadf = [&](auto rs, uint32_t off) __attribute__((always_inline)) -> float {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
+  };
+  f32x4 acc[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0, 0, 0, 0};
+  for (int kb = wave; kb < nk; kb += nw * kRowsUnroll) {
+    i32x4 b[kRowsUnroll][2], a[kRowsUnroll][MT][2];
+    float sa[kRowsUnroll][MT], sb[kRowsUnroll][4];
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      const int kk = kb + u * nw, k = kk * 128;
+      const bool in = kk < nk;
+      b[u][0] = load(rsB, b_off, k);
+      b[u][1] = load(rsB, b_off, k + 64);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        a[u][m][0] = load(rsA, a_off[m], k);
+        a[u][m][1] = load(rsA, a_off[m], k + 64);
+        sa[u][m] = loadf(rsSA, in && sa_off[m] != kOOB ? sa_off[m] + uint32_t(kk) * uint32_t(p.M) * 4u : kOOB);
+      }
+      if constexpr (B_ROWS) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int c = lane / 16 * 4 + e;
+          sb[u][e] = loadf(rsSB, in && c < cols ? (uint32_t(kk) * uint32_t(p.sb_cols) + uint32_t(t.n0 + c)) * 4u : kOOB);
+        }
+      } else {
+        sb[u][0] = loadf(rsSB, in ? (uint32_t(kk) * uint32_t(p.sb_cols) + uint32_t(t.n0 / 128)) * 4u : kOOB);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kRowsUnroll; ++u)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        Fragment<EXACT> fa, fb;
+        fb.template set<false>(__builtin_shufflevector(b[u][0], b[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
+        fa.template set<A_E5M2>(__builtin_shufflevector(a[u][m][0], a[u][m][1], 0, 1, 2, 3, 4, 5, 6, 7));
+        const f32x4 part = mfma_block<A_E5M2>(fb, fa);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[m][e] = __builtin_fmaf(part[e] * sb[u][B_ROWS ? e : 0], sa[u][m], acc[m][e]);
+      }
+  }
+  // join: lane's 4 columns of row fr of row tile m, from each wave in turn
+  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) red[(wave * MT + m) * 64 + lane] = acc[m];
+  __syncthreads();
+  for (int m = wave; m < MT; m += nw) {
+    f32x4 s = red[m * 64 + lane];
+    for (int w = 1; w < nw; ++w) {
+      const f32x4 v = red[(w * MT + m) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    const int row = t.row0 + m * 16 + fr, col = t.n0 + lane / 16 * 4;
+    if (row < t.row_end && col < p.N) {
+      auto put = [&](auto o) __attribute__((always_inline)) {
+        using O = decltype(o);
+        typename Vec4<O>::type v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(s[e]);
+        *reinterpret_cast<typename Vec4<O>::type *>(static_cast<O *>(p.C) + int64_t(row) * p.N + col) = v;
+      };
+      if (p.out_dtype == TSS_F32) put(float{});
+      else if (p.out_dtype == TSS_F16) put(_Float16{});
+      else put(__bf16{});
+    }
+  }
+}
+
+}  // namespace tss
