@@ -635,14 +635,16 @@ int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, 
  * C = (A sa) (B sb)^T: A is M x K (a_dtype TSS_E4M3 or TSS_E5M2) with
  * sa[ceil(K / 128)][M]; B is N x K (TSS_E4M3) with sb[ceil(K / 128)][N]
  * (b_block_rows 1) or sb[ceil(K / 128)][ceil(N / 128)] (128); C is M x N,
- * out_dtype TSS_F16, TSS_BF16 or TSS_F32.  Within a block of 128 of K the
- * products are summed by the matrix cores in fp32, the blocks' sums are
- * scaled and added in fp32.
+ * out_dtype TSS_F16, TSS_BF16 or TSS_F32.  Each block of 128 of K is summed by
+ * the matrix cores, the blocks' sums are scaled and added in fp32.  For an
+ * fp32 output the blocks are summed in fp32 too; for a 16-bit one the 8-bit
+ * matrix instruction sums them, which is twice as fast and about 1.7e-5 of
+ * the result's norm off.
  * workspace: tss_gemm_fp8_workspace_size(M, N, K) bytes of device memory
  * (the partial sums of a product whose K is split over workgroups; may be
  * NULL when that is 0), 16-byte aligned, scratch.
- * K a multiple of 16 and below 2^22, N a multiple of 8; A, B, C 16-byte
- * aligned, sa and sb 4-byte; each operand below 2 GiB.  M == 0 or N == 0: nothing to do.  K == 0: C is
+ * K a multiple of 16 and below 2^22, any N; A, B, C 16-byte aligned, sa and
+ * sb 4-byte; each operand below 2 GiB.  M == 0 or N == 0: nothing to do.  K == 0: C is
  * zero-filled (A, B, sa and sb may then be NULL).
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
@@ -670,7 +672,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
  * tss_gemm_grouped_fp8: C[rows of e] = (A sa)[rows of e] (B[e] sb[e])^T, A
  * T x K (a_dtype TSS_E4M3 or TSS_E5M2) with sa[ceil(K / 128)][T], B E x N x K
  * (TSS_E4M3) with sb[e][ceil(K / 128)][ceil(N / 128)]; out_dtype TSS_F16,
- * TSS_BF16 or TSS_F32; K a multiple of 16 below 2^22.
+ * TSS_BF16 or TSS_F32 (sums as in tss_gemm_fp8); K a multiple of 16 below 2^22.
  *
  * K and N multiples of 8; every tensor 16-byte aligned (sizes, sa, sb
  * 4-byte); A, C and one group's B below 2 GiB each.  T == 0 or N == 0: C is

@@ -44,10 +44,10 @@ def product(A, B, sa, sb, b_rows):
 
 
 FP8_SIZES = [
-    (1, 8, 16), (1, 264, 8192), (3, 136, 144), (16, 16, 128), (17, 24, 112), (31, 1000, 1040),  # few rows
-    (33, 8, 16), (50, 264, 528), (64, 128, 2064), (100, 1000, 4112), (257, 136, 128),           # 64 x 128, K in ranges
-    (2100, 2104, 272), (2500, 2200, 128),                                                         # 128 x 128
-    (4100, 4104, 400), (4096, 4096, 128), (8000, 2048, 16),                                       # 256 x 256
+    (1, 1, 16), (3, 7, 2064), (29, 130, 144), (1, 264, 8192), (3, 136, 144), (16, 16, 128), (17, 24, 112), (31, 1000, 1040),  # few rows
+    (33, 3, 16), (77, 129, 2064), (300, 1003, 528), (50, 264, 528), (64, 128, 2064), (100, 1000, 4112), (257, 136, 128),           # 64 x 128, K in ranges
+    (2101, 2105, 272), (2100, 2106, 144), (2500, 2200, 128),                                                         # 128 x 128
+    (4100, 4104, 400), (4099, 4101, 144), (4096, 4098, 128), (4096, 4096, 128), (8000, 2048, 16),                                       # 256 x 256
 ]
 
 

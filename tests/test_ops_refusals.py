@@ -64,8 +64,8 @@ GEMM = dict(M=4, N=64, K=128, a_dtype=E4M3, A=P, B=P, sa=P, sb=P, b_rows=128, C=
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(M=-1), ARG), (dict(N=-8), ARG), (dict(K=-16), ARG), (dict(K=136), ALIGN), (dict(N=12), ALIGN),
-    (dict(a_dtype=BF16), DTYPE), (dict(out=E4M3), DTYPE), (dict(b_rows=64), ARG), (dict(A=None), ARG), (dict(B=None), ARG),
+    (dict(M=-1), ARG), (dict(N=-8), ARG), (dict(K=-16), ARG), (dict(K=136), ALIGN),
+    (dict(K=1 << 22), ARG), (dict(a_dtype=BF16), DTYPE), (dict(out=E4M3), DTYPE), (dict(b_rows=64), ARG), (dict(A=None), ARG), (dict(B=None), ARG),
     (dict(sa=None), ARG), (dict(sb=None), ARG), (dict(C=None), ARG), (dict(A=ODD), ALIGN), (dict(B=ODD), ALIGN),
     (dict(C=ODD), ALIGN), (dict(sa=P + 2), ALIGN), (dict(sb=P + 2), ALIGN), (dict(M=1 << 20, K=2048), ARG),
     (dict(N=1 << 20, K=2048), ARG), (dict(M=1 << 31), ARG)])

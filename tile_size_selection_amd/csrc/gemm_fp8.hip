@@ -103,9 +103,9 @@ int32_t check_types(int32_t a_dtype, int32_t out_dtype) {
   return TSS_OK;
 }
 
-int32_t check_sizes(int64_t M, int64_t N, int64_t K) {
+int32_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t n_multiple) {
   if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return TSS_E_ARG;
-  if (K % 16 || N % 8) return TSS_E_ALIGN;
+  if (K % 16 || N % n_multiple) return TSS_E_ALIGN;
   if (M * K >= kTwoGiB || N * K >= kTwoGiB || M * N * 2 >= kTwoGiB * 4) return TSS_E_ARG;
   // the kernels' byte offsets are 32 bits: 256 rows of K, and a row of scales for each 128 of K
   if (K >= int64_t(1) << 22) return TSS_E_ARG;
@@ -125,7 +125,7 @@ void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
 extern "C" {
 
 int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
-  const int32_t st = check_sizes(M, N, K);
+  const int32_t st = check_sizes(M, N, K, 1);
   if (st != TSS_OK) return st;
   if (M == 0 || N == 0 || K == 0) return 0;
   // the larger of what a 16-bit and an fp32 output take
@@ -141,7 +141,7 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
                      const float *sb, int32_t b_block_rows, void *C, int32_t out_dtype, void *workspace,
                      int64_t workspace_bytes, void *stream) {
   int32_t st = check_types(a_dtype, out_dtype);
-  if (st == TSS_OK) st = check_sizes(M, N, K);
+  if (st == TSS_OK) st = check_sizes(M, N, K, 1);
   if (st != TSS_OK) return st;
   if (b_block_rows != 1 && b_block_rows != 128) return TSS_E_ARG;
   if (M == 0 || N == 0) return TSS_OK;
@@ -186,7 +186,7 @@ int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t
                              const void *B, const float *sa, const float *sb, const int32_t *sizes, void *C,
                              int32_t out_dtype, void *stream) {
   int32_t st = check_types(a_dtype, out_dtype);
-  if (st == TSS_OK) st = check_sizes(T, N, K);
+  if (st == TSS_OK) st = check_sizes(T, N, K, 8);
   if (st != TSS_OK) return st;
   if (E < 1 || E > kMaxGroups) return TSS_E_ARG;
   if (T == 0 || N == 0) return TSS_OK;

@@ -163,6 +163,53 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
   return t;
 }
 
+// Rows of C that do not start on 16-byte borders (N not a multiple of 8):
+// staged through LDS as in store_tile, then written a row at a time in 4-byte
+// words; of a 16-bit type a word is two columns, the first of them chosen by
+// the row's parity so that the word is aligned, with single columns at the ends.
+template <typename G, typename O, typename Acc>
+__device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::TN], O *C, char *smem, int m0, int n0,
+                                                     int wave, int wr, int wc, int lane, int M, int N) {
+  using E = LdsEpilogue<G, O>;
+  static_assert(E::fits, "the staging area holds a row of MFMA tiles of every wave");
+  char *area = smem + wave * E::WAVE_BYTES;
+  constexpr int PER = 4 / int(sizeof(O)), WORDS = G::WTN / PER;
+  const int col0 = n0 + wc * G::WTN;
+  block_barrier();  // every wave is done with the last stage's fragments
+#pragma unroll
+  for (int i = 0; i < G::TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < G::TN; ++j) {
+      typename Vec4<O>::type v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(acc[i][j][e]);
+      *(__attribute__((address_space(3))) typename Vec4<O>::type *)(area + (lane % 16) * E::PITCH +
+                                                                    (j * 16 + lane / 16 * 4) * int(sizeof(O))) = v;
+    }
+#pragma unroll
+    for (int w0 = 0; w0 < 16 * WORDS; w0 += 64) {
+      const int r = (w0 + lane) / WORDS, w = (w0 + lane) % WORDS;
+      const int row = m0 + wr * G::WTM + i * 16 + r;
+      if (row >= M) continue;
+      const __attribute__((address_space(3))) O *from =
+          (const __attribute__((address_space(3))) O *)(area + r * E::PITCH);
+      O *to = C + int64_t(row) * N + col0;
+      if constexpr (PER == 1) {
+        if (col0 + w < N) to[w] = from[w];
+      } else {
+        const int odd = int((int64_t(row) * N) & 1), c = 2 * w + odd;
+        if (odd && w == 0 && col0 < N) to[0] = from[0];
+        if (c + 1 < G::WTN && col0 + c + 1 < N) {
+          typedef O O2 __attribute__((ext_vector_type(2)));
+          *reinterpret_cast<O2 *>(to + c) = O2{from[c], from[c + 1]};
+        } else if (c < G::WTN && col0 + c < N) {
+          to[c] = from[c];
+        }
+      }
+    }
+  }
+}
+
 template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
 __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -314,13 +361,21 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
 
-  const int64_t base = int64_t(t.split) * p.M * p.N;
-  if (p.out_dtype == TSS_F32)
-    store_tile<G, float>(acc, static_cast<float *>(p.C) + base, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
-  else if (p.out_dtype == TSS_F16)
-    store_tile<G, _Float16>(acc, static_cast<_Float16 *>(p.C), smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
-  else
-    store_tile<G, __bf16>(acc, static_cast<__bf16 *>(p.C), smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+  auto store = [&](auto o) __attribute__((always_inline)) {
+    using O = decltype(o);
+    O *C = static_cast<O *>(p.C) + int64_t(t.split) * p.M * p.N;
+    if (GROUPED || p.N % 8 == 0)
+      store_tile<G, O>(acc, C, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+    else
+      store_tile_unaligned<G, O>(acc, C, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
+  };
+  if constexpr (EXACT) {  // taken for fp32 outputs
+    store(float{});
+  } else {
+    if (p.out_dtype == TSS_F32) store(float{});  // partial sums of a split K
+    else if (p.out_dtype == TSS_F16) store(_Float16{});
+    else store(__bf16{});
+  }
 }
 
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it
@@ -425,9 +480,16 @@ __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
         typename Vec4<O>::type v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(s[e]);
-        *reinterpret_cast<typename Vec4<O>::type *>(static_cast<O *>(p.C) + int64_t(row) * p.N + col) = v;
+        O *to = static_cast<O *>(p.C) + int64_t(row) * p.N + col;
+        if (GROUPED || p.N % 4 == 0) {
+          *reinterpret_cast<typename Vec4<O>::type *>(to) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < p.N) to[e] = v[e];
+        }
       };
-      if (p.out_dtype == TSS_F32) put(float{});
+      if constexpr (EXACT) put(float{});
       else if (p.out_dtype == TSS_F16) put(_Float16{});
       else put(__bf16{});
     }

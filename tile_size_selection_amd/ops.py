@@ -173,8 +173,9 @@ def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
 def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, stream=None):
     """C = (A sa) @ (B sb)^T for 8-bit A (M, K), e4m3 or e5m2, and B (N, K),
     e4m3, with sa[ceil(K / 128)][M] and sb[ceil(K / 128)][N or ceil(N / 128)];
-    out_dtype 'bf16', 'f16' or 'f32'.  K a multiple of 16, N of 8.
-    workspace: a device tensor of at least gemm_fp8_workspace_size bytes
+    out_dtype 'bf16', 'f16' or 'f32' (fp32 sums throughout, at half the rate;
+    tss_gemm_fp8 in include/tss.h says how the sums of a 16-bit output
+    differ).  K a multiple of 16.  workspace: a device tensor of at least gemm_fp8_workspace_size bytes
     (allocated here when one is needed and not given)."""
     adt = _name(A, "A", ("e4m3", "e5m2"))
     _name(B, "B", ("e4m3",))
