@@ -112,10 +112,14 @@ GROUPS = [
     (700, [130, 0, 257, 300]), (1000, [256, 512, 200]), (1300, [700, 0, 513]), (2000, [2000]),
 ]
 WIDTHS = [(16, 8), (144, 264), (272, 136), (400, 520)]
+# wide enough for whole rounds of large tiles, and for a last round of whole tiles and of pieces
+LARGE = [((2100, [900, 0, 1100]), (144, 5000)), ((2100, [900, 0, 1100]), (144, 8200)), ((1200, [400, 650]), (272, 4104)),
+         ((3000, [5, 2990]), (2008 // 16 * 16, 1032))]
+CASES = [(g, w) for g in GROUPS for w in WIDTHS] + LARGE
+IDS = [f"{g[0]}rows_{len(g[1])}groups_{w[0]}x{w[1]}" for g, w in CASES]
 
 
-@pytest.mark.parametrize("width", WIDTHS)
-@pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{g[0]}rows_{len(g[1])}groups")
+@pytest.mark.parametrize("groups,width", CASES, ids=IDS)
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 def test_grouped_is_exact(groups, width, dtype):
     (T, sizes), (K, N), E = groups, width, len(groups[1])
@@ -151,8 +155,7 @@ def test_grouped_is_exact(groups, width, dtype):
     assert none is None
 
 
-@pytest.mark.parametrize("width", WIDTHS)
-@pytest.mark.parametrize("groups", GROUPS, ids=lambda g: f"{g[0]}rows_{len(g[1])}groups")
+@pytest.mark.parametrize("groups,width", CASES, ids=IDS)
 @pytest.mark.parametrize("a", ["e4m3", "e5m2"])
 def test_grouped_fp8_is_exact(groups, width, a):
     (T, sizes), (K, N), E = groups, width, len(groups[1])

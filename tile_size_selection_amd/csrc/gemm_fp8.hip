@@ -12,9 +12,12 @@ constexpr int64_t kTwoGiB = int64_t(1) << 31;
 
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-using Tile256 = Fp8Geometry<256, 256, 2, 8, 2>;
-using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;
-using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;
+using Tile256 = Fp8Geometry<256, 256, 2, 8, 2>;   // with its pieces: large products
+using Piece256 = Fp8Geometry<128, 256, 3, 8, 2>;
+using Piece128 = Fp8Geometry<128, 128, 3, 8, 2>;  // also groups of middling size
+using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;   // fp32 outputs; two workgroups a CU
+using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;     // two workgroups a CU
+constexpr int kRoundsLds = Tile256::LDS_BYTES > Piece256::LDS_BYTES ? Tile256::LDS_BYTES : Piece256::LDS_BYTES;
 
 // How a product is run: by tiles of bm x bn (K in `splits` ranges), or
 // (bn == 16) by the kernel for few rows.
@@ -22,14 +25,12 @@ struct Plan {
   int bm, bn, splits;
 };
 
-constexpr int kCUs = 256;
-
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
-  if (M <= 16) return {16, 16, 1};
-  if (M <= 32) return {32, 16, 1};
+  const int64_t a_reads = (N + 15) / 16 * M * K;  // of the kernel for few rows, from L2
+  if (M <= 16 || (M <= 64 && a_reads <= int64_t(24) << 20)) return {16, 16, 1};
   auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  if (!exact && blocks(256, 256) >= kCUs) return {256, 256, 1};
-  if (blocks(128, 128) >= kCUs) return {128, 128, 1};
+  if (!exact && blocks(128, 128) >= 200) return {256, 256, 1};
+  if (exact && blocks(128, 128) >= kCUs) return {128, 128, 1};
   const int64_t b = blocks(64, 128), kb = (K + 127) / 128;
   int64_t s = b >= kCUs ? 1 : kCUs / b;
   if (s > kb / 4) s = kb / 4;  // at least four steps of K a range
@@ -39,18 +40,15 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
 
 Plan plan_grouped(int64_t T, int64_t E, bool exact) {
   const int64_t rows = T / E;  // of an average group
-  if (rows <= 16) return {16, 16, 1};
-  if (rows <= 32) return {32, 16, 1};
   if (rows <= 64) return {64, 128, 1};
-  if (rows <= 256 || exact) return {128, 128, 1};
+  if (rows <= 192 || exact) return {128, 128, 1};
   return {256, 256, 1};
 }
 
-template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
-hipError_t launch_tile(const Fp8Args &a, int64_t blocks, hipStream_t s) {
-  // dynamic LDS above 64 KiB needs an attribute per kernel and device, set on the first launch there
-  static std::atomic<uint64_t> attr_set{0};
-  auto kernel = gemm_fp8_tile_kernel<G, A_E5M2, B_ROWS, GROUPED, EXACT>;
+// Dynamic LDS above 64 KiB needs an attribute per kernel and device: set on the first launch there.
+template <typename Kernel>
+hipError_t launch_lds(Kernel kernel, std::atomic<uint64_t> &attr_set, const Fp8Args &a, int64_t blocks, int threads,
+                      int lds, hipStream_t s) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
@@ -60,17 +58,34 @@ hipError_t launch_tile(const Fp8Args &a, int64_t blocks, hipStream_t s) {
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_acq_rel);
   }
-  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(G::THREADS), G::LDS_BYTES, s, a);
+  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(threads), lds, s, a);
   return hipGetLastError();
 }
 
-template <int MT, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+hipError_t launch_tile(const Fp8Args &a, int64_t blocks, hipStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};
+  return launch_lds(gemm_fp8_tile_kernel<G, A_E5M2, B_ROWS, GROUPED, EXACT>, attr_set, a, blocks, G::THREADS,
+                    G::LDS_BYTES, s);
+}
+
+// tiles: the most there can be (grouped), or all there are.
+template <bool A_E5M2, bool B_ROWS, bool GROUPED>
+hipError_t launch_rounds(const Fp8Args &a, int64_t tiles, hipStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};
+  const int64_t whole = tiles / kCUs * kCUs, rest = tiles - whole;
+  const int64_t blocks = GROUPED ? whole + kCUs : whole + rest * fp8_pieces(int(rest));
+  return launch_lds(gemm_fp8_rounds_kernel<Tile256, Piece256, Piece128, A_E5M2, B_ROWS, GROUPED>, attr_set, a, blocks,
+                    Tile256::THREADS, kRoundsLds, s);
+}
+
+template <bool A_E5M2, bool B_ROWS, bool EXACT>
 hipError_t launch_rows(const Fp8Args &a, int64_t blocks, hipStream_t s) {
   const int nk = (a.K + 127) / 128;
   int nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
-  nw = nw < 1 ? 1 : nw > 16 ? 16 : nw;
-  hipLaunchKernelGGL((gemm_fp8_rows_kernel<MT, A_E5M2, B_ROWS, GROUPED, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64),
-                     nw * MT * 1024, s, a);
+  nw = nw > 16 ? 16 : nw;
+  hipLaunchKernelGGL((gemm_fp8_rows_kernel<A_E5M2, B_ROWS, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64), nw * 1024, s,
+                     a);
   return hipGetLastError();
 }
 
@@ -86,12 +101,14 @@ hipError_t launch(Fp8Args &a, const Plan &pl, bool exact, hipStream_t s, int32_t
   }
   auto go = [&](auto exact) {
     constexpr bool X = decltype(exact)::value;
-    if (pl.bn == 16)
-      return pl.bm == 16 ? launch_rows<1, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s)
-                         : launch_rows<2, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+    if constexpr (!GROUPED)
+      if (pl.bn == 16) return launch_rows<A_E5M2, B_ROWS, X>(a, blocks, s);
     if constexpr (!X)
-      if (pl.bm == 256) return launch_tile<Tile256, A_E5M2, B_ROWS, GROUPED, false>(a, blocks, s);
-    if (pl.bm == 128) return launch_tile<Tile128, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+      if (pl.bm == 256) return launch_rounds<A_E5M2, B_ROWS, GROUPED>(a, blocks, s);
+    if (pl.bm == 128) {
+      if constexpr (X) return launch_tile<Tile128, A_E5M2, B_ROWS, GROUPED, true>(a, blocks, s);
+      else return launch_tile<Piece128, A_E5M2, B_ROWS, GROUPED, false>(a, blocks, s);
+    }
     return launch_tile<Tile64, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
   };
   return exact ? go(std::true_type{}) : go(std::false_type{});

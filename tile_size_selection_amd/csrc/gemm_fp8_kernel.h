@@ -116,7 +116,7 @@ struct Fp8Geometry {
   static constexpr int LDS_BYTES = ST * STAGE_BYTES;
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0 && BM % 64 == 0 && BN % 64 == 0,
                 "whole wave loads");
-  static_assert(WTM % 64 == 0 && WTN % 16 == 0 && 128 % WTN == 0, "a wave's columns lie in one block of 128");
+  static_assert(TM % 4 == 0 && TM >= 4 && WTN % 16 == 0 && 128 % WTN == 0, "a wave's columns lie in one block of 128");
   static_assert(8 * NW % 16 == 0, "the swizzle is the same for every load of a lane");
   static_assert(LDS_BYTES <= 163840 && (ST - 2) * LPW < 64, "LDS, vmcnt");
   // chunk c of row r lives at c ^ swz(r): 16 consecutive rows read at one
@@ -130,37 +130,32 @@ struct Fp8Tile {
   bool any;
 };
 
+// Tile `id` of the product, bm x bn.
 template <int BM, int BN, bool GROUPED>
-__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
-  Fp8Tile t;
-  int id, n_ids, tm, tn;
+__device__ __forceinline__ Fp8Tile fp8_tile_at(const Fp8Args &p, int id, int lane) {
   if constexpr (GROUPED) {
-    // only the tiles there are take part in the XCD order; the launch's spare workgroups end here
-    n_ids = int(count_group_tiles<BM>(p.sizes, p.groups, p.M, lane)) * p.tiles_n;
-    if (int(blockIdx.x) >= n_ids) return {0, 0, 0, 0, 0, false};
-  } else {
-    n_ids = gridDim.x;
-  }
-  const int bid = blockIdx.x, xcd = bid & 7, local = bid >> 3, per = n_ids >> 3, extra = n_ids & 7;
-  id = xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
-  if constexpr (GROUPED) {
-    tm = id / p.tiles_n;
-    tn = id - tm * p.tiles_n;
+    const int tm = id / p.tiles_n, tn = id - tm * p.tiles_n;
     const GroupTile g = find_group_tile<BM>(p.sizes, p.groups, p.M, tm, lane);
-    t = {g.group, g.row0, g.row_end, tn * BN, 0, true};
+    return {g.group, g.row0, g.row_end, tn * BN, 0, true};
   } else {
-    const int mn = p.tiles_m * p.tiles_n;
-    t.split = id / mn;
-    const int in = id - t.split * mn;
+    const int mn = p.tiles_m * p.tiles_n, split = id / mn, in = id - split * mn;
     constexpr int GM = 4;  // tile rows that share an XCD's run of tiles (as in the fp16 kernel)
     const int span = GM * p.tiles_n, first = in / span * GM, gm = min(p.tiles_m - first, GM), r = in % span;
-    t.group = 0;
-    t.row0 = (first + r % gm) * BM;
-    t.row_end = min(t.row0 + BM, p.M);
-    t.n0 = r / gm * BN;
-    t.any = true;
+    const int row0 = (first + r % gm) * BM;
+    return {0, row0, min(row0 + BM, p.M), r / gm * BN, split, true};
   }
-  return t;
+}
+
+// Every workgroup one tile; in XCD order only the tiles that there are take
+// part (grouped: the launch's spare workgroups end here).
+template <int BM, int BN, bool GROUPED>
+__device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
+  int n = gridDim.x;
+  if constexpr (GROUPED) {
+    n = int(count_group_tiles<BM>(p.sizes, p.groups, p.M, lane)) * p.tiles_n;
+    if (int(blockIdx.x) >= n) return {0, 0, 0, 0, 0, false};
+  }
+  return fp8_tile_at<BM, BN, GROUPED>(p, xcd_run(blockIdx.x, n), lane);
 }
 
 // Rows of C that do not start on 16-byte borders (N not a multiple of 8):
@@ -210,14 +205,26 @@ __device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::
   }
 }
 
+// One tile's product.  A step of K (128) of a wave's TM x TN MFMA tiles runs
+// in two halves, so that neither the step's first fragments nor its barrier
+// leave the matrix cores idle:
+//   1. rows 0 .. TM/2-1, one after the other; as a row ends, its A fragment is
+//      replaced by that of the row TM/2 below;
+//   -- the next step's tile has landed, and this one's slot is read --
+//   2. rows TM/2 .., column by column; as a column ends, its B fragment is
+//      replaced by the next step's, and after the last column the A fragments
+//      are; the slot is refilled meanwhile.
+// The sums of one group of MFMAs are scaled while the next group's run.
+// Measured at 8192^3 (e4m3, 128 x 128 scales of B, bf16 out) on one box: all of
+// a step's fragments read and copies spread over it behind the barrier 482 us,
+// copies in its first half 449-459, this 439 (2.50 PFLOP/s).  Of 459 us,
+// leaving out the copies took 62, the scaling 47, the fragment reads 118; the
+// MFMAs alone took 271.
 template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
-__global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
+__device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile &t, char *smem) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / G::WN, wc = wave % G::WN;
-  const Fp8Tile t = fp8_tile<G::BM, G::BN, GROUPED>(p, lane);
-  if (!t.any) return;
   const int rows = t.row_end - t.row0, cols = min(G::BN, p.N - t.n0);
   const int kbeg = t.split * p.k_split;
   // rows of no group: no product, zeros are written
@@ -290,30 +297,21 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
     for (int j = 0; j < G::TN; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
   asm volatile("s_nop 4" ::: "memory");  // descriptors written by v_readfirstlane, before the first copy
-#pragma unroll
-  for (int s = 0; s < G::ST - 1; ++s)
-#pragma unroll
-    for (int j = 0; j < G::LPW; ++j) issue(s, s, j);
 
-  int slot = 0;
-  for (int kt = 0; kt < nk; ++kt) {
-    // tile kt has landed and every wave is done with tile kt - 1, whose slot is refilled
-    wait_vmcnt_lgkm0<(G::ST - 2) * G::LPW>();
-    block_barrier();
-    const int free_slot = slot == 0 ? G::ST - 1 : slot - 1;
-    const char *st = smem + slot * G::STAGE_BYTES;
-    const char *sta = st + wr * G::WTM * 128, *stb = st + G::A_BYTES + wc * G::WTN * 128;
+  constexpr int TM = G::TM, TN = G::TN, R = TM / 2, ST = G::ST;
+  float sav[TM], sbv[TN][4];
+  Fragment<EXACT> fa[R], fb[TN];
+  auto read_scales = [&](const char *st) __attribute__((always_inline)) {
     const float *ss = reinterpret_cast<const float *>(st + G::A_BYTES + G::B_BYTES);
-    float sav[G::TM], sbv[G::TN][4];
 #pragma unroll
-    for (int i = 0; i < G::TM; i += 4) {
-      const f32x4 v = *(const __attribute__((address_space(3))) f32x4 *)(ss + wr * G::WTM + fr * G::TM + i);
+    for (int i = 0; i < TM; i += 4) {
+      const f32x4 v = *(const __attribute__((address_space(3))) f32x4 *)(ss + wr * G::WTM + fr * TM + i);
 #pragma unroll
       for (int e = 0; e < 4; ++e) sav[i + e] = v[e];
     }
     if constexpr (B_ROWS) {
 #pragma unroll
-      for (int j = 0; j < G::TN; ++j) {
+      for (int j = 0; j < TN; ++j) {
         const f32x4 v = *(const __attribute__((address_space(3))) f32x4 *)(ss + G::BM + wc * G::WTN + j * 16 + lane / 16 * 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) sbv[j][e] = v[e];
@@ -321,43 +319,77 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
     } else {
       const float v = *(const __attribute__((address_space(3))) float *)(ss + G::BM + wc * G::WTN);
 #pragma unroll
-      for (int i = 0; i < G::TM; ++i) sav[i] *= v;
+      for (int i = 0; i < TM; ++i) sav[i] *= v;
     }
-    i32x8 fa[2];
-    Fragment<EXACT> fb[G::TN];
-    fa[0] = frag(sta);
+  };
+  constexpr int NP = TN > R ? TN : R;
+  f32x4 part[2][NP];
+  auto scale_tile = [&](f32x4 v, int i, int j) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < G::TN; ++j) fb[j].template set<false>(frag(stb + j * 16 * 128));
-    // Row i's block sums are scaled while row i + 1's MFMAs run.  The fences
-    // keep the compiler from reading fragments further ahead than one row,
-    // which would not fit the registers beside the accumulators.
-    f32x4 part[2][G::TN];
+    for (int e = 0; e < 4; ++e)
+      acc[i][j][e] = __builtin_fmaf(B_ROWS ? v[e] * sbv[j][e] : v[e], sav[i], acc[i][j][e]);
+  };
 #pragma unroll
-    for (int i = 0; i <= G::TM; ++i) {
-      if (i < G::TM) {
-        if (i + 1 < G::TM) fa[(i + 1) % 2] = frag(sta + (i + 1) * 16 * 128);
-        Fragment<EXACT> a;
-        a.template set<A_E5M2>(fa[i % 2]);
+  for (int s = 0; s < ST; ++s)
 #pragma unroll
-        for (int j = 0; j < G::TN; ++j) part[i % 2][j] = mfma_block<A_E5M2>(fb[j], a);
-      }
+    for (int j = 0; j < G::LPW; ++j) issue(s, s, j);
+  wait_vmcnt_lgkm0<(ST - 1) * G::LPW>();
+  block_barrier();
+  int slot = 0;
+  {
+    const char *sta = smem + wr * G::WTM * 128, *stb = smem + G::A_BYTES + wc * G::WTN * 128;
+#pragma unroll
+    for (int i = 0; i < R; ++i) fa[i].template set<A_E5M2>(frag(sta + i * 16 * 128));
+#pragma unroll
+    for (int j = 0; j < TN; ++j) fb[j].template set<false>(frag(stb + j * 16 * 128));
+    read_scales(smem);
+  }
+  for (int kt = 0; kt < nk; ++kt) {
+    const int next = slot + 1 == ST ? 0 : slot + 1;
+    const char *sta = smem + slot * G::STAGE_BYTES + wr * G::WTM * 128;
+    const char *stn = smem + next * G::STAGE_BYTES;
+    const char *stna = stn + wr * G::WTM * 128, *stnb = stn + G::A_BYTES + wc * G::WTN * 128;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < TN; ++j) part[i % 2][j] = mfma_block<A_E5M2>(fb[j], fa[i]);
+      fa[i].template set<A_E5M2>(frag(sta + (R + i) * 16 * 128));
       if (i > 0) {
 #pragma unroll
-        for (int j = 0; j < G::TN; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float v = part[(i - 1) % 2][j][e];
-            acc[i - 1][j][e] = __builtin_fmaf(B_ROWS ? v * sbv[j][e] : v, sav[i - 1], acc[i - 1][j][e]);
-          }
+        for (int j = 0; j < TN; ++j) scale_tile(part[(i - 1) % 2][j], i - 1, j);
       }
       __builtin_amdgcn_sched_barrier(0);
-      if (i < G::TM) {
-#pragma unroll
-        for (int c = i * G::LPW / G::TM; c < (i + 1) * G::LPW / G::TM; ++c) issue(kt + G::ST - 1, free_slot, c);
-        __builtin_amdgcn_sched_barrier(0);
-      }
     }
-    slot = slot + 1 == G::ST ? 0 : slot + 1;
+    // tile kt + 1 has landed, and tile kt's slot is read
+    wait_vmcnt_lgkm0<(ST - 2) * G::LPW>();
+    block_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      const int g = R + j;  // the group's number in the step
+#pragma unroll
+      for (int i = 0; i < R; ++i) part[g % 2][i] = mfma_block<A_E5M2>(fb[j], fa[i]);
+      fb[j].template set<false>(frag(stnb + j * 16 * 128));
+      if (j == TN - 1) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) fa[i].template set<A_E5M2>(frag(stna + i * 16 * 128));
+      }
+      if (j == 0) {
+#pragma unroll
+        for (int jj = 0; jj < TN; ++jj) scale_tile(part[(R - 1) % 2][jj], R - 1, jj);
+      } else {
+#pragma unroll
+        for (int i = 0; i < R; ++i) scale_tile(part[(g - 1) % 2][i], R + i, j - 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int c = j * G::LPW / TN; c < (j + 1) * G::LPW / TN; ++c) issue(kt + ST, slot, c);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) scale_tile(part[(R + TN - 1) % 2][i], R + i, TN - 1);
+    read_scales(stn);
+    slot = next;
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
 
@@ -378,41 +410,73 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
   }
 }
 
+template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+__global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const Fp8Tile t = fp8_tile<G::BM, G::BN, GROUPED>(p, threadIdx.x & 63);
+  if (t.any) fp8_tile_product<G, A_E5M2, B_ROWS, GROUPED, EXACT>(p, t, smem);
+}
+
+// Large products: one workgroup fills a CU, so the tiles run in rounds of
+// kCUs, and a last round with few of them would leave most CUs idle.  Its
+// tiles are cut into pieces, two of 128 x 256 or four of 128 x 128, where that
+// many fit one round; an element's sums are the same in any of them.
+constexpr int kCUs = 256;
+
+__host__ __device__ constexpr int fp8_pieces(int rest) { return rest * 4 <= kCUs ? 4 : rest * 2 <= kCUs ? 2 : 1; }
+
+template <typename G, typename Half, typename Quarter, bool A_E5M2, bool B_ROWS, bool GROUPED>
+__global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  static_assert(G::THREADS == Half::THREADS && G::THREADS == Quarter::THREADS && Half::BM * 2 == G::BM &&
+                    Quarter::BM * 2 == G::BM && Half::BN == G::BN && Quarter::BN * 2 == G::BN, "pieces of a tile");
+  const int lane = threadIdx.x & 63, bid = blockIdx.x;
+  const int n = (GROUPED ? int(count_group_tiles<G::BM>(p.sizes, p.groups, p.M, lane)) : p.tiles_m) * p.tiles_n;
+  const int whole = n / kCUs * kCUs, rest = n - whole, pieces = fp8_pieces(rest);
+  if (bid < whole || pieces == 1) {
+    if (bid >= n) return;
+    const int id = bid < whole ? xcd_run(bid, whole) : whole + xcd_run(bid - whole, rest);
+    fp8_tile_product<G, A_E5M2, B_ROWS, GROUPED, false>(p, fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane), smem);
+    return;
+  }
+  if (bid >= whole + rest * pieces) return;
+  const int piece = xcd_run(bid - whole, rest * pieces), id = whole + piece / pieces, part = piece % pieces;
+  Fp8Tile t = fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane);
+  t.row0 += (pieces == 2 ? part : part / 2) * Half::BM;
+  t.row_end = min(t.row_end, t.row0 + Half::BM);
+  if (pieces == 4) t.n0 += part % 2 * Quarter::BN;
+  if (t.row0 >= t.row_end || t.n0 >= p.N) return;
+  if (pieces == 2) fp8_tile_product<Half, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
+  else fp8_tile_product<Quarter, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
+}
+
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it
-// goes from memory straight into MFMA fragments.  A workgroup takes 16 * MT
-// rows and 16 columns; its NW waves share K, block by block of 128, and their
-// sums are joined through LDS in the order of the waves.  A (a few rows, read
-// by every workgroup) comes from L2.
+// goes from memory straight into MFMA fragments.  A workgroup takes 16 rows
+// and 16 columns; its waves share K, block by block of 128, and their sums
+// are joined through LDS in the order of the waves: one launch, where the
+// tiles above need a second for a split K.  A (read by every workgroup) comes
+// from L2.
 constexpr int kRowsUnroll = 4;  // blocks of K whose loads a wave has in flight
 
-template <int MT, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+template <bool A_E5M2, bool B_ROWS, bool EXACT>
 __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Fp8Tile t = fp8_tile<16 * MT, 16, GROUPED>(p, lane);
-  if (!t.any) return;
+  const Fp8Tile t = fp8_tile<16, 16, false>(p, lane);
   const int rows = t.row_end - t.row0, cols = min(16, p.N - t.n0);
-  const int K = GROUPED && t.group == p.groups ? 0 : p.K;
-  const int nk = (K + 127) / 128;
-  const int group = K ? t.group : 0;
+  const int K = p.K, nk = (K + 127) / 128;
   auto rsrc = [](const void *base, uint32_t range) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
   };
-  const auto rsA = rsrc(p.A + int64_t(t.row0) * p.K, K ? uint32_t(rows) * uint32_t(K) : 0u);
-  const auto rsB = rsrc(p.B + (int64_t(group) * p.N + t.n0) * p.K, K ? uint32_t(cols) * uint32_t(K) : 0u);
-  const auto rsSA = rsrc(p.sa + t.row0, nk ? (uint32_t(nk - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u : 0u);
-  const auto rsSB = rsrc(p.sb + int64_t(group) * nk * p.sb_cols, uint32_t(nk) * uint32_t(p.sb_cols) * 4u);
+  const auto rsA = rsrc(p.A + int64_t(t.row0) * K, uint32_t(rows) * uint32_t(K));
+  const auto rsB = rsrc(p.B + int64_t(t.n0) * K, uint32_t(cols) * uint32_t(K));
+  const auto rsSA = rsrc(p.sa + t.row0, (uint32_t(nk - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u);
+  const auto rsSB = rsrc(p.sb, uint32_t(nk) * uint32_t(p.sb_cols) * 4u);
   const int fr = lane % 16, ch = lane / 16 * 16;
-  const uint32_t b_off = fr < cols ? uint32_t(fr) * uint32_t(p.K) + uint32_t(ch) : kOOB;
-  uint32_t a_off[MT], sa_off[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = m * 16 + fr;
-    a_off[m] = r < rows ? uint32_t(r) * uint32_t(p.K) + uint32_t(ch) : kOOB;
-    sa_off[m] = r < rows ? uint32_t(r) * 4u : kOOB;
-  }
-  // a lane's 16 bytes at k (kOOB from K on); `ch` is its place within 64
+  const uint32_t a_off = fr < rows ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
+  const uint32_t b_off = fr < cols ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
+  // a lane's 16 bytes at k (zeros from K on); `ch` is its place within 64
   auto load = [&](auto rs, uint32_t off, int k) __attribute__((always_inline)) -> i32x4 {
     const uint32_t o = k + ch < K && off != kOOB ? off + uint32_t(k) : kOOB;
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
@@ -420,24 +484,19 @@ __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
   auto loadf = [&](auto rs, uint32_t off) __attribute__((always_inline)) -> float {
     return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, off, 0, 0));
   };
-  f32x4 acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) acc[m] = f32x4{0, 0, 0, 0};
+  f32x4 acc = {0, 0, 0, 0};
   for (int kb = wave; kb < nk; kb += nw * kRowsUnroll) {
-    i32x4 b[kRowsUnroll][2], a[kRowsUnroll][MT][2];
-    float sa[kRowsUnroll][MT], sb[kRowsUnroll][4];
+    i32x4 b[kRowsUnroll][2], a[kRowsUnroll][2];
+    float sa[kRowsUnroll], sb[kRowsUnroll][4];
 #pragma unroll
     for (int u = 0; u < kRowsUnroll; ++u) {
       const int kk = kb + u * nw, k = kk * 128;
       const bool in = kk < nk;
-      b[u][0] = load(rsB, b_off, k);
-      b[u][1] = load(rsB, b_off, k + 64);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        a[u][m][0] = load(rsA, a_off[m], k);
-        a[u][m][1] = load(rsA, a_off[m], k + 64);
-        sa[u][m] = loadf(rsSA, in && sa_off[m] != kOOB ? sa_off[m] + uint32_t(kk) * uint32_t(p.M) * 4u : kOOB);
-      }
+      for (int h = 0; h < 2; ++h) b[u][h] = load(rsB, b_off, k + 64 * h);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a[u][h] = load(rsA, a_off, k + 64 * h);
+      sa[u] = loadf(rsSA, in && fr < rows ? (uint32_t(kk) * uint32_t(p.M) + uint32_t(fr)) * 4u : kOOB);
       if constexpr (B_ROWS) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -449,51 +508,44 @@ __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u)
+    for (int u = 0; u < kRowsUnroll; ++u) {
+      Fragment<EXACT> fa, fb;
+      fb.template set<false>(__builtin_shufflevector(b[u][0], b[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
+      fa.template set<A_E5M2>(__builtin_shufflevector(a[u][0], a[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
+      const f32x4 part = mfma_block<A_E5M2>(fb, fa);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        Fragment<EXACT> fa, fb;
-        fb.template set<false>(__builtin_shufflevector(b[u][0], b[u][1], 0, 1, 2, 3, 4, 5, 6, 7));
-        fa.template set<A_E5M2>(__builtin_shufflevector(a[u][m][0], a[u][m][1], 0, 1, 2, 3, 4, 5, 6, 7));
-        const f32x4 part = mfma_block<A_E5M2>(fb, fa);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          acc[m][e] = __builtin_fmaf(part[e] * sb[u][B_ROWS ? e : 0], sa[u][m], acc[m][e]);
-      }
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(part[e] * sb[u][B_ROWS ? e : 0], sa[u], acc[e]);
+    }
   }
-  // join: lane's 4 columns of row fr of row tile m, from each wave in turn
   f32x4 *red = reinterpret_cast<f32x4 *>(smem);
-#pragma unroll
-  for (int m = 0; m < MT; ++m) red[(wave * MT + m) * 64 + lane] = acc[m];
+  red[wave * 64 + lane] = acc;
   __syncthreads();
-  for (int m = wave; m < MT; m += nw) {
-    f32x4 s = red[m * 64 + lane];
-    for (int w = 1; w < nw; ++w) {
-      const f32x4 v = red[(w * MT + m) * 64 + lane];
+  if (wave != 0) return;
+  f32x4 s = red[lane];
+  for (int w = 1; w < nw; ++w) {
+    const f32x4 v = red[w * 64 + lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[e] += v[e];
-    }
-    const int row = t.row0 + m * 16 + fr, col = t.n0 + lane / 16 * 4;
-    if (row < t.row_end && col < p.N) {
-      auto put = [&](auto o) __attribute__((always_inline)) {
-        using O = decltype(o);
-        typename Vec4<O>::type v;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(s[e]);
-        O *to = static_cast<O *>(p.C) + int64_t(row) * p.N + col;
-        if (GROUPED || p.N % 4 == 0) {
-          *reinterpret_cast<typename Vec4<O>::type *>(to) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < p.N) to[e] = v[e];
-        }
-      };
-      if constexpr (EXACT) put(float{});
-      else if (p.out_dtype == TSS_F16) put(_Float16{});
-      else put(__bf16{});
-    }
+    for (int e = 0; e < 4; ++e) s[e] += v[e];
   }
+  const int row = t.row0 + fr, col = t.n0 + lane / 16 * 4;
+  if (row >= t.row_end || col >= p.N) return;
+  auto put = [&](auto o) __attribute__((always_inline)) {
+    using O = decltype(o);
+    typename Vec4<O>::type v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(s[e]);
+    O *to = static_cast<O *>(p.C) + int64_t(row) * p.N + col;
+    if (p.N % 4 == 0) {
+      *reinterpret_cast<typename Vec4<O>::type *>(to) = v;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < p.N) to[e] = v[e];
+    }
+  };
+  if constexpr (EXACT) put(float{});
+  else if (p.out_dtype == TSS_F16) put(_Float16{});
+  else put(__bf16{});
 }
 
 }  // namespace tss

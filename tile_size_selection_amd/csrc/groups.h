@@ -13,6 +13,14 @@ namespace tss {
 
 constexpr int kMaxGroups = 4096;
 
+// Workgroups are dealt to the 8 XCDs round-robin: this gives each XCD a
+// contiguous run of 0 .. n-1, so that lines shared by neighbours are shared
+// in one L2.
+__device__ __forceinline__ int xcd_run(int bid, int n) {
+  const int xcd = bid & 7, local = bid >> 3, per = n >> 3, extra = n & 7;
+  return xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
+}
+
 // Tiles of BM rows that T rows in E groups (and a rest) can need: each group
 // and the rest end at most one tile short, and no tile is empty.
 inline int64_t max_group_tiles(int64_t T, int64_t E, int64_t BM) {

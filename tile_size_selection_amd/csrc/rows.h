@@ -156,12 +156,4 @@ __device__ __forceinline__ u32x2 pack8(const float (&v)[8], const BlockScale<Q> 
   return r;
 }
 
-// Workgroups are dealt to the 8 XCDs round-robin: this gives each XCD a
-// contiguous run of 0 .. n-1, so that lines shared by neighbours are shared
-// in one L2.
-__device__ __forceinline__ int xcd_run(int bid, int n) {
-  const int xcd = bid & 7, local = bid >> 3, per = n >> 3, extra = n & 7;
-  return xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
-}
-
 }  // namespace tss
