@@ -27,19 +27,21 @@ struct Plan {
 
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
   const int64_t a_reads = (N + 15) / 16 * M * K;  // of the kernel for few rows, from L2
-  if (M <= 16 || (M <= 64 && a_reads <= int64_t(24) << 20)) return {16, 16, 1};
+  if (M <= 16 || (M <= 64 && a_reads <= int64_t(40) << 20)) return {16, 16, 1};
   auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  if (!exact && blocks(128, 128) >= 200) return {256, 256, 1};
+  if (!exact && blocks(128, 128) >= 160) return {256, 256, 1};
   if (exact && blocks(128, 128) >= kCUs) return {128, 128, 1};
   const int64_t b = blocks(64, 128), kb = (K + 127) / 128;
   int64_t s = b >= kCUs ? 1 : kCUs / b;
-  if (s > kb / 4) s = kb / 4;  // at least four steps of K a range
-  if (s < 1) s = 1;
+  if (s > kb / 8) s = kb / 8;  // at least eight steps of K a range
+  s = s > 8 ? 8 : s < 1 ? 1 : s;
   return {64, 128, int(s)};
 }
 
-Plan plan_grouped(int64_t T, int64_t E, bool exact) {
+Plan plan_grouped(int64_t T, int64_t N, int64_t K, int64_t E, bool exact) {
   const int64_t rows = T / E;  // of an average group
+  const int64_t tiles64 = (T / 64 + E < T ? T / 64 + E : T) * ((N + 127) / 128), a_reads = (N + 15) / 16 * T * K;
+  if (K > 0 && tiles64 < kCUs && a_reads <= int64_t(40) << 20) return {16, 16, 1};
   if (rows <= 64) return {64, 128, 1};
   if (rows <= 192 || exact) return {128, 128, 1};
   return {256, 256, 1};
@@ -79,12 +81,12 @@ hipError_t launch_rounds(const Fp8Args &a, int64_t tiles, hipStream_t s) {
                     Tile256::THREADS, kRoundsLds, s);
 }
 
-template <bool A_E5M2, bool B_ROWS, bool EXACT>
+template <bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
 hipError_t launch_rows(const Fp8Args &a, int64_t blocks, hipStream_t s) {
   const int nk = (a.K + 127) / 128;
   int nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
   nw = nw > 16 ? 16 : nw;
-  hipLaunchKernelGGL((gemm_fp8_rows_kernel<A_E5M2, B_ROWS, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64), nw * 1024, s,
+  hipLaunchKernelGGL((gemm_fp8_rows_kernel<A_E5M2, B_ROWS, GROUPED, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64), nw * 1024, s,
                      a);
   return hipGetLastError();
 }
@@ -101,8 +103,7 @@ hipError_t launch(Fp8Args &a, const Plan &pl, bool exact, hipStream_t s, int32_t
   }
   auto go = [&](auto exact) {
     constexpr bool X = decltype(exact)::value;
-    if constexpr (!GROUPED)
-      if (pl.bn == 16) return launch_rows<A_E5M2, B_ROWS, X>(a, blocks, s);
+    if (pl.bn == 16) return launch_rows<A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
     if constexpr (!X)
       if (pl.bm == 256) return launch_rounds<A_E5M2, B_ROWS, GROUPED>(a, blocks, s);
     if (pl.bm == 128) {
@@ -228,7 +229,7 @@ int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t
   a.out_dtype = out_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool exact = out_dtype == TSS_F32;
-  const Plan pl = plan_grouped(T, E, exact);
+  const Plan pl = plan_grouped(T, N, K, E, exact);
   const hipError_t err = a_dtype == TSS_E5M2 ? launch<true, false, true>(a, pl, exact, s, &st)
                                              : launch<false, false, true>(a, pl, exact, s, &st);
   if (st != TSS_OK) return st;

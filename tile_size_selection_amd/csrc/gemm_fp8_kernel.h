@@ -344,52 +344,66 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
     for (int j = 0; j < TN; ++j) fb[j].template set<false>(frag(stb + j * 16 * 128));
     read_scales(smem);
   }
-  for (int kt = 0; kt < nk; ++kt) {
-    const int next = slot + 1 == ST ? 0 : slot + 1;
-    const char *sta = smem + slot * G::STAGE_BYTES + wr * G::WTM * 128;
-    const char *stn = smem + next * G::STAGE_BYTES;
-    const char *stna = stn + wr * G::WTM * 128, *stnb = stn + G::A_BYTES + wc * G::WTN * 128;
+  // A wave whose rows are all past the tile's end (the last tile of a group,
+  // say) only copies: its SIMD's other wave then has the matrix core alone.
+  // (A loop of its own: with the test inside the loop below the registers
+  // spill.)
+  if (wr * G::WTM >= rows) {
+    for (int kt = 0; kt < nk; ++kt) {
+      wait_vmcnt_lgkm0<(ST - 2) * G::LPW>();
+      block_barrier();
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) part[i % 2][j] = mfma_block<A_E5M2>(fb[j], fa[i]);
-      fa[i].template set<A_E5M2>(frag(sta + (R + i) * 16 * 128));
-      if (i > 0) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j) scale_tile(part[(i - 1) % 2][j], i - 1, j);
-      }
-      __builtin_amdgcn_sched_barrier(0);
+      for (int c = 0; c < G::LPW; ++c) issue(kt + ST, slot, c);
+      slot = slot + 1 == ST ? 0 : slot + 1;
     }
-    // tile kt + 1 has landed, and tile kt's slot is read
-    wait_vmcnt_lgkm0<(ST - 2) * G::LPW>();
-    block_barrier();
-    __builtin_amdgcn_sched_barrier(0);
+  } else {
+    for (int kt = 0; kt < nk; ++kt) {
+      const int next = slot + 1 == ST ? 0 : slot + 1;
+      const char *sta = smem + slot * G::STAGE_BYTES + wr * G::WTM * 128;
+      const char *stn = smem + next * G::STAGE_BYTES;
+      const char *stna = stn + wr * G::WTM * 128, *stnb = stn + G::A_BYTES + wc * G::WTN * 128;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int g = R + j;  // the group's number in the step
+      for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) part[g % 2][i] = mfma_block<A_E5M2>(fb[j], fa[i]);
-      fb[j].template set<false>(frag(stnb + j * 16 * 128));
-      if (j == TN - 1) {
+        for (int j = 0; j < TN; ++j) part[i % 2][j] = mfma_block<A_E5M2>(fb[j], fa[i]);
+        fa[i].template set<A_E5M2>(frag(sta + (R + i) * 16 * 128));
+        if (i > 0) {
 #pragma unroll
-        for (int i = 0; i < R; ++i) fa[i].template set<A_E5M2>(frag(stna + i * 16 * 128));
+          for (int j = 0; j < TN; ++j) scale_tile(part[(i - 1) % 2][j], i - 1, j);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (j == 0) {
-#pragma unroll
-        for (int jj = 0; jj < TN; ++jj) scale_tile(part[(R - 1) % 2][jj], R - 1, jj);
-      } else {
-#pragma unroll
-        for (int i = 0; i < R; ++i) scale_tile(part[(g - 1) % 2][i], R + i, j - 1);
-      }
+      // tile kt + 1 has landed, and tile kt's slot is read
+      wait_vmcnt_lgkm0<(ST - 2) * G::LPW>();
+      block_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int c = j * G::LPW / TN; c < (j + 1) * G::LPW / TN; ++c) issue(kt + ST, slot, c);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < TN; ++j) {
+        const int g = R + j;  // the group's number in the step
+#pragma unroll
+        for (int i = 0; i < R; ++i) part[g % 2][i] = mfma_block<A_E5M2>(fb[j], fa[i]);
+        fb[j].template set<false>(frag(stnb + j * 16 * 128));
+        if (j == TN - 1) {
+#pragma unroll
+          for (int i = 0; i < R; ++i) fa[i].template set<A_E5M2>(frag(stna + i * 16 * 128));
+        }
+        if (j == 0) {
+#pragma unroll
+          for (int jj = 0; jj < TN; ++jj) scale_tile(part[(R - 1) % 2][jj], R - 1, jj);
+        } else {
+#pragma unroll
+          for (int i = 0; i < R; ++i) scale_tile(part[(g - 1) % 2][i], R + i, j - 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int c = j * G::LPW / TN; c < (j + 1) * G::LPW / TN; ++c) issue(kt + ST, slot, c);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+      for (int i = 0; i < R; ++i) scale_tile(part[(R + TN - 1) % 2][i], R + i, TN - 1);
+      read_scales(stn);
+      slot = next;
     }
-#pragma unroll
-    for (int i = 0; i < R; ++i) scale_tile(part[(R + TN - 1) % 2][i], R + i, TN - 1);
-    read_scales(stn);
-    slot = next;
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
 
@@ -458,21 +472,23 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) 
 // from L2.
 constexpr int kRowsUnroll = 4;  // blocks of K whose loads a wave has in flight
 
-template <bool A_E5M2, bool B_ROWS, bool EXACT>
+template <bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
 __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const Fp8Tile t = fp8_tile<16, 16, false>(p, lane);
+  const Fp8Tile t = fp8_tile<16, 16, GROUPED>(p, lane);
+  if (!t.any) return;
   const int rows = t.row_end - t.row0, cols = min(16, p.N - t.n0);
-  const int K = p.K, nk = (K + 127) / 128;
+  const bool none = GROUPED && t.group == p.groups;  // rows of no group: zeros
+  const int K = p.K, kblocks = (K + 127) / 128, nk = none ? 0 : kblocks, group = none ? 0 : t.group;
   auto rsrc = [](const void *base, uint32_t range) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
   };
   const auto rsA = rsrc(p.A + int64_t(t.row0) * K, uint32_t(rows) * uint32_t(K));
-  const auto rsB = rsrc(p.B + int64_t(t.n0) * K, uint32_t(cols) * uint32_t(K));
-  const auto rsSA = rsrc(p.sa + t.row0, (uint32_t(nk - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u);
-  const auto rsSB = rsrc(p.sb, uint32_t(nk) * uint32_t(p.sb_cols) * 4u);
+  const auto rsB = rsrc(p.B + (int64_t(group) * p.N + t.n0) * K, uint32_t(cols) * uint32_t(K));
+  const auto rsSA = rsrc(p.sa + t.row0, (uint32_t(kblocks - 1) * uint32_t(p.M) + uint32_t(rows)) * 4u);
+  const auto rsSB = rsrc(p.sb + int64_t(group) * kblocks * p.sb_cols, uint32_t(kblocks) * uint32_t(p.sb_cols) * 4u);
   const int fr = lane % 16, ch = lane / 16 * 16;
   const uint32_t a_off = fr < rows ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
   const uint32_t b_off = fr < cols ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
