@@ -431,14 +431,8 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
   if (t.any) fp8_tile_product<G, A_E5M2, B_ROWS, GROUPED, EXACT>(p, t, smem);
 }
 
-// Large products: one workgroup fills a CU, so the tiles run in rounds of
-// kCUs, and a last round with few of them would leave most CUs idle.  Its
-// tiles are cut into pieces, two of 128 x 256 or four of 128 x 128, where that
-// many fit one round; an element's sums are the same in any of them.
-constexpr int kCUs = 256;
-
-__host__ __device__ constexpr int fp8_pieces(int rest) { return rest * 4 <= kCUs ? 4 : rest * 2 <= kCUs ? 2 : 1; }
-
+// Large products: one workgroup fills a CU, and the last round's tiles are cut
+// into pieces as in grouped_gemm_kernel.
 template <typename G, typename Half, typename Quarter, bool A_E5M2, bool B_ROWS, bool GROUPED>
 __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
@@ -446,7 +440,7 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) 
                     Quarter::BM * 2 == G::BM && Half::BN == G::BN && Quarter::BN * 2 == G::BN, "pieces of a tile");
   const int lane = threadIdx.x & 63, bid = blockIdx.x;
   const int n = (GROUPED ? int(count_group_tiles<G::BM>(p.sizes, p.groups, p.M, lane)) : p.tiles_m) * p.tiles_n;
-  const int whole = n / kCUs * kCUs, rest = n - whole, pieces = fp8_pieces(rest);
+  const int whole = n / kCUs * kCUs, rest = n - whole, pieces = tile_pieces(rest, GROUPED);
   if (bid < whole || pieces == 1) {
     if (bid >= n) return;
     const int id = bid < whole ? xcd_run(bid, whole) : whole + xcd_run(bid - whole, rest);

@@ -13,23 +13,32 @@ constexpr int64_t kTwoGiB = int64_t(1) << 31;
 bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
 using Tile256 = Geometry<256, 256, 64, 2, 8, 16>;
+using Piece256 = Geometry<128, 256, 64, 3, 8, 16>;
+using Piece128 = Geometry<128, 128, 64, 4, 8, 16>;
 using Tile128 = Geometry<128, 128, 64, 2, 4, 16>;
 using Tile64 = Geometry<64, 64, 64, 4, 4, 16>;
 
-template <typename G, typename T, int GRP>
-hipError_t launch(KernelArgs &a, int64_t z, hipStream_t s, int32_t *status) {
+constexpr int most(int a, int b) { return a > b ? a : b; }
+
+template <typename G, typename Half, typename Quarter, typename T, int GRP>
+hipError_t launch(KernelArgs &a, hipStream_t s, int32_t *status) {
+  constexpr bool ragged = GRP != kGroupGradB, pieces = !__is_same(G, Half);
   a.tiles_n = int32_t((int64_t(a.N) + G::BN - 1) / G::BN);
-  const int64_t tiles_m = GRP == kGroupGradB ? (int64_t(a.M) + G::BM - 1) / G::BM : max_group_tiles(a.M, a.groups, G::BM);
+  const int64_t tiles_m = ragged ? max_group_tiles(a.M, a.groups, G::BM) : (int64_t(a.M) + G::BM - 1) / G::BM;
   a.tiles_m = int32_t(tiles_m);
   a.group_m = a.tiles_m < 4 ? a.tiles_m : 4;
-  const int64_t blocks = z * tiles_m * a.tiles_n;
+  const int64_t tiles = tiles_m * a.tiles_n * (ragged ? 1 : a.groups);
+  // (ragged: the most there can be)
+  const int64_t whole = pieces ? tiles / kCUs * kCUs : tiles, rest = tiles - whole;
+  const int64_t blocks = !pieces ? tiles : whole + (ragged ? kCUs * 4 / 3 : rest * tile_pieces(int(rest), false));
   if (blocks * G::THREADS > int64_t(UINT32_MAX)) {  // the launch's thread count is 32 bits
     *status = TSS_E_ARG;
     return hipSuccess;
   }
   // dynamic LDS above 64 KiB needs an attribute per kernel and device, set on the first launch there
   static std::atomic<uint64_t> attr_set{0};
-  auto kernel = tiled_gemm_kernel<G, T, false, GRP>;
+  auto kernel = grouped_gemm_kernel<G, Half, Quarter, T, GRP>;
+  constexpr int lds = most(G::lds_bytes(false), most(Half::lds_bytes(false), Quarter::lds_bytes(false)));
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
@@ -39,23 +48,27 @@ hipError_t launch(KernelArgs &a, int64_t z, hipStream_t s, int32_t *status) {
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_acq_rel);
   }
-  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(G::THREADS), G::lds_bytes(false), s, a);
+  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(G::THREADS), lds, s, a);
   return hipGetLastError();
 }
 
+// Few rows in an average group: the groups' weights are the cost, and small
+// tiles put more of their loads in flight.  Forward, E = 32, K = N = 2048,
+// 64 x 64 against 256 x 256 tiles: 16 rows a group 57 and 61 us, 64 rows 73
+// and 63, 256 rows 181 and 99.
 template <typename T, int GRP>
 hipError_t launch_rows(KernelArgs &a, hipStream_t s, int32_t *status) {
-  const int64_t rows = a.M / a.groups;  // of an average group
-  if (rows <= 64) return launch<Tile64, T, GRP>(a, 1, s, status);
-  if (rows <= 256) return launch<Tile128, T, GRP>(a, 1, s, status);
-  return launch<Tile256, T, GRP>(a, 1, s, status);
+  if (a.M / a.groups <= 32) return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
+  return launch<Tile256, Piece256, Piece128, T, GRP>(a, s, status);
 }
 
+// With few rows to reduce over the writes are the cost.  E = 32, K = 4096,
+// N = 2048, 2 rows a group: 128 x 128 tiles 165 us, 256 x 256 178; K = N =
+// 2048, 64 rows a group 99 and 100, 256 rows 143 and 136.
 template <typename T>
 hipError_t launch_grad_b(KernelArgs &a, hipStream_t s, int32_t *status) {
-  const int64_t t256 = ((int64_t(a.M) + 255) / 256) * ((int64_t(a.N) + 255) / 256) * a.groups;
-  if (t256 >= 512) return launch<Tile256, T, kGroupGradB>(a, a.groups, s, status);
-  return launch<Tile128, T, kGroupGradB>(a, a.groups, s, status);
+  if (a.rows_total / a.groups <= 64) return launch<Tile128, Tile128, Tile128, T, kGroupGradB>(a, s, status);
+  return launch<Tile256, Piece256, Piece128, T, kGroupGradB>(a, s, status);
 }
 
 int32_t check(int64_t T, int64_t E, int64_t K, int64_t N, int32_t dtype, int32_t out_dtype) {

@@ -450,12 +450,15 @@ __device__ __forceinline__ void store_conv(const Acc (&acc)[G::TM][G::TN], O *y,
 
 // ---- the kernel ----------------------------------------------------------------
 
+// The product of one tile: rows m0 .. M - 1 (at most BM) and columns from n0
+// of batch entry, conv tile or group bz, over K elements from kbeg (K == 0 for
+// a range past the end, and for rows of no group: zeros).
 template <typename G, typename T, bool CONV, int GRP = kUngrouped>
-__global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
+__device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, int m0, int n0, int M, int K, int bz,
+                                             int split, int kbeg) {
   static_assert(!CONV || GRP == kUngrouped, "grouped convolutions are not built here");
   constexpr bool AT = GRP == kGroupGradB;           // A operand K-outer, read with the transpose read
   constexpr bool BK_ROWS = CONV || GRP == kGroupGradA;  // B operand K-contiguous, copied and read like A
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
   using Acc = typename AccType<G::MF>::type;
   constexpr int MF = G::MF;
   constexpr int S = G::ST;
@@ -463,54 +466,6 @@ __global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / G::WN, wc = wave % G::WN;
-
-  // -- block -> tile.  Workgroups are dealt to the 8 XCDs round-robin; remap
-  // so that each XCD gets a contiguous run of tiles, ordered in groups of
-  // group_m tile rows so that the run shares A and B panels in its L2.
-  int nblk = gridDim.x;
-  const int bid = blockIdx.x;
-  if constexpr (GRP == kGroupForward || GRP == kGroupGradA) {
-    // only the tiles there are take part; the launch's spare workgroups end here
-    nblk = int(count_group_tiles<G::BM>(p.sizes, p.groups, p.M, lane)) * p.tiles_n;
-    if (bid >= nblk) return;
-  }
-  const int xcd = bid & 7, local = bid >> 3;
-  const int per = nblk >> 3, extra = nblk & 7;
-  const int t = xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
-  const int tiles_mn = p.tiles_m * p.tiles_n;
-  int m0, n0, M = p.M, K, bz, split = 0, kbeg = 0;
-  if constexpr (GRP == kGroupForward || GRP == kGroupGradA) {
-    // one tile row after the other: the column tiles of a group's rows are
-    // neighbours in an XCD's run; rows of no group have no product
-    const int tm = t / p.tiles_n;
-    const GroupTile g = find_group_tile<G::BM>(p.sizes, p.groups, p.M, tm, lane);
-    m0 = g.row0;
-    n0 = (t - tm * p.tiles_n) * G::BN;
-    M = g.row_end;
-    K = g.group == p.groups ? 0 : p.K;
-    bz = g.group == p.groups ? 0 : g.group;
-  } else {
-    const int bzs = t / tiles_mn;  // (batch entry, conv tile or group) * splits + K range
-    const int tt = t - bzs * tiles_mn;
-    split = bzs % p.splits;
-    bz = bzs / p.splits;
-    const int span = p.group_m * p.tiles_n;
-    const int first_m = (tt / span) * p.group_m;
-    const int gm = min(p.tiles_m - first_m, p.group_m);
-    const int in_g = tt - (tt / span) * span;
-    const int tm = first_m + in_g % gm, tn = in_g / gm;
-    m0 = tm * G::BM;
-    n0 = tn * G::BN;
-    if constexpr (GRP == kGroupGradB) {
-      const GroupTile g = group_rows(p.sizes, p.groups, p.rows_total, bz, lane);
-      kbeg = g.row0;
-      K = g.row_end - g.row0;
-    } else {
-      // this block's K range [kbeg, kbeg + K) (K == 0 for a range past the end)
-      kbeg = split * p.k_split;
-      K = max(0, min(p.k_split, p.K - kbeg));
-    }
-  }
   const int lda = p.lda;
 
   // -- convolution: this block's tile (images, output rows, output
@@ -973,6 +928,101 @@ __global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
     else
       store_conv<G, __bf16>(acc, reinterpret_cast<__bf16 *>(p.C), p, m0, n0, wr, wc, lane, nb0, o0, rows_t, q0, cols_t,
                                 N);
+  }
+}
+
+template <typename G, typename T, bool CONV>
+__global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  // -- block -> tile.  Workgroups are dealt to the 8 XCDs round-robin; remap
+  // so that each XCD gets a contiguous run of tiles, ordered in groups of
+  // group_m tile rows so that the run shares A and B panels in its L2.
+  const int t = xcd_run(blockIdx.x, gridDim.x);
+  const int tiles_mn = p.tiles_m * p.tiles_n;
+  const int bzs = t / tiles_mn;  // (batch entry or conv tile) * splits + K range
+  const int tt = t - bzs * tiles_mn;
+  const int split = bzs % p.splits, bz = bzs / p.splits;
+  const int span = p.group_m * p.tiles_n;
+  const int first_m = (tt / span) * p.group_m;
+  const int gm = min(p.tiles_m - first_m, p.group_m);
+  const int in_g = tt - (tt / span) * span;
+  const int tm = first_m + in_g % gm, tn = in_g / gm;
+  // this block's K range [kbeg, kbeg + K) (K == 0 for a range past the end)
+  const int kbeg = split * p.k_split;
+  const int K = max(0, min(p.k_split, p.K - kbeg));
+  tile_product<G, T, CONV>(p, smem, tm * G::BM, tn * G::BN, p.M, K, bz, split, kbeg);
+}
+
+// Grouped products.  The tiles are those of G, 512 threads and one workgroup
+// a CU; where the last round of kCUs tiles has few of them they are cut into
+// pieces, two of 128 x 256 or four of 128 x 128 (an element's sums are the
+// same in any of them).  Half == G: small tiles, all alike.
+constexpr int kCUs = 256;
+
+// Of ragged rows a group's last tile is often less than half full and its
+// empty pieces end at once, so a third more than a round may be launched.
+__host__ __device__ constexpr int tile_pieces(int rest, bool ragged) {
+  const int most = ragged ? kCUs * 4 / 3 : kCUs;
+  return rest * 4 <= most ? 4 : rest * 2 <= most ? 2 : 1;
+}
+
+template <typename G, typename Half, typename Quarter, typename T, int GRP>
+__global__ __launch_bounds__(G::THREADS) void grouped_gemm_kernel(KernelArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  constexpr bool PIECES = !__is_same(G, Half);
+  constexpr bool RAGGED = GRP != kGroupGradB;
+  static_assert(G::THREADS == Half::THREADS && G::THREADS == Quarter::THREADS, "one launch");
+  static_assert(!PIECES || (Half::BM * 2 == G::BM && Quarter::BM * 2 == G::BM && Half::BN == G::BN &&
+                            Quarter::BN * 2 == G::BN), "pieces of a tile");
+  const int lane = threadIdx.x & 63, bid = blockIdx.x;
+  // only the tiles there are take part; the launch's spare workgroups end here
+  const int n = (RAGGED ? int(count_group_tiles<G::BM>(p.sizes, p.groups, p.M, lane)) : p.groups * p.tiles_m) * p.tiles_n;
+  const int whole = PIECES ? n / kCUs * kCUs : n, rest = n - whole;
+  const int pieces = PIECES ? tile_pieces(rest, RAGGED) : 1;
+  if (bid >= whole + rest * pieces) return;
+  // RAGGED: the XCDs get runs of equal length.  GradB's tiles cost as much as
+  // their group has rows, so there each group is dealt over the XCDs (given
+  // whole groups, the XCD of the largest one held up the others: 365 -> 244 us
+  // on 16384 rows in 8 uneven groups, K 4096, N 2048).
+  int id = bid, part = 0;
+  if (bid >= whole) {
+    const int x = RAGGED ? xcd_run(bid - whole, rest * pieces) : bid - whole;
+    id = whole + x / pieces;
+    part = x % pieces;
+  } else if constexpr (RAGGED) {
+    id = xcd_run(bid, whole);
+  }
+  int m0, n0, M = p.M, K, bz, kbeg = 0;
+  if constexpr (RAGGED) {
+    // one tile row after the other: the column tiles of a group's rows are
+    // neighbours in an XCD's run
+    const int tm = id / p.tiles_n;
+    const GroupTile g = find_group_tile<G::BM>(p.sizes, p.groups, p.M, tm, lane);
+    m0 = g.row0;
+    n0 = (id - tm * p.tiles_n) * G::BN;
+    M = g.row_end;
+    const bool none = g.group == p.groups;  // rows of no group
+    K = none ? 0 : p.K;
+    bz = none ? 0 : g.group;
+  } else {
+    const int mn = p.tiles_m * p.tiles_n;
+    bz = id / mn;
+    const int in = xcd_run(id - bz * mn, mn), span = p.group_m * p.tiles_n, first = in / span * p.group_m;
+    const int gm = min(p.tiles_m - first, p.group_m), r = in % span;
+    m0 = (first + r % gm) * G::BM;
+    n0 = r / gm * G::BN;
+    const GroupTile g = group_rows(p.sizes, p.groups, p.rows_total, bz, lane);
+    kbeg = g.row0;
+    K = g.row_end - g.row0;
+  }
+  if (!PIECES || bid < whole || pieces == 1) {
+    tile_product<G, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
+  } else if constexpr (PIECES) {
+    m0 += (pieces == 2 ? part : part / 2) * Half::BM;
+    if (pieces == 4) n0 += part % 2 * Quarter::BN;
+    if (m0 >= M || n0 >= p.N) return;
+    if (pieces == 2) tile_product<Half, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
+    else tile_product<Quarter, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
   }
 }
 
