@@ -74,13 +74,13 @@ def test_gemm_fp8_refuses(change, status):
 
 
 def test_gemm_fp8_wants_its_workspace():
-    need = tss.gemm_fp8_workspace_size(100, 128, 8192)
-    assert need > 0 and need % (100 * 128 * 4) == 0
-    big = dict(GEMM, M=100, N=128, K=8192)
+    need = tss.gemm_fp8_workspace_size(512, 512, 8192)
+    assert need > 0 and need % (512 * 512 * 4) == 0
+    big = dict(GEMM, M=512, N=512, K=8192)
     assert C.lib().tss_gemm_fp8(*big.values()) == ARG
     assert C.lib().tss_gemm_fp8(*_with(big, ws=P, ws_bytes=need - 1)) == ARG
     assert C.lib().tss_gemm_fp8(*_with(big, ws=ODD, ws_bytes=need)) == ALIGN
-    assert tss.gemm_fp8_workspace_size(0, 128, 8192) == 0
+    assert tss.gemm_fp8_workspace_size(0, 512, 8192) == 0
     with pytest.raises(tss.TssError):
         tss.gemm_fp8_workspace_size(100, 128, 8190)
 

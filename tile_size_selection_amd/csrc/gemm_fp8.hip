@@ -26,12 +26,17 @@ struct Plan {
 };
 
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
-  const int64_t a_reads = (N + 15) / 16 * M * K;  // of the kernel for few rows, from L2
-  if (M <= 16 || (M <= 64 && a_reads <= int64_t(40) << 20)) return {16, 16, 1};
+  const int64_t kb = (K + 127) / 128;
+  // The kernel for few rows takes about 3.6 us and, every 16 x 16 tile reading
+  // its own rows of both operands from L2, MNK / 8 bytes at 8 TB/s; tiles take
+  // about 5 us and 0.37 a step, or about 10 with K split.  76 x 480 x 3200:
+  // 6.2 against 10.4 us; 64 x 2048 x 2048: 7.2 and 10; 64 x 8192 x 4096: 33 and 13.
+  const int64_t steps100 = 160 + 37 * kb;
+  if (M <= 16 || M * N * K <= 640000 * (steps100 < 700 ? steps100 : 700)) return {16, 16, 1};
   auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
   if (!exact && blocks(128, 128) >= 160) return {256, 256, 1};
   if (exact && blocks(128, 128) >= kCUs) return {128, 128, 1};
-  const int64_t b = blocks(64, 128), kb = (K + 127) / 128;
+  const int64_t b = blocks(64, 128);
   int64_t s = b >= kCUs ? 1 : kCUs / b;
   if (s > kb / 8) s = kb / 8;  // at least eight steps of K a range
   s = s > 8 ? 8 : s < 1 ? 1 : s;

@@ -159,48 +159,53 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
 }
 
 // Rows of C that do not start on 16-byte borders (N not a multiple of 8):
-// staged through LDS as in store_tile, then written a row at a time in 4-byte
-// words; of a 16-bit type a word is two columns, the first of them chosen by
-// the row's parity so that the word is aligned, with single columns at the ends.
+// staged through LDS as in store_tile, but each row at its place within 16
+// bytes of memory, so that whole 16-byte pieces of memory are written from
+// aligned pieces of LDS; the elements of the pieces at a row's ends are
+// written one by one (their other elements are another wave's).  Measured at
+// 8192 x 8191 x 512, bf16: 4-byte words 118 us, see gemm_fp8.hip for this.
 template <typename G, typename O, typename Acc>
 __device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::TN], O *C, char *smem, int m0, int n0,
                                                      int wave, int wr, int wc, int lane, int M, int N) {
   using E = LdsEpilogue<G, O>;
   static_assert(E::fits, "the staging area holds a row of MFMA tiles of every wave");
+  typedef __attribute__((address_space(3))) O lds_o;
+  constexpr int SIZE = int(sizeof(O)), PER = 16 / SIZE, CPR = G::WTN / PER;
   char *area = smem + wave * E::WAVE_BYTES;
-  constexpr int PER = 4 / int(sizeof(O)), WORDS = G::WTN / PER;
-  const int col0 = n0 + wc * G::WTN;
+  const int col0 = n0 + wc * G::WTN, row0 = m0 + wr * G::WTM;
+  const int cols = min(G::WTN, N - col0);
+  // bytes that the wave's part of a row starts past a 16-byte border
+  auto shift = [&](int row) __attribute__((always_inline)) {
+    return int(((uint32_t(row) * uint32_t(N) + uint32_t(col0)) * uint32_t(SIZE)) & 15u);
+  };
   block_barrier();  // every wave is done with the last stage's fragments
+  if (cols <= 0) return;
 #pragma unroll
   for (int i = 0; i < G::TM; ++i) {
+    {
+      const int r = lane % 16;
+      char *to = area + r * E::PITCH + shift(row0 + i * 16 + r) + lane / 16 * 4 * SIZE;
 #pragma unroll
-    for (int j = 0; j < G::TN; ++j) {
-      typename Vec4<O>::type v;
+      for (int j = 0; j < G::TN; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = convert_out<O>(acc[i][j][e]);
-      *(__attribute__((address_space(3))) typename Vec4<O>::type *)(area + (lane % 16) * E::PITCH +
-                                                                    (j * 16 + lane / 16 * 4) * int(sizeof(O))) = v;
+        for (int e = 0; e < 4; ++e) *(lds_o *)(to + (j * 16 + e) * SIZE) = convert_out<O>(acc[i][j][e]);
     }
 #pragma unroll
-    for (int w0 = 0; w0 < 16 * WORDS; w0 += 64) {
-      const int r = (w0 + lane) / WORDS, w = (w0 + lane) % WORDS;
-      const int row = m0 + wr * G::WTM + i * 16 + r;
-      if (row >= M) continue;
-      const __attribute__((address_space(3))) O *from =
-          (const __attribute__((address_space(3))) O *)(area + r * E::PITCH);
+    for (int c = 0; c < 16 * CPR / 64; ++c) {
+      const int r = (c * 64 + lane) / CPR, row = row0 + i * 16 + r, a = shift(row);
+      const int q = (c * 64 + lane) % CPR + (a ? 1 : 0);  // the piece of memory, from the one that the row starts in
+      if (row < M && (q + 1) * 16 <= a + cols * SIZE)
+        *(i16x8 *)((char *)(C + int64_t(row) * N + col0) - a + q * 16) = *(const lds_i16x8 *)(area + r * E::PITCH + q * 16);
+    }
+#pragma unroll
+    for (int c = 0; c < 16 * PER / 64; ++c) {
+      const int r = (c * 64 + lane) / PER, x = (c * 64 + lane) % PER, row = row0 + i * 16 + r, a = shift(row);
+      const int end = a + cols * SIZE, last = end & ~15;  // the piece that the row ends in
       O *to = C + int64_t(row) * N + col0;
-      if constexpr (PER == 1) {
-        if (col0 + w < N) to[w] = from[w];
-      } else {
-        const int odd = int((int64_t(row) * N) & 1), c = 2 * w + odd;
-        if (odd && w == 0 && col0 < N) to[0] = from[0];
-        if (c + 1 < G::WTN && col0 + c + 1 < N) {
-          typedef O O2 __attribute__((ext_vector_type(2)));
-          *reinterpret_cast<O2 *>(to + c) = O2{from[c], from[c + 1]};
-        } else if (c < G::WTN && col0 + c < N) {
-          to[c] = from[c];
-        }
-      }
+      const char *from = area + r * E::PITCH;
+      const int head = a + x * SIZE, tail = last + x * SIZE;
+      if (row < M && (a || end < 16) && head < 16 && head < end) to[x] = *(const lds_o *)(from + head);
+      if (row < M && last > 0 && tail < end) to[(tail - a) / SIZE] = *(const lds_o *)(from + tail);
     }
   }
 }

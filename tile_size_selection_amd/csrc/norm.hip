@@ -102,7 +102,7 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_kernel(int rows, int d, 
 // share of dw in registers over the rows, and the workgroup writes it to its
 // own slice of the workspace (added up in a fixed order afterwards: no
 // atomics, the same bits on every run).
-template <typename T, int CH>
+template <typename T, int CH, int D>
 __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(int rows, int d, const T *dy, const T *hh,
                                                                         const T *weight, const float *rstd, const T *dh,
                                                                         T *dx, float *partial) {
@@ -117,52 +117,72 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(int rows
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = 0;
   }
-  int slot = 0;
-  for (int row = blockIdx.x; row < rows; row += gridDim.x, slot ^= 1) {
+  // the next D rows' loads are in flight while a row is reduced and written
+  Raw8<T> a[D][CH], b[D][CH], e[D][CH];
+  auto load_row = [&](int s, int row) __attribute__((always_inline)) {
     const int64_t base = int64_t(row) * d;
-    Raw8<T> a[CH], b[CH], e[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = threadIdx.x * 8 + c * step;
-      const bool in = col < d;
-      a[c] = in ? load8(dy + base + col) : zero8<T>();
-      b[c] = in ? load8(hh + base + col) : zero8<T>();
-      e[c] = in && dh ? load8(dh + base + col) : zero8<T>();
+      const bool in = col < d && row < rows;
+      a[s][c] = in ? load8(dy + base + col) : zero8<T>();
+      b[s][c] = in ? load8(hh + base + col) : zero8<T>();
+      e[s][c] = in && dh ? load8(dh + base + col) : zero8<T>();
     }
-    const float r = rstd[row];
-    float dot = 0;
+  };
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      float g[8], h[8];
-      widen8(a[c], g);
-      widen8(b[c], h);
+  for (int s = 0; s < D; ++s) load_row(s, blockIdx.x + s * gridDim.x);
+  int slot = 0;
+  for (int row0 = blockIdx.x; row0 < rows; row0 += D * gridDim.x) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xg = h[i] * r * g[i];
-        dw[c][i] += xg;
-        dot += xg * w[c][i];
+    for (int s = 0; s < D; ++s) {
+      const int row = row0 + s * gridDim.x;
+      if (row >= rows) break;
+      const float r = rstd[row];
+      Raw8<T> ca[CH], cb[CH], ce[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        ca[c] = a[s][c];
+        cb[c] = b[s][c];
+        ce[c] = e[s][c];
       }
-    }
-    dot = sum64(dot);
-    if (nw > 1) {
-      // two sets of slots: a wave writes the next row's while others may still read this row's
-      if ((threadIdx.x & 63) == 0) red[slot][wave] = dot;
-      __syncthreads();
-      dot = 0;
-      for (int i = 0; i < nw; ++i) dot += red[slot][i];
-    }
-    const float m = dot / float(d);
+      load_row(s, row + D * gridDim.x);
+      float dot = 0;
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int col = threadIdx.x * 8 + c * step;
-      if (col >= d) continue;
-      float g[8], h[8], o[8];
-      widen8(a[c], g);
-      widen8(b[c], h);
-      widen8(e[c], o);
+      for (int c = 0; c < CH; ++c) {
+        float g[8], h[8];
+        widen8(ca[c], g);
+        widen8(cb[c], h);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[c][i] - h[i] * r * m);
-      store8(dx + base + col, o);
+        for (int i = 0; i < 8; ++i) {
+          const float xg = h[i] * r * g[i];
+          dw[c][i] += xg;
+          dot += xg * w[c][i];
+        }
+      }
+      dot = sum64(dot);
+      if (nw > 1) {
+        // two sets of slots: a wave writes the next row's while others may still read this row's
+        if ((threadIdx.x & 63) == 0) red[slot][wave] = dot;
+        __syncthreads();
+        dot = 0;
+        for (int i = 0; i < nw; ++i) dot += red[slot][i];
+        slot ^= 1;
+      }
+      const float m = dot / float(d);
+      const int64_t base = int64_t(row) * d;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const int col = threadIdx.x * 8 + c * step;
+        if (col >= d) continue;
+        float g[8], h[8], o[8];
+        widen8(ca[c], g);
+        widen8(cb[c], h);
+        widen8(ce[c], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[c][i] - h[i] * r * m);
+        store8(dx + base + col, o);
+      }
     }
   }
 #pragma unroll
@@ -172,27 +192,36 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(int rows
   }
 }
 
-// dw[col] = sum of n partials: a workgroup takes 32 columns, 32 groups of 8
-// lanes each add every 32nd partial, and the groups' sums are added in order.
-constexpr int kReduceCols = 32;
-__global__ __launch_bounds__(256) void rms_norm_dweight_kernel(int n, int d, const float *partial, float *dw) {
-  __shared__ f32x4 s[32][9];
-  const int g = threadIdx.x / 8, l = threadIdx.x % 8;
-  const int col = blockIdx.x * kReduceCols + l * 4;
-  f32x4 acc = {0, 0, 0, 0};
-  if (col < d)
-    for (int p = g; p < n; p += 32) {
+// dw[col] = sum of n partials: a workgroup takes 4 L columns; its groups of L
+// lanes add every (1024 / L)th partial, a wave's groups are joined by shuffles
+// and the 16 waves' sums in order.  L = 8 reads whole lines; narrow rows take
+// L = 2, which gives them four times the workgroups.
+constexpr int kReduceBlock = 1024;
+template <int L>
+__global__ __launch_bounds__(kReduceBlock) void rms_norm_dweight_kernel(int n, int d, const float *partial, float *dw) {
+  __shared__ f32x4 s[kReduceBlock / 64][L];
+  const int g = threadIdx.x / L, l = threadIdx.x % L;
+  const int col = (blockIdx.x * L + l) * 4;
+  float acc[4] = {0, 0, 0, 0};
+  if (col < d) {
+#pragma unroll 4
+    for (int p = g; p < n; p += kReduceBlock / L) {
       const f32x4 v = *reinterpret_cast<const f32x4 *>(partial + int64_t(p) * d + col);
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] += v[i];
     }
-  s[g][l] = acc;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int m = L; m < 64; m *= 2) acc[i] += __shfl_xor(acc[i], m);
+  if (threadIdx.x % 64 < L) s[threadIdx.x / 64][l] = f32x4{acc[0], acc[1], acc[2], acc[3]};
   __syncthreads();
-  if (threadIdx.x < kReduceCols) {
-    const int c = threadIdx.x;
+  const int c = threadIdx.x;
+  if (c < 4 * L && blockIdx.x * 4 * L + c < d) {
     float sum = 0;
-    for (int i = 0; i < 32; ++i) sum += s[i][c / 4][c % 4];
-    if (blockIdx.x * kReduceCols + c < d) dw[blockIdx.x * kReduceCols + c] = sum;
+    for (int i = 0; i < kReduceBlock / 64; ++i) sum += s[i][c / 4][c % 4];
+    dw[blockIdx.x * 4 * L + c] = sum;
   }
 }
 
@@ -246,21 +275,30 @@ void launch_norm(int64_t rows, int64_t d, const void *x, const void *residual, c
   else go(rms_norm_kernel<T, FP8, 4>);
 }
 
-// Workgroups of the backward pass: enough to fill the chip twice over.
-int64_t backward_blocks(int64_t rows) { return rows < 1024 ? rows : 1024; }
+// Workgroups of the backward pass: 12 waves a CU and two workgroups at least,
+// but each adds 8 bytes a column (its share of dw, written and read) to the 8
+// a column that a row of 16-bit elements moves, so no more than one for every
+// 4 rows where that still gives every CU one.
+int64_t backward_blocks(int64_t rows, int64_t d) {
+  constexpr int64_t cus = 256;
+  const int64_t per_cu = 12 / row_shape(d, 1).waves, fill = cus * (per_cu > 2 ? per_cu : 2);
+  const int64_t n = rows / 4 < cus ? cus : rows / 4 > fill ? fill : rows / 4;
+  return rows < n ? rows : n;
+}
 
 template <typename T>
 void launch_backward(int64_t rows, int64_t d, const void *dy, const void *h, const void *weight, const float *rstd,
                      const void *dh, void *dx, float *partial, hipStream_t s) {
-  const RowShape f = row_shape(d, 2);
-  const dim3 grid(uint32_t(backward_blocks(rows)));
+  const RowShape f = row_shape(d, 1);
+  const dim3 grid(uint32_t(backward_blocks(rows, d)));
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(f.waves * 64), 0, s, int(rows), int(d), static_cast<const T *>(dy),
                        static_cast<const T *>(h), static_cast<const T *>(weight), rstd, static_cast<const T *>(dh),
                        static_cast<T *>(dx), partial);
   };
-  if (f.chunks == 2) go(rms_norm_backward_kernel<T, 2>);
-  else go(rms_norm_backward_kernel<T, 4>);
+  if (f.chunks == 1) go(rms_norm_backward_kernel<T, 1, 2>);
+  else if (f.chunks == 2) go(rms_norm_backward_kernel<T, 2, 1>);
+  else go(rms_norm_backward_kernel<T, 4, 1>);
 }
 
 }  // namespace
@@ -295,7 +333,7 @@ int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d) {
   if (rows < 0 || d < 1) return TSS_E_ARG;
   if (d % 8) return TSS_E_ALIGN;
   if (d > kMaxD) return TSS_E_UNSUPPORTED;
-  return backward_blocks(rows) * d * 4;
+  return backward_blocks(rows, d) * d * 4;
 }
 
 int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
@@ -318,8 +356,12 @@ int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void
   if (dtype == TSS_F16) launch_backward<_Float16>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
   else if (dtype == TSS_BF16) launch_backward<__bf16>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
   else launch_backward<float>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
-  hipLaunchKernelGGL(rms_norm_dweight_kernel, dim3(uint32_t((d + kReduceCols - 1) / kReduceCols)), dim3(256), 0, s,
-                     int(backward_blocks(rows)), int(d), partial, dweight);
+  auto reduce = [&](auto kernel, int64_t cols) {
+    hipLaunchKernelGGL(kernel, dim3(uint32_t((d + cols - 1) / cols)), dim3(kReduceBlock), 0, s,
+                       int(backward_blocks(rows, d)), int(d), partial, dweight);
+  };
+  if (d > 2048) reduce(rms_norm_dweight_kernel<8>, 32);
+  else reduce(rms_norm_dweight_kernel<2>, 8);
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 
