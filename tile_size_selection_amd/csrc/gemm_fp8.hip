@@ -19,10 +19,11 @@ using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;   // fp32 outputs; two workgroup
 using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;     // two workgroups a CU
 constexpr int kRoundsLds = Tile256::LDS_BYTES > Piece256::LDS_BYTES ? Tile256::LDS_BYTES : Piece256::LDS_BYTES;
 
-// How a product is run: by tiles of bm x bn (K in `splits` ranges), or
-// (bn == 16) by the kernel for few rows.
+// How a product is run: by tiles of bm x bn, K in `splits` ranges of their own
+// workgroups and each of them in `sets` of a workgroup's waves; or (bn == 16)
+// by the kernel for few rows.
 struct Plan {
-  int bm, bn, splits;
+  int bm, bn, splits, sets = 1;
 };
 
 Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
@@ -40,14 +41,23 @@ Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
   int64_t s = b >= kCUs ? 1 : kCUs / b;
   if (s > kb / 8) s = kb / 8;  // at least eight steps of K a range
   s = s > 8 ? 8 : s < 1 ? 1 : s;
-  return {64, 128, int(s)};
+  // Two sets of waves in a workgroup, where a CU has but one: they shorten the
+  // steps' chains of waits (1620 x 776 x 3584: 17.0 -> 15.2 us; fp32 output,
+  // 1236 x 1382 x 5008: 37.8 -> 29.2) but cost 1 to 2 us at the ends (968 x
+  // 2052 x 864: 12.1 -> 18.5).
+  const bool sets = b * s <= kCUs && kb / s >= (exact ? 8 : 16);
+  return {64, 128, int(s), sets ? 2 : 1};
 }
 
+// Small tiles where they leave CUs free anyway (581 rows in 3 groups, K 2240, N
+// 792: 13.9 us against 16.0 and 15.5 with 128 x 128 and 256 x 256) and for few
+// rows a group; large ones from 192 (128 rows a group, E = 32, K = 4096, N =
+// 2048: 95, 85 and 92 us with the three tiles; 256 rows: 155, 141 and 111).
 Plan plan_grouped(int64_t T, int64_t N, int64_t K, int64_t E, bool exact) {
   const int64_t rows = T / E;  // of an average group
   const int64_t tiles64 = (T / 64 + E < T ? T / 64 + E : T) * ((N + 127) / 128), a_reads = (N + 15) / 16 * T * K;
   if (K > 0 && tiles64 < kCUs && a_reads <= int64_t(40) << 20) return {16, 16, 1};
-  if (rows <= 64) return {64, 128, 1};
+  if (rows <= 64 || tiles64 <= kCUs) return {64, 128, 1, tiles64 <= kCUs && K >= (exact ? 1024 : 4096) ? 2 : 1};
   if (rows <= 192 || exact) return {128, 128, 1};
   return {256, 256, 1};
 }
@@ -69,11 +79,11 @@ hipError_t launch_lds(Kernel kernel, std::atomic<uint64_t> &attr_set, const Fp8A
   return hipGetLastError();
 }
 
-template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+template <typename G, int KG, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
 hipError_t launch_tile(const Fp8Args &a, int64_t blocks, hipStream_t s) {
   static std::atomic<uint64_t> attr_set{0};
-  return launch_lds(gemm_fp8_tile_kernel<G, A_E5M2, B_ROWS, GROUPED, EXACT>, attr_set, a, blocks, G::THREADS,
-                    G::LDS_BYTES, s);
+  return launch_lds(gemm_fp8_tile_kernel<G, KG, A_E5M2, B_ROWS, GROUPED, EXACT>, attr_set, a, blocks, KG * G::THREADS,
+                    KG * G::LDS_BYTES, s);
 }
 
 // tiles: the most there can be (grouped), or all there are.
@@ -112,10 +122,11 @@ hipError_t launch(Fp8Args &a, const Plan &pl, bool exact, hipStream_t s, int32_t
     if constexpr (!X)
       if (pl.bm == 256) return launch_rounds<A_E5M2, B_ROWS, GROUPED>(a, blocks, s);
     if (pl.bm == 128) {
-      if constexpr (X) return launch_tile<Tile128, A_E5M2, B_ROWS, GROUPED, true>(a, blocks, s);
-      else return launch_tile<Piece128, A_E5M2, B_ROWS, GROUPED, false>(a, blocks, s);
+      if constexpr (X) return launch_tile<Tile128, 1, A_E5M2, B_ROWS, GROUPED, true>(a, blocks, s);
+      else return launch_tile<Piece128, 1, A_E5M2, B_ROWS, GROUPED, false>(a, blocks, s);
     }
-    return launch_tile<Tile64, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
+    return pl.sets == 2 ? launch_tile<Tile64, 2, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s)
+                        : launch_tile<Tile64, 1, A_E5M2, B_ROWS, GROUPED, X>(a, blocks, s);
   };
   return exact ? go(std::true_type{}) : go(std::false_type{});
 }

@@ -225,18 +225,29 @@ __device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::
 // copies in its first half 449-459, this 439 (2.50 PFLOP/s).  Of 459 us,
 // leaving out the copies took 62, the scaling 47, the fragment reads 118; the
 // MFMAs alone took 271.
-template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
-__device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile &t, char *smem) {
+//
+// KG > 1: as many sets of G::NW waves share the tile, each taking a range of K
+// with a ring of its own; their sums are added at the end, in order.  It fills
+// a CU where there are too few tiles for two workgroups each.
+template <typename G, int KG, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+__device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile &t, char *smem0) {
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int set = KG > 1 ? wave_all / G::NW : 0, wave = KG > 1 ? wave_all % G::NW : wave_all;
   const int wr = wave / G::WN, wc = wave % G::WN;
+  char *smem = smem0 + set * G::LDS_BYTES;
   const int rows = t.row_end - t.row0, cols = min(G::BN, p.N - t.n0);
-  const int kbeg = t.split * p.k_split;
+  int kbeg = t.split * p.k_split;
   // rows of no group: no product, zeros are written
-  const int K = GROUPED && t.group == p.groups ? 0 : max(0, min(p.k_split, p.K - kbeg));
+  int K = GROUPED && t.group == p.groups ? 0 : max(0, min(p.k_split, p.K - kbeg));
+  const int steps = (K + KG * 128 - 1) / (KG * 128);  // of every set; past a set's end they add zeros
+  if constexpr (KG > 1) {
+    kbeg += set * steps * 128;
+    K = max(0, min(K - set * steps * 128, steps * 128));
+  }
   const int nk = (K + 127) / 128;
   const int kb0 = kbeg / 128, kblocks = (p.K + 127) / 128;
-  const int group = GROUPED ? (K ? t.group : 0) : 0;
+  const int group = GROUPED && t.group < p.groups ? t.group : 0;
 
   const i32x4 rsA = buffer_rsrc(p.A + int64_t(t.row0) * p.K + kbeg, K ? uint32_t(rows - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
   const i32x4 rsB = buffer_rsrc(p.B + (int64_t(group) * p.N + t.n0) * p.K + kbeg,
@@ -354,7 +365,7 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
   // (A loop of its own: with the test inside the loop below the registers
   // spill.)
   if (wr * G::WTM >= rows) {
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = 0; kt < steps; ++kt) {
       wait_vmcnt_lgkm0<(ST - 2) * G::LPW>();
       block_barrier();
 #pragma unroll
@@ -362,7 +373,7 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
       slot = slot + 1 == ST ? 0 : slot + 1;
     }
   } else {
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = 0; kt < steps; ++kt) {
       const int next = slot + 1 == ST ? 0 : slot + 1;
       const char *sta = smem + slot * G::STAGE_BYTES + wr * G::WTM * 128;
       const char *stn = smem + next * G::STAGE_BYTES;
@@ -411,6 +422,35 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
     }
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
+  if constexpr (KG > 1) {
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    lds_f32x4 *sums = (lds_f32x4 *)smem0;  // [set - 1][MFMA tile][wave][lane]
+    static_assert((KG - 1) * G::TM * G::TN * G::NW * 1024 <= KG * G::LDS_BYTES, "the sets' sums fit");
+    block_barrier();
+    if (set > 0) {
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j)
+          sums[(((set - 1) * G::TM * G::TN + i * G::TN + j) * G::NW + wave) * 64 + lane] = acc[i][j];
+      wait_vmcnt_lgkm0<0>();
+    }
+    block_barrier();
+    if (set > 0) {
+      block_barrier();  // the one that the store begins with
+      return;
+    }
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < G::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < G::TN; ++j) {
+          const f32x4 v = sums[((g * G::TM * G::TN + i * G::TN + j) * G::NW + wave) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
+        }
+    wait_vmcnt_lgkm0<0>();
+  }
 
   auto store = [&](auto o) __attribute__((always_inline)) {
     using O = decltype(o);
@@ -429,11 +469,11 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
   }
 }
 
-template <typename G, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
-__global__ __launch_bounds__(G::THREADS) void gemm_fp8_tile_kernel(Fp8Args p) {
+template <typename G, int KG, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
+__global__ __launch_bounds__(G::THREADS *KG) void gemm_fp8_tile_kernel(Fp8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const Fp8Tile t = fp8_tile<G::BM, G::BN, GROUPED>(p, threadIdx.x & 63);
-  if (t.any) fp8_tile_product<G, A_E5M2, B_ROWS, GROUPED, EXACT>(p, t, smem);
+  if (t.any) fp8_tile_product<G, KG, A_E5M2, B_ROWS, GROUPED, EXACT>(p, t, smem);
 }
 
 // Large products: one workgroup fills a CU, and the last round's tiles are cut
@@ -449,7 +489,7 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) 
   if (bid < whole || pieces == 1) {
     if (bid >= n) return;
     const int id = bid < whole ? xcd_run(bid, whole) : whole + xcd_run(bid - whole, rest);
-    fp8_tile_product<G, A_E5M2, B_ROWS, GROUPED, false>(p, fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane), smem);
+    fp8_tile_product<G, 1, A_E5M2, B_ROWS, GROUPED, false>(p, fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane), smem);
     return;
   }
   if (bid >= whole + rest * pieces) return;
@@ -459,8 +499,8 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) 
   t.row_end = min(t.row_end, t.row0 + Half::BM);
   if (pieces == 4) t.n0 += part % 2 * Quarter::BN;
   if (t.row0 >= t.row_end || t.n0 >= p.N) return;
-  if (pieces == 2) fp8_tile_product<Half, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
-  else fp8_tile_product<Quarter, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
+  if (pieces == 2) fp8_tile_product<Half, 1, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
+  else fp8_tile_product<Quarter, 1, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
 }
 
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it

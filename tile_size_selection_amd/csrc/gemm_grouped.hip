@@ -18,6 +18,135 @@ using Piece128 = Geometry<128, 128, 64, 4, 8, 16>;
 using Tile128 = Geometry<128, 128, 64, 2, 4, 16>;
 using Tile64 = Geometry<64, 64, 64, 4, 4, 16>;
 
+// Few rows: the weights' bytes and the length of a workgroup's walk over K are
+// the cost.  A workgroup takes 16 rows and 32 columns; its waves share K in
+// chunks of 32, every chunk of the weights going from memory straight into
+// MFMA fragments, and their sums are joined through LDS in the order of the
+// waves.  A lane of a v_mfma_f32_16x16x32 fragment holds 8 of K.
+//   Forward: B's rows run along N.  A lane loads two neighbouring columns of
+//   each of its 8 k, the even one for the first MFMA tile and the odd one for
+//   the second: a byte permutation of the lane's own words gives both their
+//   fragments.  (Eight columns a lane and 128 a workgroup need a fourth of the
+//   loads but leave too few workgroups: 1 row, 6 groups, K = 2048, N = 800:
+//   8.7 us against 6.0.)
+//   GradA: B's rows run along the reduction, and are loaded as fragments.
+constexpr int kFewTiles = 2, kFewCols = 16 * kFewTiles;
+constexpr int kFewUnroll = 4;  // chunks whose loads a wave has in flight
+
+template <typename T, int GRP>
+__global__ __launch_bounds__(1024) void grouped_rows_kernel(KernelArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = int(count_group_tiles<16>(p.sizes, p.groups, p.M, lane)) * p.tiles_n;
+  if (int(blockIdx.x) >= n) return;
+  const int id = xcd_run(blockIdx.x, n), tm = id / p.tiles_n, n0 = (id - tm * p.tiles_n) * kFewCols;
+  const GroupTile t = find_group_tile<16>(p.sizes, p.groups, p.M, tm, lane);
+  const bool none = t.group == p.groups;  // rows of no group: zeros
+  const int rows = t.row_end - t.row0, K = none ? 0 : p.K, N = p.N;
+  auto rsrc = [](const void *base, uint32_t range) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
+  };
+  const auto rsA = rsrc(static_cast<const T *>(p.A) + int64_t(t.row0) * p.lda, uint32_t(rows) * uint32_t(p.lda) * 2u);
+  const T *B = static_cast<const T *>(p.B) + (none ? 0 : int64_t(t.group) * p.batch_stride_b);
+  const auto rsB = rsrc(B, uint32_t(p.batch_stride_b) * 2u);  // one group's: below 2 GiB
+  const int fr = lane % 16, kl = lane / 16 * 8;
+  const uint32_t a_off = fr < rows ? (uint32_t(fr) * uint32_t(p.lda) + uint32_t(kl)) * 2u : kOOB;
+
+  f32x4 acc[kFewTiles];
+#pragma unroll
+  for (int j = 0; j < kFewTiles; ++j) acc[j] = f32x4{0, 0, 0, 0};
+  for (int k0 = wave * 32; k0 < K; k0 += nw * 32 * kFewUnroll) {
+    i32x4 a[kFewUnroll];
+    uint32_t b[kFewUnroll][8];  // forward: a word for each k; GradA: four for each tile
+#pragma unroll
+    for (int u = 0; u < kFewUnroll; ++u) {
+      const int k = k0 + u * nw * 32 + kl;  // K is a multiple of 8: a lane's 8 are all in or all out
+      a[u] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                           rsA, k < K && a_off != kOOB ? a_off + uint32_t(k - kl) * 2u : kOOB, 0, 0));
+      if constexpr (GRP == kGroupForward) {
+        const int col = n0 + fr * 2;  // N is even: both columns are in or out
+        const uint32_t off = k < K && col < N ? (uint32_t(k) * uint32_t(N) + uint32_t(col)) * 2u : kOOB;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          b[u][j] = uint32_t(__builtin_amdgcn_raw_buffer_load_b32(
+              rsB, off == kOOB ? kOOB : off + uint32_t(j) * uint32_t(N) * 2u, 0, 0));
+      } else {
+#pragma unroll
+        for (int j = 0; j < kFewTiles; ++j) {
+          const int row = n0 + j * 16 + fr;
+          const i32x4 v = __builtin_bit_cast(
+              i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                         rsB, k < K && row < N ? (uint32_t(row) * uint32_t(p.ldb) + uint32_t(k)) * 2u : kOOB, 0, 0));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[u][j * 4 + i] = uint32_t(v[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFewUnroll; ++u)
+#pragma unroll
+      for (int j = 0; j < kFewTiles; ++j) {
+        i32x4 f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          f[i] = GRP == kGroupForward
+                     ? int(__builtin_amdgcn_perm(b[u][2 * i + 1], b[u][2 * i], j ? 0x07060302u : 0x05040100u))
+                     : int(b[u][j * 4 + i]);
+        acc[j] = Mfma<T>::m16(__builtin_bit_cast(i16x8, f), __builtin_bit_cast(i16x8, a[u]), acc[j]);
+      }
+  }
+  f32x4 *red = reinterpret_cast<f32x4 *>(smem);
+#pragma unroll
+  for (int j = 0; j < kFewTiles; ++j) red[(wave * kFewTiles + j) * 64 + lane] = acc[j];
+  __syncthreads();
+  // wave w adds up tiles w, w + nw, ...
+  for (int j = wave; j < kFewTiles; j += nw) {
+    f32x4 s = red[j * 64 + lane];
+    for (int w = 1; w < nw; ++w) {
+      const f32x4 v = red[(w * kFewTiles + j) * 64 + lane];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += v[e];
+    }
+    red[j * 64 + lane] = s;  // read by this wave only so far
+  }
+  __syncthreads();
+  // 16 rows of 32 columns, 4 neighbours a lane
+  auto put = [&](auto o) __attribute__((always_inline)) {
+    using O = decltype(o);
+    for (int x = threadIdx.x; x < 16 * kFewCols / 4; x += blockDim.x) {
+      const int r = x / (kFewCols / 4), c = x % (kFewCols / 4) * 4;
+      if (r >= rows || n0 + c >= N) continue;
+      typename Vec4<O>::type v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // column c + i: its tile, and its place 0 .. 15 in the tile (lane group and register)
+        const int j = GRP == kGroupForward ? (c + i) % kFewTiles : (c + i) / 16;
+        const int at = GRP == kGroupForward ? (c + i) / kFewTiles : (c + i) % 16;
+        v[i] = convert_out<O>(red[j * 64 + at / 4 * 16 + r][at % 4]);
+      }
+      *reinterpret_cast<typename Vec4<O>::type *>(static_cast<O *>(p.C) + int64_t(t.row0 + r) * N + n0 + c) = v;
+    }
+  };
+  if (p.out_dtype == TSS_F32) put(float{});
+  else if (p.out_dtype == TSS_F16) put(_Float16{});
+  else put(__bf16{});
+}
+
+template <typename T, int GRP>
+hipError_t launch_few(KernelArgs &a, hipStream_t s, int32_t *status) {
+  a.tiles_n = int32_t((int64_t(a.N) + kFewCols - 1) / kFewCols);
+  const int64_t blocks = max_group_tiles(a.M, a.groups, 16) * a.tiles_n;
+  int nw = (a.K + 32 * kFewUnroll - 1) / (32 * kFewUnroll);
+  nw = nw > 8 ? 8 : nw < 1 ? 1 : nw;  // (16: 6.8 us where 8 take 6.0)
+  if (blocks * nw * 64 > int64_t(UINT32_MAX)) {
+    *status = TSS_E_ARG;
+    return hipSuccess;
+  }
+  hipLaunchKernelGGL((grouped_rows_kernel<T, GRP>), dim3(uint32_t(blocks)), dim3(nw * 64), nw * kFewTiles * 1024, s, a);
+  return hipGetLastError();
+}
+
 constexpr int most(int a, int b) { return a > b ? a : b; }
 
 template <typename G, typename Half, typename Quarter, typename T, int GRP>
@@ -55,10 +184,18 @@ hipError_t launch(KernelArgs &a, hipStream_t s, int32_t *status) {
 // Few rows in an average group: the groups' weights are the cost, and small
 // tiles put more of their loads in flight.  Forward, E = 32, K = N = 2048,
 // 64 x 64 against 256 x 256 tiles: 16 rows a group 57 and 61 us, 64 rows 73
-// and 63, 256 rows 181 and 99.
+// and 63, 256 rows 181 and 99; where the small ones fit the chip at once, 78
+// rows in 25 groups, K = 2208, N = 640: 22 and 38.
 template <typename T, int GRP>
 hipError_t launch_rows(KernelArgs &a, hipStream_t s, int32_t *status) {
-  if (a.M / a.groups <= 32) return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
+  // The kernel for few rows reads 3/16 of a byte for each of T K N from L2, at
+  // 5.5 TB/s, against 0.2 us for each 64 of K where the small tiles leave CUs
+  // free: T N up to about 1e5.  162 rows in 2 groups, K = 2560, N = 344: 10.1
+  // and 13.1 us; 64 rows in 32 groups, K = 4096, N = 2048: 89 and 83.
+  const int64_t rows64 = a.M / 64 + a.groups, tiles64 = (rows64 < a.M ? rows64 : a.M) * ((int64_t(a.N) + 63) / 64);
+  if (tiles64 <= 2 * kCUs && int64_t(a.M) * a.N <= int64_t(1) << 17) return launch_few<T, GRP>(a, s, status);
+  const int64_t rows = a.M / a.groups;  // of an average group
+  if (rows <= 32 || (rows <= 128 && tiles64 <= 3 * kCUs)) return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
   return launch<Tile256, Piece256, Piece128, T, GRP>(a, s, status);
 }
 
