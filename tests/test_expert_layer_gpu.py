@@ -29,7 +29,7 @@ def test_layer_and_its_gradients():
     dev = [t.to(CUDA) for t in (x, residual, norm, w1, w2)]
     r = X.route(expert.to(CUDA), weight.to(CUDA), experts)
     assert r.sizes.tolist() == [int((expert == e).sum()) for e in range(experts)]
-    off = lambda got, want: float((got.double().cpu() - want).norm() / want.norm())  # noqa: E731
+    off = lambda got, want: float((got.double().cpu() - want.detach()).norm() / want.detach().norm())  # noqa: E731
     got, got_h, saved = X.forward(*dev, r)
     back = X.backward(dout.to(CUDA), dh.to(CUDA), *dev[2:], r, saved)
     # a chain of at most 8 roundings to bf16 (2^-8 each, and of random signs over the norm)

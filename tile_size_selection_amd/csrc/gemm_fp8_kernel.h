@@ -24,7 +24,7 @@
 // operands through LDS; gemm_fp8_rows_kernel, for few rows, streams B from
 // memory straight into registers.
 #pragma once
-#include "gemm_kernel.h"
+#include "grouped_kernel.h"
 
 namespace tss {
 
@@ -489,7 +489,12 @@ __global__ __launch_bounds__(G::THREADS) void gemm_fp8_rounds_kernel(Fp8Args p) 
   if (bid < whole || pieces == 1) {
     if (bid >= n) return;
     const int id = bid < whole ? xcd_run(bid, whole) : whole + xcd_run(bid - whole, rest);
-    fp8_tile_product<G, 1, A_E5M2, B_ROWS, GROUPED, false>(p, fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane), smem);
+    const Fp8Tile t = fp8_tile_at<G::BM, G::BN, GROUPED>(p, id, lane);
+    // the last tile of a group, when half empty: one piece holds it
+    if (GROUPED && t.row_end - t.row0 <= Half::BM)
+      fp8_tile_product<Half, 1, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
+    else
+      fp8_tile_product<G, 1, A_E5M2, B_ROWS, GROUPED, false>(p, t, smem);
     return;
   }
   if (bid >= whole + rest * pieces) return;

@@ -1,8 +1,8 @@
 // Products grouped by expert in fp16 / bf16: tss_gemm_grouped and its
-// gradients, on the GEMM kernel's group modes (gemm_kernel.h).
+// gradients (grouped_kernel.h).
 #include <atomic>
 
-#include "gemm_kernel.h"
+#include "grouped_kernel.h"
 
 using namespace tss;
 
@@ -34,7 +34,7 @@ constexpr int kFewTiles = 2, kFewCols = 16 * kFewTiles;
 constexpr int kFewUnroll = 4;  // chunks whose loads a wave has in flight
 
 template <typename T, int GRP>
-__global__ __launch_bounds__(1024) void grouped_rows_kernel(KernelArgs p) {
+__global__ __launch_bounds__(1024) void grouped_rows_kernel(GroupedArgs p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -48,8 +48,8 @@ __global__ __launch_bounds__(1024) void grouped_rows_kernel(KernelArgs p) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
   };
   const auto rsA = rsrc(static_cast<const T *>(p.A) + int64_t(t.row0) * p.lda, uint32_t(rows) * uint32_t(p.lda) * 2u);
-  const T *B = static_cast<const T *>(p.B) + (none ? 0 : int64_t(t.group) * p.batch_stride_b);
-  const auto rsB = rsrc(B, uint32_t(p.batch_stride_b) * 2u);  // one group's: below 2 GiB
+  const T *B = static_cast<const T *>(p.B) + (none ? 0 : int64_t(t.group) * p.b_stride);
+  const auto rsB = rsrc(B, uint32_t(p.b_stride) * 2u);  // one group's: below 2 GiB
   const int fr = lane % 16, kl = lane / 16 * 8;
   const uint32_t a_off = fr < rows ? (uint32_t(fr) * uint32_t(p.lda) + uint32_t(kl)) * 2u : kOOB;
 
@@ -134,7 +134,7 @@ __global__ __launch_bounds__(1024) void grouped_rows_kernel(KernelArgs p) {
 }
 
 template <typename T, int GRP>
-hipError_t launch_few(KernelArgs &a, hipStream_t s, int32_t *status) {
+hipError_t launch_few(GroupedArgs &a, hipStream_t s, int32_t *status) {
   a.tiles_n = int32_t((int64_t(a.N) + kFewCols - 1) / kFewCols);
   const int64_t blocks = max_group_tiles(a.M, a.groups, 16) * a.tiles_n;
   int nw = (a.K + 32 * kFewUnroll - 1) / (32 * kFewUnroll);
@@ -150,12 +150,11 @@ hipError_t launch_few(KernelArgs &a, hipStream_t s, int32_t *status) {
 constexpr int most(int a, int b) { return a > b ? a : b; }
 
 template <typename G, typename Half, typename Quarter, typename T, int GRP>
-hipError_t launch(KernelArgs &a, hipStream_t s, int32_t *status) {
+hipError_t launch(GroupedArgs &a, hipStream_t s, int32_t *status) {
   constexpr bool ragged = GRP != kGroupGradB, pieces = !__is_same(G, Half);
   a.tiles_n = int32_t((int64_t(a.N) + G::BN - 1) / G::BN);
   const int64_t tiles_m = ragged ? max_group_tiles(a.M, a.groups, G::BM) : (int64_t(a.M) + G::BM - 1) / G::BM;
   a.tiles_m = int32_t(tiles_m);
-  a.group_m = a.tiles_m < 4 ? a.tiles_m : 4;
   const int64_t tiles = tiles_m * a.tiles_n * (ragged ? 1 : a.groups);
   // (ragged: the most there can be)
   const int64_t whole = pieces ? tiles / kCUs * kCUs : tiles, rest = tiles - whole;
@@ -187,7 +186,7 @@ hipError_t launch(KernelArgs &a, hipStream_t s, int32_t *status) {
 // and 63, 256 rows 181 and 99; where the small ones fit the chip at once, 78
 // rows in 25 groups, K = 2208, N = 640: 22 and 38.
 template <typename T, int GRP>
-hipError_t launch_rows(KernelArgs &a, hipStream_t s, int32_t *status) {
+hipError_t launch_rows(GroupedArgs &a, hipStream_t s, int32_t *status) {
   // The kernel for few rows reads 3/16 of a byte for each of T K N from L2, at
   // 5.5 TB/s, against 0.2 us for each 64 of K where the small tiles leave CUs
   // free: T N up to about 1e5.  162 rows in 2 groups, K = 2560, N = 344: 10.1
@@ -203,7 +202,7 @@ hipError_t launch_rows(KernelArgs &a, hipStream_t s, int32_t *status) {
 // N = 2048, 2 rows a group: 128 x 128 tiles 165 us, 256 x 256 178; K = N =
 // 2048, 64 rows a group 99 and 100, 256 rows 143 and 136.
 template <typename T>
-hipError_t launch_grad_b(KernelArgs &a, hipStream_t s, int32_t *status) {
+hipError_t launch_grad_b(GroupedArgs &a, hipStream_t s, int32_t *status) {
   if (a.rows_total / a.groups <= 64) return launch<Tile128, Tile128, Tile128, T, kGroupGradB>(a, s, status);
   return launch<Tile256, Piece256, Piece128, T, kGroupGradB>(a, s, status);
 }
@@ -229,16 +228,15 @@ int32_t tss_gemm_grouped(int64_t T, int64_t E, int64_t K, int64_t N, int32_t dty
   if (T == 0 || N == 0) return TSS_OK;
   if (!C || !sizes || (K > 0 && (!A || !B))) return TSS_E_ARG;
   if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(sizes, 4)) return TSS_E_ALIGN;
-  KernelArgs a{};
+  GroupedArgs a{};
   a.A = A;
   a.B = B;
   a.C = C;
   a.M = int32_t(T);
   a.N = int32_t(N);
-  a.K = a.lda = a.k_split = int32_t(K);
-  a.splits = 1;
+  a.K = a.lda = int32_t(K);
   a.out_dtype = out_dtype;
-  a.batch_stride_b = K * N;
+  a.b_stride = K * N;
   a.sizes = sizes;
   a.groups = int32_t(E);
   a.rows_total = int32_t(T);
@@ -262,8 +260,7 @@ int32_t tss_gemm_grouped_backward(int64_t T, int64_t E, int64_t K, int64_t N, in
     return TSS_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err = hipSuccess;
-  KernelArgs a{};
-  a.splits = 1;
+  GroupedArgs a{};
   a.sizes = sizes;
   a.groups = int32_t(E);
   a.rows_total = int32_t(T);
@@ -273,9 +270,9 @@ int32_t tss_gemm_grouped_backward(int64_t T, int64_t E, int64_t K, int64_t N, in
     a.C = dA;
     a.M = int32_t(T);
     a.N = int32_t(K);
-    a.K = a.lda = a.ldb = a.k_split = int32_t(N);
+    a.K = a.lda = a.ldb = int32_t(N);
     a.out_dtype = dtype;
-    a.batch_stride_b = K * N;
+    a.b_stride = K * N;
     err = dtype == TSS_F16 ? launch_rows<_Float16, kGroupGradA>(a, s, &st) : launch_rows<__bf16, kGroupGradA>(a, s, &st);
   }
   if (want_b && err == hipSuccess && st == TSS_OK) {
@@ -284,9 +281,9 @@ int32_t tss_gemm_grouped_backward(int64_t T, int64_t E, int64_t K, int64_t N, in
     a.C = dB;
     a.M = a.lda = int32_t(K);
     a.N = int32_t(N);
-    a.K = a.k_split = int32_t(T);
+    a.K = int32_t(T);
     a.out_dtype = db_dtype;
-    a.batch_stride_c = K * N;
+    a.c_stride = K * N;
     err = dtype == TSS_F16 ? launch_grad_b<_Float16>(a, s, &st) : launch_grad_b<__bf16>(a, s, &st);
   }
   if (st != TSS_OK) return st;

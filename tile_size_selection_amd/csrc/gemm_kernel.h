@@ -41,16 +41,6 @@
 // derives its input rows and columns and the sub-operator pads from the
 // Tiling page's H/W tiling formulas; chunks that fall in a pad, outside the
 // slice or past the channels read as zero.
-//
-// And it computes products grouped by expert (GRP != kUngrouped): rows sorted
-// by group, the groups' sizes in device memory (groups.h).
-//   kGroupForward: C[rows of e] = A[rows of e] B[e]; as the GEMM, the rows of
-//     a tile ending with their group;
-//   kGroupGradA:   dA[rows of e] = dC[rows of e] B[e]^T; the B operand's rows
-//     are contiguous along the reduction, so it is copied and read like A;
-//   kGroupGradB:   dB[e] = A[rows of e]^T dC[rows of e]; the reduction runs
-//     over the group's rows, so the A operand is copied and read like the
-//     GEMM's B, with the transpose read.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -58,11 +48,8 @@
 #include <utility>
 
 #include "../../include/tss.h"
-#include "groups.h"
 
 namespace tss {
-
-enum GroupMode { kUngrouped, kGroupForward, kGroupGradA, kGroupGradB };
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -101,12 +88,6 @@ struct KernelArgs {
   int32_t Cs;  // channels per pixel in memory: B's pixel stride and A's stride per tap (Cp or Cin)
   int32_t tile_ow, tile_n, n_ht, n_wt;
   int32_t y_nhwc;  // output y[Nb][OH][OW][Cout] (channel-last) instead of y[Nb][Cout][OH][OW]
-  // Grouped products only.  M x N x K: the forward's T x N x K; GradA's T x K
-  // x N; GradB's K x N with T rows to reduce over.  batch_stride_b (and, for
-  // GradB, batch_stride_c) steps from group to group.
-  const int32_t *sizes;  // rows of each group, device memory
-  int32_t groups, ldb;   // ldb: GradA, elements between B's rows
-  int32_t rows_total;    // T
 };
 
 // ---- small device helpers --------------------------------------------------
@@ -250,9 +231,8 @@ struct Geometry {
   // rows (k % 4 == 0) in each 16-lane group, rows 8 apart across groups; the
   // swizzle spreads those rows over distinct 64-byte quarters and 32-byte
   // halves of the bank space.
-  template <int CHUNKS = CB>
   static __device__ __forceinline__ int swz_b(int k) {
-    int q = CHUNKS >= 16 ? 4 * (k % 4) : 4 * ((k / 2) % 2);
+    int q = CB >= 16 ? 4 * (k % 4) : 4 * ((k / 2) % 2);
     return q ^ (2 * ((k / 8) % 2));
   }
 
@@ -266,16 +246,15 @@ struct Geometry {
     const int lc = q * (FK / 8) + lane / MF;
     return uint32_t((row0 + r) * BK * 2 + ((swizzle ? lc ^ swz_a(r) : lc) * 16));
   }
-  // N-contiguous rows (the GEMM's B; WIDTH columns), read by the transpose read (4 k-rows x
+  // N-contiguous rows (the GEMM's B), read by the transpose read (4 k-rows x
   // 16 columns per 16-lane group): source lane s = lane % 16 points at row
   // kbase + s/4, columns col0 + 4*(s%4) .. +3; K step q adds q*FK rows.
-  template <int WIDTH = BN>
   static __device__ __forceinline__ uint32_t frag_n_rows(int col0, int lane, bool swizzle = true) {
     const int g = lane / 16, s = lane % 16;
     const int krow = MF == 32 ? (g / 2) * 8 + s / 4 : g * 8 + s / 4;
     const int n = col0 + (MF == 32 ? (g % 2) * 16 + 4 * (s % 4) : 4 * (s % 4));
     const int lc = n / 8;
-    return uint32_t(krow * WIDTH * 2 + ((swizzle ? lc ^ swz_b<WIDTH / 8>(krow) : lc) * 16) + (n % 8) * 2);
+    return uint32_t(krow * BN * 2 + ((swizzle ? lc ^ swz_b(krow) : lc) * 16) + (n % 8) * 2);
   }
 };
 
@@ -450,15 +429,9 @@ __device__ __forceinline__ void store_conv(const Acc (&acc)[G::TM][G::TN], O *y,
 
 // ---- the kernel ----------------------------------------------------------------
 
-// The product of one tile: rows m0 .. M - 1 (at most BM) and columns from n0
-// of batch entry, conv tile or group bz, over K elements from kbeg (K == 0 for
-// a range past the end, and for rows of no group: zeros).
-template <typename G, typename T, bool CONV, int GRP = kUngrouped>
-__device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, int m0, int n0, int M, int K, int bz,
-                                             int split, int kbeg) {
-  static_assert(!CONV || GRP == kUngrouped, "grouped convolutions are not built here");
-  constexpr bool AT = GRP == kGroupGradB;           // A operand K-outer, read with the transpose read
-  constexpr bool BK_ROWS = CONV || GRP == kGroupGradA;  // B operand K-contiguous, copied and read like A
+template <typename G, typename T, bool CONV>
+__global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
   using Acc = typename AccType<G::MF>::type;
   constexpr int MF = G::MF;
   constexpr int S = G::ST;
@@ -466,6 +439,28 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / G::WN, wc = wave % G::WN;
+
+  // -- block -> tile.  Workgroups are dealt to the 8 XCDs round-robin; remap
+  // so that each XCD gets a contiguous run of tiles, ordered in groups of
+  // group_m tile rows so that the run shares A and B panels in its L2.
+  const int nblk = gridDim.x, bid = blockIdx.x;
+  const int xcd = bid & 7, local = bid >> 3;
+  const int per = nblk >> 3, extra = nblk & 7;
+  const int t = xcd < extra ? xcd * (per + 1) + local : extra * (per + 1) + (xcd - extra) * per + local;
+  const int tiles_mn = p.tiles_m * p.tiles_n;
+  const int bzs = t / tiles_mn;  // (batch entry or conv tile) * splits + K range
+  const int tt = t - bzs * tiles_mn;
+  const int split = bzs % p.splits, bz = bzs / p.splits;
+  const int span = p.group_m * p.tiles_n;
+  const int first_m = (tt / span) * p.group_m;
+  const int gm = min(p.tiles_m - first_m, p.group_m);
+  const int in_g = tt - (tt / span) * span;
+  const int tm = first_m + in_g % gm, tn = in_g / gm;
+  const int m0 = tm * G::BM, n0 = tn * G::BN;
+  const int M = p.M;
+  // this block's K range [kbeg, kbeg + K) (K == 0 for a range past the end)
+  const int kbeg = split * p.k_split;
+  const int K = max(0, min(p.k_split, p.K - kbeg));
   const int lda = p.lda;
 
   // -- convolution: this block's tile (images, output rows, output
@@ -501,12 +496,11 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
   // GEMM: rows [m0, M), columns [kbeg, kbeg + K) of each (rows past the last
   // one read as zero).  conv: rows [m0, M) whole; a K tile's columns come
   // from the tap cursor (below)
-  const T *Ab = reinterpret_cast<const T *>(p.A) +
-                (AT ? int64_t(kbeg) * lda + m0
-                    : (CONV || GRP ? 0 : int64_t(bz) * p.batch_stride_a) + int64_t(m0) * lda + (CONV ? 0 : kbeg));
+  const T *Ab = reinterpret_cast<const T *>(p.A) + (CONV ? 0 : int64_t(bz) * p.batch_stride_a) + int64_t(m0) * lda +
+                (CONV ? 0 : kbeg);
   const int a_rows = min(G::BM, M - m0);
   const uint32_t a_range =
-      (a_rows > 0 && K > 0) ? (AT ? (uint32_t(K) * uint32_t(lda) - uint32_t(m0)) * 2u : CONV ? uint32_t(a_rows) * uint32_t(lda) * 2u
+      (a_rows > 0 && K > 0) ? (CONV ? uint32_t(a_rows) * uint32_t(lda) * 2u
                                     : (uint32_t(a_rows - 1) * uint32_t(lda) + uint32_t(K)) * 2u)
                             : 0u;
   const i32x4 rsA4 = buffer_rsrc(Ab, a_range);
@@ -514,13 +508,8 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
   if constexpr (CONV) {
     // the channel-last input x[Nb][H][W][Cs]
     rsB4 = buffer_rsrc(p.B, uint32_t(p.Nb) * uint32_t(p.H) * uint32_t(p.W) * uint32_t(p.Cs) * 2u);
-  } else if constexpr (GRP == kGroupGradA) {
-    // B's rows are the result's columns
-    const T *Bb = reinterpret_cast<const T *>(p.B) + int64_t(bz) * p.batch_stride_b + int64_t(n0) * p.ldb;
-    const int b_rows = min(G::BN, N - n0);
-    rsB4 = buffer_rsrc(Bb, K > 0 ? (uint32_t(b_rows - 1) * uint32_t(p.ldb) + uint32_t(K)) * 2u : 0u);
   } else {
-    const T *Bb = reinterpret_cast<const T *>(p.B) + (AT ? 0 : int64_t(bz) * p.batch_stride_b) + int64_t(kbeg) * N + n0;
+    const T *Bb = reinterpret_cast<const T *>(p.B) + int64_t(bz) * p.batch_stride_b + int64_t(kbeg) * N + n0;
     // elements [n0, K*N); with K == 0 the range is empty (otherwise n0 < N <= K*N)
     rsB4 = buffer_rsrc(Bb, K > 0 ? (uint32_t(K) * uint32_t(N) - uint32_t(n0)) * 2u : 0u);
   }
@@ -531,19 +520,10 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
 #pragma unroll
   for (int j = 0; j < G::A_LOADS; ++j) {
     int pchunk = (j * G::NW + wave) * 64 + lane;
-    if constexpr (AT) {
-      // chunk (k, lc): elements m0 + 8lc .. +7 of row k
-      constexpr int CM = G::BM / 8;
-      const int k = pchunk / CM, lc = pchunk % CM ^ G::template swz_b<CM>(k);
-      const bool ok = m0 + lc * 8 < M;
-      a_off[j] = ok ? uint32_t(k) * uint32_t(lda) * 2u + uint32_t(lc) * 16u : kOOB;
-      a_kc[j] = ok ? k : (1 << 30);
-    } else {
-      int r = pchunk / G::CA, pc = pchunk % G::CA;
-      int lc = pc ^ G::swz_a(r);
-      a_off[j] = uint32_t(r) * uint32_t(lda) * 2u + uint32_t(lc) * 16u;
-      a_kc[j] = lc * 8;
-    }
+    int r = pchunk / G::CA, pc = pchunk % G::CA;
+    int lc = pc ^ G::swz_a(r);
+    a_off[j] = uint32_t(r) * uint32_t(lda) * 2u + uint32_t(lc) * 16u;
+    a_kc[j] = lc * 8;
   }
   // -- B copy plan.
   // GEMM: B is K x N, N-contiguous; chunk (k, lc) of the stage holds columns
@@ -564,12 +544,7 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
 #pragma unroll
   for (int j = 0; j < G::B_LOADS; ++j) {
     const int pchunk = (j * G::NW + wave) * 64 + lane;
-    if constexpr (GRP == kGroupGradA) {
-      const int r = pchunk / G::CA, lc = pchunk % G::CA ^ G::swz_a(r);
-      const bool ok = n0 + r < N;
-      b_off[j] = ok ? uint32_t(r) * uint32_t(p.ldb) * 2u + uint32_t(lc) * 16u : kOOB;
-      b_k[j] = ok ? lc * 8 : (1 << 30);
-    } else if constexpr (!CONV) {
+    if constexpr (!CONV) {
       int k = pchunk / G::CB, pc = pchunk % G::CB;
       int lc = pc ^ G::swz_b(k);
       bool col_ok = n0 + lc * 8 < N;
@@ -594,9 +569,6 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
     }
   }
 
-  // bytes that A and B advance by for each step of K
-  const uint32_t a_step = AT ? uint32_t(lda) * 2u : 2u;
-  const uint32_t b_step = BK_ROWS ? 2u : uint32_t(N) * 2u;
   const int nk = (K + G::BK - 1) / G::BK;
   const int nfull = K / G::BK;  // K tiles that lie inside K
 
@@ -660,12 +632,12 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
     if (j < G::A_LOADS) {
       lds_void *dst = (lds_void *)(a_slot(sa) + (j * G::NW + wave) * 1024);
       if constexpr (CONV) copy_to_lds16(rsA4, conv_a_ok(k0, j) ? a_off[j] : kOOB, conv_a_soff(), dst);
-      else copy_to_lds16(rsA4, a_off[j], uint32_t(k0) * a_step, dst);
+      else copy_to_lds16(rsA4, a_off[j], uint32_t(k0) * 2u, dst);
     } else {
       const int jb = j - G::A_LOADS;
       lds_void *dst = (lds_void *)(b_slot(sb) + (jb * G::NW + wave) * 1024);
       if constexpr (CONV) copy_to_lds16<true>(rsB4, conv_b_off(k0, jb), 0u, dst);
-      else copy_to_lds16(rsB4, b_off[jb], uint32_t(k0) * b_step, dst);
+      else copy_to_lds16(rsB4, b_off[jb], uint32_t(k0) * uint32_t(N) * 2u, dst);
     }
   };
   // Copy j of any K tile ckt: a full tile as above; the ragged last tile
@@ -680,7 +652,7 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
         if constexpr (CONV) {
           copy_to_lds16(rsA4, conv_a_ok(k0, j) ? a_off[j] : kOOB, conv_a_soff(), dst);
         } else {
-          const uint32_t off = (k0 + a_kc[j] < K) ? a_off[j] + uint32_t(k0) * a_step : kOOB;
+          const uint32_t off = (k0 + a_kc[j] < K) ? a_off[j] + uint32_t(k0) * 2u : kOOB;
           copy_to_lds16(rsA4, off, 0u, dst);
         }
       } else {
@@ -689,7 +661,7 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
         if constexpr (CONV) {
           copy_to_lds16<true>(rsB4, conv_b_off(k0, jb), 0u, dst);
         } else {
-          const uint32_t off = (k0 + b_k[jb] < K) ? b_off[jb] + uint32_t(k0) * b_step : kOOB;
+          const uint32_t off = (k0 + b_k[jb] < K) ? b_off[jb] + uint32_t(k0) * uint32_t(N) * 2u : kOOB;
           copy_to_lds16(rsB4, off, 0u, dst);
         }
       }
@@ -700,14 +672,12 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
   // A: one address per MFMA K step (MFMA tile i adds i*MF rows).
   // B, GEMM: one address per MFMA tile (K step q adds q*FK rows).
   // B, conv (pixel rows, K-contiguous): read like A, one address per K step.
-  constexpr int NFA = AT ? G::TM : G::KSUB;
-  uint32_t fa[NFA];
+  uint32_t fa[G::KSUB];
 #pragma unroll
-  for (int q = 0; q < NFA; ++q)
-    fa[q] = AT ? G::template frag_n_rows<G::BM>(wr * G::WTM + q * MF, lane) : G::frag_k_rows(wr * G::WTM, lane, q);
-  constexpr int NFB = BK_ROWS ? G::KSUB : G::TN;
+  for (int q = 0; q < G::KSUB; ++q) fa[q] = G::frag_k_rows(wr * G::WTM, lane, q);
+  constexpr int NFB = CONV ? G::KSUB : G::TN;
   uint32_t fb[NFB];
-  if constexpr (BK_ROWS) {
+  if constexpr (CONV) {
 #pragma unroll
     for (int q = 0; q < G::KSUB; ++q) fb[q] = G::frag_k_rows(wc * G::WTN, lane, q);
   } else {
@@ -751,21 +721,20 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
     // row of a step reads all of them.  The steps alternate B buffers and
     // every tile starts on buffer 0.
     i16x8 fa_[G::TM], fb_[2][G::TN];
-    // 8 consecutive k of one column of rows of `width` elements: two transpose reads, 4 rows apart
-    auto read_tr = [](const char *p, int width) __attribute__((always_inline)) -> i16x8 {
-      i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p));
-      i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(p + 4 * width * 2));
-      return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    };
     auto read_a = [&](const char *sta, int q, int i) __attribute__((always_inline)) {
-      if constexpr (AT) fa_[i] = read_tr(sta + fa[i] + q * G::FK * G::BM * 2, G::BM);
-      else fa_[i] = *(const lds_i16x8 *)(sta + fa[q] + i * MF * G::BK * 2);
+      fa_[i] = *(const lds_i16x8 *)(sta + fa[q] + i * MF * G::BK * 2);
     };
     auto read_b = [&](const char *stb, int q, int pb, int j) __attribute__((always_inline)) {
-      if constexpr (BK_ROWS) fb_[pb][j] = *(const lds_i16x8 *)(stb + fb[q] + j * MF * G::BK * 2);
-      else fb_[pb][j] = read_tr(stb + fb[j] + q * G::FK * G::BN * 2, G::BN);
+      if constexpr (CONV) {
+        fb_[pb][j] = *(const lds_i16x8 *)(stb + fb[q] + j * MF * G::BK * 2);
+      } else {
+        const char *bp = stb + fb[j] + q * G::FK * G::BN * 2;
+        i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(bp));
+        i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(bp + 4 * G::BN * 2));
+        fb_[pb][j] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+      }
     };
-    constexpr int AREADS = AT ? 2 : 1, BREADS = BK_ROWS ? 1 : 2;  // LDS reads per fragment
+    constexpr int BREADS = CONV ? 1 : 2;  // LDS reads per B fragment
     // outstanding copies at the barrier once the next tile has landed: the
     // plain ring's S-2 younger tiles; the A3 ring's A refill of this tile
     constexpr int WAIT_VM = A3 ? G::A_LOADS : (S - 2) * G::LPW;
@@ -815,7 +784,7 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
 #pragma unroll
             for (int a = a0; a < a1; ++a) read_a(nsa, nq, a);
             // the row's MFMAs with its LDS reads in between, one read after each MFMA
-            constexpr int NRD = BREADS * (b1 - b0) + AREADS * (a1 - a0);
+            constexpr int NRD = BREADS * (b1 - b0) + (a1 - a0);
             [&]<int... U>(std::integer_sequence<int, U...>) __attribute__((always_inline)) {
               ((__builtin_amdgcn_sched_group_barrier(0x008, 1, 0),
                 (U < NRD ? __builtin_amdgcn_sched_group_barrier(0x100, 1, 0) : (void)0)),
@@ -911,7 +880,7 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
 
   // -- epilogue
   if constexpr (!CONV) {
-    const int64_t cbase = GRP == kGroupForward || GRP == kGroupGradA ? 0 : (int64_t(bz) * p.splits + split) * p.batch_stride_c;
+    const int64_t cbase = (int64_t(bz) * p.splits + split) * p.batch_stride_c;
     if (p.out_dtype == TSS_F32)
       store_tile<G, float>(acc, reinterpret_cast<float *>(p.C) + cbase, smem, m0, n0, wave, wr, wc, lane, M, N);
     else if (p.out_dtype == TSS_F16)
@@ -928,101 +897,6 @@ __device__ __forceinline__ void tile_product(const KernelArgs &p, char *smem, in
     else
       store_conv<G, __bf16>(acc, reinterpret_cast<__bf16 *>(p.C), p, m0, n0, wr, wc, lane, nb0, o0, rows_t, q0, cols_t,
                                 N);
-  }
-}
-
-template <typename G, typename T, bool CONV>
-__global__ __launch_bounds__(G::THREADS) void tiled_gemm_kernel(KernelArgs p) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  // -- block -> tile.  Workgroups are dealt to the 8 XCDs round-robin; remap
-  // so that each XCD gets a contiguous run of tiles, ordered in groups of
-  // group_m tile rows so that the run shares A and B panels in its L2.
-  const int t = xcd_run(blockIdx.x, gridDim.x);
-  const int tiles_mn = p.tiles_m * p.tiles_n;
-  const int bzs = t / tiles_mn;  // (batch entry or conv tile) * splits + K range
-  const int tt = t - bzs * tiles_mn;
-  const int split = bzs % p.splits, bz = bzs / p.splits;
-  const int span = p.group_m * p.tiles_n;
-  const int first_m = (tt / span) * p.group_m;
-  const int gm = min(p.tiles_m - first_m, p.group_m);
-  const int in_g = tt - (tt / span) * span;
-  const int tm = first_m + in_g % gm, tn = in_g / gm;
-  // this block's K range [kbeg, kbeg + K) (K == 0 for a range past the end)
-  const int kbeg = split * p.k_split;
-  const int K = max(0, min(p.k_split, p.K - kbeg));
-  tile_product<G, T, CONV>(p, smem, tm * G::BM, tn * G::BN, p.M, K, bz, split, kbeg);
-}
-
-// Grouped products.  The tiles are those of G, 512 threads and one workgroup
-// a CU; where the last round of kCUs tiles has few of them they are cut into
-// pieces, two of 128 x 256 or four of 128 x 128 (an element's sums are the
-// same in any of them).  Half == G: small tiles, all alike.
-constexpr int kCUs = 256;
-
-// Of ragged rows a group's last tile is often less than half full and its
-// empty pieces end at once, so a third more than a round may be launched.
-__host__ __device__ constexpr int tile_pieces(int rest, bool ragged) {
-  const int most = ragged ? kCUs * 4 / 3 : kCUs;
-  return rest * 4 <= most ? 4 : rest * 2 <= most ? 2 : 1;
-}
-
-template <typename G, typename Half, typename Quarter, typename T, int GRP>
-__global__ __launch_bounds__(G::THREADS) void grouped_gemm_kernel(KernelArgs p) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  constexpr bool PIECES = !__is_same(G, Half);
-  constexpr bool RAGGED = GRP != kGroupGradB;
-  static_assert(G::THREADS == Half::THREADS && G::THREADS == Quarter::THREADS, "one launch");
-  static_assert(!PIECES || (Half::BM * 2 == G::BM && Quarter::BM * 2 == G::BM && Half::BN == G::BN &&
-                            Quarter::BN * 2 == G::BN), "pieces of a tile");
-  const int lane = threadIdx.x & 63, bid = blockIdx.x;
-  // only the tiles there are take part; the launch's spare workgroups end here
-  const int n = (RAGGED ? int(count_group_tiles<G::BM>(p.sizes, p.groups, p.M, lane)) : p.groups * p.tiles_m) * p.tiles_n;
-  const int whole = PIECES ? n / kCUs * kCUs : n, rest = n - whole;
-  const int pieces = PIECES ? tile_pieces(rest, RAGGED) : 1;
-  if (bid >= whole + rest * pieces) return;
-  // RAGGED: the XCDs get runs of equal length.  GradB's tiles cost as much as
-  // their group has rows, so there each group is dealt over the XCDs (given
-  // whole groups, the XCD of the largest one held up the others: 365 -> 244 us
-  // on 16384 rows in 8 uneven groups, K 4096, N 2048).
-  int id = bid, part = 0;
-  if (bid >= whole) {
-    const int x = RAGGED ? xcd_run(bid - whole, rest * pieces) : bid - whole;
-    id = whole + x / pieces;
-    part = x % pieces;
-  } else if constexpr (RAGGED) {
-    id = xcd_run(bid, whole);
-  }
-  int m0, n0, M = p.M, K, bz, kbeg = 0;
-  if constexpr (RAGGED) {
-    // one tile row after the other: the column tiles of a group's rows are
-    // neighbours in an XCD's run
-    const int tm = id / p.tiles_n;
-    const GroupTile g = find_group_tile<G::BM>(p.sizes, p.groups, p.M, tm, lane);
-    m0 = g.row0;
-    n0 = (id - tm * p.tiles_n) * G::BN;
-    M = g.row_end;
-    const bool none = g.group == p.groups;  // rows of no group
-    K = none ? 0 : p.K;
-    bz = none ? 0 : g.group;
-  } else {
-    const int mn = p.tiles_m * p.tiles_n;
-    bz = id / mn;
-    const int in = xcd_run(id - bz * mn, mn), span = p.group_m * p.tiles_n, first = in / span * p.group_m;
-    const int gm = min(p.tiles_m - first, p.group_m), r = in % span;
-    m0 = (first + r % gm) * G::BM;
-    n0 = r / gm * G::BN;
-    const GroupTile g = group_rows(p.sizes, p.groups, p.rows_total, bz, lane);
-    kbeg = g.row0;
-    K = g.row_end - g.row0;
-  }
-  if (!PIECES || bid < whole || pieces == 1) {
-    tile_product<G, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
-  } else if constexpr (PIECES) {
-    m0 += (pieces == 2 ? part : part / 2) * Half::BM;
-    if (pieces == 4) n0 += part % 2 * Quarter::BN;
-    if (m0 >= M || n0 >= p.N) return;
-    if (pieces == 2) tile_product<Half, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
-    else tile_product<Quarter, T, false, GRP>(p, smem, m0, n0, M, K, bz, 0, kbeg);
   }
 }
 

@@ -7,6 +7,7 @@
 
 #include "../../include/tss.h"
 #include "gemm_kernel.h"
+#include "groups.h"
 
 namespace tss {
 

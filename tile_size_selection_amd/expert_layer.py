@@ -148,7 +148,7 @@ def main():
     leaves = [t.float().requires_grad_() for t in (x, norm, w1, w2)]
     out, h = reference(leaves[0], residual.float(), *leaves[1:], expert, weight)
     grads = torch.autograd.grad([out, h], leaves, [dout.float(), dh.float()])
-    off = lambda got, want: float((got.float() - want).norm() / want.norm())  # noqa: E731
+    off = lambda got, want: float((got.float() - want.detach()).norm() / want.detach().norm())  # noqa: E731
     out8, _ = forward_fp8(x, residual, w8, r)
     got, _, saved = forward(x, residual, norm, w1, w2, r)
     back = backward(dout, dh, norm, w1, w2, r, saved)
