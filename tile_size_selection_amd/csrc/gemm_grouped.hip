@@ -184,7 +184,8 @@ hipError_t launch(GroupedArgs &a, hipStream_t s, int32_t *status) {
 // tiles put more of their loads in flight.  Forward, E = 32, K = N = 2048,
 // 64 x 64 against 256 x 256 tiles: 16 rows a group 57 and 61 us, 64 rows 73
 // and 63, 256 rows 181 and 99; where the small ones fit the chip at once, 78
-// rows in 25 groups, K = 2208, N = 640: 22 and 38.
+// rows in 25 groups, K = 2208, N = 640: 22 and 38; 300 rows in 2, K = 4096, N =
+// 1024: 19 and 29; 323 rows in 3, K = 2016, N = 1952, 558 small tiles: 27 and 21.
 template <typename T, int GRP>
 hipError_t launch_rows(GroupedArgs &a, hipStream_t s, int32_t *status) {
   // The kernel for few rows reads 3/16 of a byte for each of T K N from L2, at
@@ -194,7 +195,8 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s, int32_t *status) {
   const int64_t rows64 = a.M / 64 + a.groups, tiles64 = (rows64 < a.M ? rows64 : a.M) * ((int64_t(a.N) + 63) / 64);
   if (tiles64 <= 2 * kCUs && int64_t(a.M) * a.N <= int64_t(1) << 17) return launch_few<T, GRP>(a, s, status);
   const int64_t rows = a.M / a.groups;  // of an average group
-  if (rows <= 32 || (rows <= 128 && tiles64 <= 3 * kCUs)) return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
+  if (rows <= 32 || tiles64 <= (rows <= 128 ? 3 * kCUs : 7 * kCUs / 4))
+    return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
   return launch<Tile256, Piece256, Piece128, T, GRP>(a, s, status);
 }
 
