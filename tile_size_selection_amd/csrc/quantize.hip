@@ -3,7 +3,7 @@
 //
 //   v = x,  or  v = silu(gate) up  with gate | up the two halves of a row of x
 //   scale = max(largest |v| of the block, 1e-30) / largest value of the type
-//   q = v / scale, rounded to nearest even
+//   q = v / scale, rounded to nearest even (gated, 1 x 128: as in 64 bits)
 //
 // scale is K-block-major, scale[column block][row or row block]: the matrix
 // products read the scales of one step of K for consecutive rows.
@@ -17,19 +17,15 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// g / (1 + exp(-g)), to about an ulp: exp(-g) = 2^t with t = -g log2(e) in two
-// parts (the rounding of the product alone would cost |g| ulps), and the
-// quotient's reciprocal corrected once.  Where exp is 0 or has overflowed to
-// infinity the corrections are left out: the reciprocal is 1 or 0.
+// g / (1 + exp(-g)).  The argument of 2^t is off by half its ulp, so for g above
+// -22 the result is off by at most 16 units of fp32 (4 near 0); below about -88
+// exp overflows to infinity, and the result is its limit 0.  Two corrections
+// (t in two parts, the reciprocal's remainder) would make it one unit for 40
+// of the 124 vector cycles that an element then takes: 41 us against 36 at
+// 16400 x 2048, bf16.  Where 16 units could matter they are computed away
+// (quantize_rows_kernel).
 __device__ __forceinline__ float silu(float g) {
-  constexpr float c = -1.44269502162933349609f, c_low = -1.92596299112661746887e-8f;  // -log2(e) in two parts
-  const float t = g * c;
-  const float low = __builtin_fmaf(g, c_low, __builtin_fmaf(g, c, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  const bool inside = e > 0.0f && e < __builtin_inff();
-  const float d = 1.0f + (inside ? __builtin_fmaf(e * 0.693147180559945309f, low, e) : e);
-  const float r = __builtin_amdgcn_rcpf(d);
-  return g * (inside ? __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r) : r);
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
 }
 
 // v of 8 columns; the gated form reads the second half of the row too.
@@ -57,6 +53,29 @@ struct Source {
   }
 };
 
+// How far a quotient's low 20 (e4m3) or 21 (e5m2) bits, the part that rounding
+// takes off a normal value, are past kNear units of fp32 below their half: at
+// most kNearSpan within kNear units of a rounding border.
+constexpr uint32_t kNear = 16;
+template <typename Q>
+constexpr int kKeptBits = __is_same(Q, E4M3) ? 12 : 11;
+template <typename Q>
+constexpr uint32_t kNearSpan = (2 * kNear) << kKeptBits<Q>;
+template <typename Q>
+__device__ __forceinline__ uint32_t past_border(float f) {
+  return (__builtin_bit_cast(uint32_t, f) << kKeptBits<Q>) - (((1u << (31 - kKeptBits<Q>)) - kNear) << kKeptBits<Q>);
+}
+
+template <typename T>
+__device__ __forceinline__ float pick(const Raw8<T> &r, int i) {
+  float f[8], x;
+  widen8(r, f);
+  x = f[0];
+#pragma unroll
+  for (int j = 1; j < 8; ++j) x = i == j ? f[j] : x;
+  return x;
+}
+
 // 1 x 128 blocks.  16 lanes hold a block; a workgroup takes 16 rows (so that
 // it writes 16 neighbouring scales) and kBlocks blocks of each, whose loads
 // are all in flight before the first is used.
@@ -77,6 +96,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(int rows, int d
     if (row < rows && col < d) src[c].load(xrow, d, col);
     else src[c].clear();
   }
+  uint32_t again = 0;
 #pragma unroll
   for (int c = 0; c < kBlocks; ++c) {
     const int col = col0 + c * kScaleBlock;
@@ -85,9 +105,65 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(int rows, int d
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max_abs(amax, v[i]);
     const BlockScale<Q> s(max16(amax));
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = GATED ? v[i] * s.inv : s.quotient(v[i]);
+    if constexpr (GATED) {
+      uint32_t least = ~0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) least = min(least, past_border<Q>(f[i]));
+      again |= uint32_t(least <= kNearSpan<Q>) << c;
+    }
     if (row < rows && col < d) {
-      *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = pack8(v, s);
+      *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = round8<Q>(f);
       if (threadIdx.x % 16 == 0) scale[int64_t(col / kScaleBlock) * rows + row] = s.scale;
+    }
+  }
+  if constexpr (GATED) {
+    // The values are computed, and up to 16 units of fp32 off.  Where that could
+    // round one the other way (one value in 30000) it is computed again in 64
+    // bits, as is the value that sets the scale, from memory, once the
+    // registers of the others are free.  A block with an infinity or a NaN
+    // keeps its fp32 results.
+#pragma unroll 1
+    for (int c = 0; c < kBlocks; ++c) {
+      if (!__any(again >> c & 1)) continue;
+      const int col = col0 + c * kScaleBlock;
+      Source<T, true> x;
+      if (row < rows && col < d) x.load(xrow, d, col);
+      else x.clear();
+      auto exact = [&](int i) __attribute__((always_inline)) {
+        const double g = pick(x.a, i);
+        return g / (1.0 + exp(-g)) * double(pick(x.b, i));
+      };
+      float v[8], f[8], amax = 0;
+      x.values(v);
+      int most = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        most = __builtin_fabsf(v[i]) > amax ? i : most;
+        amax = max_abs(amax, v[i]);
+      }
+      const BlockScale<Q> s(max16(amax));
+      uint32_t near = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        f[i] = v[i] * s.inv;
+        near |= uint32_t(past_border<Q>(f[i]) <= kNearSpan<Q>) << i;
+      }
+      double top = fmax(fabs(exact(most)), double(kSmallestAmax));
+#pragma unroll
+      for (int m = 1; m < 16; m *= 2) top = fmax(top, __shfl_xor(top, m));
+      const double inv = double(kLargest<Q>) / top;
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        if (!__any(near >> i & 1)) continue;
+        const float t = float(exact(i) * inv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = i == j && (near >> i & 1) ? t : f[j];
+      }
+      if (row < rows && col < d && s.scale < __builtin_inff())
+        *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = round8<Q>(f);
     }
   }
 }

@@ -136,11 +136,9 @@ struct BlockScale {
   }
 };
 
+// 8 quotients, rounded to the type.
 template <typename Q>
-__device__ __forceinline__ u32x2 pack8(const float (&v)[8], const BlockScale<Q> &s) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = s.quotient(v[i]);
+__device__ __forceinline__ u32x2 round8(const float (&f)[8]) {
   u32x2 r;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -155,6 +153,14 @@ __device__ __forceinline__ u32x2 pack8(const float (&v)[8], const BlockScale<Q> 
     r[i] = uint32_t(w);
   }
   return r;
+}
+
+template <typename Q>
+__device__ __forceinline__ u32x2 pack8(const float (&v)[8], const BlockScale<Q> &s) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = s.quotient(v[i]);
+  return round8<Q>(f);
 }
 
 }  // namespace tss
