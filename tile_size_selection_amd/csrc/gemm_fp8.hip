@@ -94,6 +94,10 @@ template <bool A_E5M2, bool B_ROWS, bool GROUPED>
 hipError_t launch_rounds(const Fp8Args &a, int64_t tiles, hipStream_t s) {
   static std::atomic<uint64_t> attr_set{0};
   const int64_t whole = tiles / kCUs * kCUs, rest = tiles - whole;
+  // no pieces: the kernel without them is 2% faster (8192^3: 458 us against 467)
+  if constexpr (!GROUPED)
+    if (rest == 0 || tile_pieces(int(rest), false) == 1)
+      return launch_tile<Tile256, 1, A_E5M2, B_ROWS, false, false>(a, tiles, s);
   const int64_t blocks = whole + (GROUPED ? kCUs * 4 / 3 : rest * tile_pieces(int(rest), false));
   return launch_lds(gemm_fp8_rounds_kernel<Tile256, Piece256, Piece128, A_E5M2, B_ROWS, GROUPED>, attr_set, a, blocks,
                     Tile256::THREADS, kRoundsLds, s);
