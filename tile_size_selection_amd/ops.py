@@ -2,11 +2,13 @@
 and grouped matrix products: argument checks and marshalling only, as in
 api.py; the work is libtss.so's (include/tss.h documents each entry point).
 
+Each call takes stream=, the stream to run on (the current one without it).
 Element types are named 'f16', 'bf16', 'f32', 'e4m3' and 'e5m2'.  Scales of
 8-bit tensors are float32, one for each block of 1 or 128 rows x 128 columns,
 column-block-major: scale[column block][row or row block]."""
 from __future__ import annotations
 
+import functools
 from typing import NamedTuple, Optional, Tuple
 
 from . import _capi as C
@@ -56,19 +58,35 @@ _raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", N
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _call(where: str, fn, tensors, stream, *args):
-    """fn(*args, stream) with the tensors' GPU current; every tensor (None
-    aside) must be on it."""
+def _streamed(f):
+    """f with stream=None or the stream to run on (a torch stream, or a HIP
+    stream's handle).  The stream is made current for the call, so that what
+    is allocated in it belongs to that stream too: a workspace freed on return
+    is reused behind the launch that uses it."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        if stream is None:
+            return f(*args, **kwargs)
+        if not isinstance(stream, torch.cuda.Stream):
+            first = args[0] if args else next(iter(kwargs.values()))
+            stream = torch.cuda.ExternalStream(stream, device=first.device)
+        with torch.cuda.stream(stream):
+            return f(*args, **kwargs)
+    return call
+
+
+def _call(where: str, fn, tensors, *args):
+    """fn(*args, current stream) with the tensors' GPU current; every tensor
+    (None aside) must be on it."""
     index = tensors[0].get_device()
     for t in tensors:
         if t is not None and (t.get_device() != index or index < 0):
             raise ValueError("every tensor must be on the same GPU")
-    handle = _raw_stream(index) if stream is None else getattr(stream, "cuda_stream", stream)
     if index == torch.cuda.current_device():
-        st = fn(*args, handle)
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            st = fn(*args, handle)
+            st = fn(*args, _raw_stream(index))
     if st != C.TSS_OK:
         C.check(st, where)
 
@@ -84,8 +102,9 @@ class RmsNorm(NamedTuple):
     rstd: Optional["torch.Tensor"]   # 1 / sqrt(mean(h^2) + eps), where asked for
 
 
+@_streamed
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype: Optional[str] = None, out=None, scale=None,
-             residual_out=None, rstd=None, stream=None) -> RmsNorm:
+             residual_out=None, rstd=None) -> RmsNorm:
     """h = x + residual (x without one); y = h / sqrt(mean(h^2) + eps) * weight
     over the last dimension of x (rows, d), d a multiple of 8 up to 32768;
     fp32 inside.  out_dtype: x's type (the default) or 'e4m3', with a scale
@@ -114,14 +133,15 @@ def rms_norm(x, weight, residual=None, eps: float = 1e-6, out_dtype: Optional[st
         rstd = None
     elif rstd is not None:
         rstd = _out(None if rstd is True else rstd, "rstd", (rows,), torch.float32, x.device)
-    _call("tss_rms_norm", C.lib().tss_rms_norm, (x, weight, out, residual, scale, residual_out, rstd), stream,
+    _call("tss_rms_norm", C.lib().tss_rms_norm, (x, weight, out, residual, scale, residual_out, rstd),
           rows, d, _DT[dt], x.data_ptr(), _ptr(residual), weight.data_ptr(), eps, _DT[od], out.data_ptr(), _ptr(scale),
           _ptr(residual_out), _ptr(rstd))
     return RmsNorm(out, scale, residual_out, rstd)
 
 
-def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None, workspace=None,
-                      stream=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
+@_streamed
+def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
+                      workspace=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
     """(dx, dweight) of rms_norm from its h (or x, without a residual) and
     rstd: dx = dh + rstd (dy weight - xhat mean(dy weight xhat)) with xhat =
     h rstd, the gradient of both x and residual (dh: the gradient that arrives
@@ -144,14 +164,15 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None, works
         C.check(int(need), "tss_rms_norm_backward_workspace_size")
     workspace = _workspace(workspace, need, dy.device)
     _call("tss_rms_norm_backward", C.lib().tss_rms_norm_backward,
-          (dy, h, weight, rstd, dh, dx, dweight, workspace), stream,
+          (dy, h, weight, rstd, dh, dx, dweight, workspace),
           rows, d, _DT[dt], dy.data_ptr(), h.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _ptr(dh), dx.data_ptr(),
           dweight.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return dx, dweight
 
 
-def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1, out=None, scale=None,
-                 stream=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
+@_streamed
+def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1, out=None,
+                 scale=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
     """(q, scale) of x (rows, d), or with gated of silu(gate) * up where x is
     (rows, 2 d), gate then up: q in 'e4m3' or 'e5m2' with a float32 scale for
     each block of block_rows (1 or 128) x 128, scale[ceil(d / 128)][rows or
@@ -168,7 +189,7 @@ def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1,
         d //= 2
     out = _out(out, "out", (rows, d), _TORCH[fp8], x.device)
     scale = _out(scale, "scale", (_blocks(d), rows if block_rows == 1 else _blocks(rows)), torch.float32, x.device)
-    _call("tss_quantize_fp8", C.lib().tss_quantize_fp8, (x, out, scale), stream,
+    _call("tss_quantize_fp8", C.lib().tss_quantize_fp8, (x, out, scale),
           rows, d, _DT[dt], x.data_ptr(), int(gated), _DT[fp8], block_rows, out.data_ptr(), scale.data_ptr())
     return out, scale
 
@@ -180,7 +201,8 @@ def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
     return int(n)
 
 
-def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, stream=None):
+@_streamed
+def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
     """C = (A sa) @ (B sb)^T for 8-bit A (M, K), e4m3 or e5m2, and B (N, K),
     e4m3, with sa[ceil(K / 128)][M] and sb[ceil(K / 128)][N or ceil(N / 128)];
     out_dtype 'bf16', 'f16' or 'f32' (fp32 sums throughout, at half the rate;
@@ -203,7 +225,7 @@ def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, st
     need = gemm_fp8_workspace_size(M, N, K)
     if need:
         workspace = _workspace(workspace, need, A.device)
-    _call("tss_gemm_fp8", C.lib().tss_gemm_fp8, (A, B, sa, sb, out, workspace), stream,
+    _call("tss_gemm_fp8", C.lib().tss_gemm_fp8, (A, B, sa, sb, out, workspace),
           M, N, K, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), b_rows, out.data_ptr(),
           _DT[out_dtype], _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
@@ -216,7 +238,8 @@ def _groups(sizes) -> int:
     return sizes.shape[0]
 
 
-def gemm_grouped(A, B, sizes, out_dtype: Optional[str] = None, out=None, stream=None):
+@_streamed
+def gemm_grouped(A, B, sizes, out_dtype: Optional[str] = None, out=None):
     """C[rows of group e] = A[rows of e] @ B[e]: A (T, K) sorted by group, B
     (E, K, N), f16 or bf16; sizes (E,) int32 on the GPU, the rows of each
     group (read on the device, so a captured graph follows them).  Rows past
@@ -232,13 +255,14 @@ def gemm_grouped(A, B, sizes, out_dtype: Optional[str] = None, out=None, stream=
         raise ValueError("sizes and B disagree on the number of groups")
     od = _choice(out_dtype or dt, "out_dtype", (dt, "f32"))
     out = _out(out, "out", (T, N), _TORCH[od], A.device)
-    _call("tss_gemm_grouped", C.lib().tss_gemm_grouped, (A, B, sizes, out), stream,
+    _call("tss_gemm_grouped", C.lib().tss_gemm_grouped, (A, B, sizes, out),
           T, E, K, N, _DT[dt], A.data_ptr(), B.data_ptr(), sizes.data_ptr(), out.data_ptr(), _DT[od])
     return out
 
 
+@_streamed
 def gemm_grouped_backward(dC, A, B, sizes, dA=None, dB=None, db_dtype: str = "f32", need_dA: bool = True,
-                          need_dB: bool = True, stream=None):
+                          need_dB: bool = True):
     """(dA, dB) of gemm_grouped: dA[rows of e] = dC[rows of e] @ B[e]^T in A's
     type (rows of no group: zero), dB[e] = A[rows of e]^T @ dC[rows of e] in
     db_dtype ('f32' or A's type; a group without rows: zero).  need_dA or
@@ -259,13 +283,14 @@ def gemm_grouped_backward(dC, A, B, sizes, dA=None, dB=None, db_dtype: str = "f3
         dA = _out(dA, "dA", (T, K), A.dtype, A.device)
     if need_dB:
         dB = _out(dB, "dB", (E, K, N), _TORCH[db_dtype], A.device)
-    _call("tss_gemm_grouped_backward", C.lib().tss_gemm_grouped_backward, (A, B, dC, sizes, dA, dB), stream,
+    _call("tss_gemm_grouped_backward", C.lib().tss_gemm_grouped_backward, (A, B, dC, sizes, dA, dB),
           T, E, K, N, _DT[dt], dC.data_ptr(), A.data_ptr(), B.data_ptr(), sizes.data_ptr(), _ptr(dA), _ptr(dB),
           _DT[db_dtype])
     return dA, dB
 
 
-def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None, stream=None):
+@_streamed
+def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None):
     """C[rows of group e] = (A sa)[rows of e] @ (B[e] sb[e])^T: A (T, K), e4m3
     or e5m2, sorted by group, with sa[ceil(K / 128)][T]; B (E, N, K), e4m3,
     with sb[e][ceil(K / 128)][ceil(N / 128)]; sizes and the rows of no group
@@ -283,7 +308,7 @@ def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None, str
         raise ValueError("sizes and B disagree on the number of groups")
     _choice(out_dtype, "out_dtype", ("bf16", "f16", "f32"))
     out = _out(out, "out", (T, N), _TORCH[out_dtype], A.device)
-    _call("tss_gemm_grouped_fp8", C.lib().tss_gemm_grouped_fp8, (A, B, sa, sb, sizes, out), stream,
+    _call("tss_gemm_grouped_fp8", C.lib().tss_gemm_grouped_fp8, (A, B, sa, sb, sizes, out),
           T, E, K, N, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), sizes.data_ptr(),
           out.data_ptr(), _DT[out_dtype])
     return out
