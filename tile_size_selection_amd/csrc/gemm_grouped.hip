@@ -30,6 +30,8 @@ using Tile64 = Geometry<64, 64, 64, 4, 4, 16>;
 //   loads but leave too few workgroups: 1 row, 6 groups, K = 2048, N = 800:
 //   8.7 us against 6.0.)
 //   GradA: B's rows run along the reduction, and are loaded as fragments.
+// 3 rows in 8 groups, K = N = 2048: 9.5 us (64 x 64 tiles: 11.4); 62 rows in 6,
+// K = 5152, N = 328: 15.9 us (21.1).
 constexpr int kFewTiles = 2, kFewCols = 16 * kFewTiles;
 constexpr int kFewUnroll = 4;  // chunks whose loads a wave has in flight
 

@@ -8,7 +8,9 @@
 // scale is K-block-major, scale[column block][row or row block]: the matrix
 // products read the scales of one step of K for consecutive rows.
 // Memory-bound: an element is read once, kept in registers while its block's
-// maximum is found, and written in 8 bits.
+// maximum is found, and written in 8 bits.  bf16 to e4m3, 16400 x 2048: 17.5 us
+// (5.9 TB/s), gated 36.6 (4.6 TB/s: exp and reciprocal take 20 of it behind the
+// loads); 128 x 128 blocks, 5000 x 8200: 22 us (5.6 TB/s).
 #include "rows.h"
 
 using namespace tss;
