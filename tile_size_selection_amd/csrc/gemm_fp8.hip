@@ -154,6 +154,9 @@ int32_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t n_multiple) {
   return TSS_OK;
 }
 
+// Elements between the partial sums of two ranges: whole 16-byte pieces.
+int64_t slice_elements(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
+
 // K of a range: a multiple of 128; the ranges that hold any.
 void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
   const int64_t kb = (K + 127) / 128, per = (kb + splits - 1) / splits;
@@ -175,7 +178,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
     split_ranges(K, plan_product(M, N, K, exact).splits, &n, &ks);
     most = n > most ? n : most;
   }
-  return most > 1 ? most * M * N * 4 : 0;
+  return most > 1 ? most * slice_elements(M, N) * 4 : 0;
 }
 
 int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const void *A, const void *B, const float *sa,
@@ -206,10 +209,11 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
   if (K) split_ranges(K, pl.splits, &a.splits, &a.k_split);
   const bool split = a.splits > 1;
   if (split) {
-    if (!workspace || workspace_bytes < a.splits * M * N * 4) return TSS_E_ARG;
+    if (!workspace || workspace_bytes < a.splits * slice_elements(M, N) * 4) return TSS_E_ARG;
     if (misaligned(workspace, 16)) return TSS_E_ALIGN;
   }
   a.C = split ? workspace : C;
+  a.c_split = slice_elements(M, N);
   a.out_dtype = split ? TSS_F32 : out_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err;
@@ -219,7 +223,8 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
     err = b_block_rows == 1 ? launch<false, true, false>(a, pl, exact, s, &st) : launch<false, false, false>(a, pl, exact, s, &st);
   if (st != TSS_OK) return st;
   if (err == hipSuccess && split)
-    err = launch_splitk_reduce(static_cast<const float *>(workspace), C, out_dtype, 1, M * N, a.splits, s);
+    err = launch_splitk_reduce(static_cast<const float *>(workspace), C, out_dtype, 1, M * N, a.splits, s,
+                               slice_elements(M, N));
   return err == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 

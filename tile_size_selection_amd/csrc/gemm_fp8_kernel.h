@@ -35,13 +35,14 @@ struct Fp8Args {
   const uint8_t *B;   // [groups][N][K]
   const float *sa;    // [ceil(K / 128)][M]
   const float *sb;    // [groups][ceil(K / 128)][sb_cols]
-  void *C;            // [M][N]; split K: [splits][M][N] fp32
+  void *C;            // [M][N]; split K: fp32 [splits][M][N], the slices c_split elements apart
   const int32_t *sizes;  // grouped: rows of each group
   int32_t M, N, K, groups;
   int32_t sb_cols;    // N, or ceil(N / 128)
   int32_t tiles_m, tiles_n, splits;
   int32_t k_split;    // K of a range, a multiple of 128
   int32_t out_dtype;
+  int64_t c_split;    // split K: a multiple of 4, so that every slice starts on a 16-byte border
 };
 
 // A fragment: the 32 bytes that a lane holds of a block of 128 of K, as they
@@ -158,7 +159,7 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
   return fp8_tile_at<BM, BN, GROUPED>(p, xcd_run(blockIdx.x, n), lane);
 }
 
-// Rows of C that do not start on 16-byte borders (N not a multiple of 8):
+// Rows of C that do not start on 16-byte borders (N not a multiple of 8; C itself does):
 // staged through LDS as in store_tile, but each row at its place within 16
 // bytes of memory, so that whole 16-byte pieces of memory are written from
 // aligned pieces of LDS; the elements of the pieces at a row's ends are
@@ -454,7 +455,7 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
 
   auto store = [&](auto o) __attribute__((always_inline)) {
     using O = decltype(o);
-    O *C = static_cast<O *>(p.C) + int64_t(t.split) * p.M * p.N;
+    O *C = static_cast<O *>(p.C) + t.split * p.c_split;
     if (GROUPED || p.N % 8 == 0)
       store_tile<G, O>(acc, C, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
     else
