@@ -7,7 +7,7 @@ import torch
 
 import tile_size_selection_amd as tss
 import ops_util as U
-from test_ops_plans import SPLIT
+from test_ops_plans import GROUPED, PRODUCTS, SPLIT
 
 pytestmark = pytest.mark.gpu
 
@@ -46,6 +46,70 @@ def check_product(size, a, b_rows, outs=("f32", "bf16", "f16"), **options):
 
 @pytest.mark.parametrize("b_rows", [128, 1])
 @pytest.mark.parametrize("a", ["e4m3", "e5m2"])
-@pytest.mark.parametrize("size", SPLIT)
-def test_gemm_fp8_with_k_in_ranges_is_exact(size, a, b_rows):
+@pytest.mark.parametrize("size", SPLIT + [s for s in PRODUCTS if s not in SPLIT])
+def test_gemm_fp8_is_exact(size, a, b_rows):
     check_product(size, a, b_rows)
+
+
+@pytest.mark.parametrize("a", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("size", [(300, 24, 256), (1500, 1210, 144), (1001, 1001, 4112), (1700, 1704, 272), (2101, 2105, 272)])
+def test_gemm_fp8_takes_every_value(size, a):
+    # a row of A holds one value that is not zero, so each element of C is one product, exact in fp32; the values are
+    # the type's finite codes, subnormals among them
+    M, N, K = size
+    g = U.gen(70)
+    code = (torch.arange(M) % 256).to(torch.uint8).view(U.TYPES[a])
+    code = torch.where(code.float().isfinite(), code.float(), torch.zeros(M))
+    A, B = torch.zeros(M, K), ints(g, (N, K), 2, "e4m3")
+    k = torch.randint(K, (M,), generator=g)
+    A[torch.arange(M), k] = code
+    want = code.double()[:, None] * B.double()[:, k].t()
+    dev = [t.to(CUDA) for t in (A.to(U.TYPES[a]), B, torch.ones(U.blocks(K), M), torch.ones(U.blocks(K), U.blocks(N)))]
+    for out in ("f32", "bf16"):  # (e5m2 passes fp16's largest value)
+        equal(tss.gemm_fp8(*dev, out_dtype=out), want, out)
+
+
+@pytest.mark.parametrize("a", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("case", GROUPED)
+def test_grouped_fp8_is_exact(case, a):
+    T, sizes, K, N = case
+    E, g = len(sizes), U.gen(T + K)
+    A, B = ints(g, (T, K), 3, a), ints(g, (E, N, K), 2, "e4m3")
+    sa, sb = powers(g, U.blocks(K), T), powers(g, E, U.blocks(K), U.blocks(N))
+    at, used = U.spans(sizes, T)
+    C = torch.zeros(T, N, dtype=torch.float64)
+    for e, (i, j) in enumerate(at):
+        C[i:j] = (U.values(A[i:j], sa[:, i:j], 1).to(CUDA) @ U.values(B[e], sb[e], 128).to(CUDA).t().contiguous()).cpu()
+    A[used:] = float("nan")  # rows of no group are not read
+    sa[:, used:] = float("nan")
+    dev = [t.to(CUDA) for t in (A, B, sa, sb)] + [torch.tensor(sizes, dtype=torch.int32, device=CUDA)]
+    for out in ("f32", "bf16", "f16"):
+        got = torch.full((T + 3, N), float("nan"), dtype=U.TYPES[out], device=CUDA)
+        tss.gemm_grouped_fp8(*dev, out_dtype=out, out=got[:T])
+        equal(got[:T], C, out)
+        assert got[T:].isnan().all()
+
+
+def test_thousands_of_groups():
+    T, E, K, N = 3300, 4096, 48, 24
+    g = U.gen(80)
+    sizes = torch.randint(-1, 3, (E,), generator=g, dtype=torch.int32)
+    group = torch.repeat_interleave(torch.arange(E), sizes.clamp(min=0).long())[:T]
+    used = group.numel()
+    assert 2000 < used < T  # about three quarters of a row a group, and rows of none
+    A, B, dC = ints(g, (T, K), 2, "bf16"), ints(g, (E, K, N), 2, "bf16"), ints(g, (T, N), 2, "bf16")
+    picked = B.double()[group]
+    C, dA, dB = torch.zeros(T, N).double(), torch.zeros(T, K).double(), torch.zeros(E, K, N).double()
+    C[:used] = (A[:used].double()[:, :, None] * picked).sum(1)
+    dA[:used] = (dC[:used].double()[:, None, :] * picked).sum(2)
+    dB.index_add_(0, group, A[:used].double()[:, :, None] * dC[:used].double()[:, None, :])
+    dev = [t.to(CUDA) for t in (A, B, dC, sizes)]
+    equal(tss.gemm_grouped(dev[0], dev[1], dev[3], out_dtype="f32"), C, "C")
+    got = tss.gemm_grouped_backward(dev[2], dev[0], dev[1], dev[3])
+    equal(got[0], dA, "dA")
+    equal(got[1], dB, "dB")
+    f8 = torch.float8_e4m3fn
+    ones = lambda *s: torch.ones(*s, device=CUDA)  # noqa: E731
+    got = tss.gemm_grouped_fp8(dev[0].to(f8), dev[1].transpose(1, 2).contiguous().to(f8), ones(1, T), ones(E, 1, 1), dev[3],
+                               out_dtype="f32")
+    equal(got, C, "C of 8 bits")

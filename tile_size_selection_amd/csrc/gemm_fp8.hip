@@ -2,6 +2,7 @@
 #include <atomic>
 
 #include "gemm_fp8_kernel.h"
+#include "plans.h"
 #include "splitk_reduce.h"
 
 using namespace tss;
@@ -18,52 +19,6 @@ using Piece128 = Fp8Geometry<128, 128, 3, 8, 2>;  // also groups of middling siz
 using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;   // fp32 outputs; two workgroups a CU
 using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;     // two workgroups a CU
 constexpr int kRoundsLds = Tile256::LDS_BYTES > Piece256::LDS_BYTES ? Tile256::LDS_BYTES : Piece256::LDS_BYTES;
-
-// How a product is run: by tiles of bm x bn, K in `splits` ranges of their own
-// workgroups and each of them in `sets` of a workgroup's waves; or (bn == 16)
-// by the kernel for few rows.
-struct Plan {
-  int bm, bn, splits, sets = 1;
-};
-
-Plan plan_product(int64_t M, int64_t N, int64_t K, bool exact) {
-  const int64_t kb = (K + 127) / 128;
-  // The kernel for few rows takes about 3.6 us and, every 16 x 16 tile reading
-  // its own rows of both operands from L2, MNK / 8 bytes at 8 TB/s; tiles take
-  // about 5 us and 0.37 a step, or about 10 with K split.  76 x 480 x 3200:
-  // 6.2 against 10.4 us; 64 x 2048 x 2048: 7.2 and 10; 64 x 8192 x 4096: 33 and 13.
-  const int64_t steps100 = 160 + 37 * kb;
-  if (M <= 16 || M * N * K <= 640000 * (steps100 < 700 ? steps100 : 700)) return {16, 16, 1};
-  auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  // One round of 128 x 128 tiles where they fit it (3249 x 1098 x 2384: 20.6 us,
-  // and 27.7 in halves of 256 x 256).
-  const int64_t b128 = blocks(128, 128);
-  if (!exact && b128 >= 160) return b128 <= kCUs ? Plan{128, 128, 1} : Plan{256, 256, 1};
-  if (exact && b128 >= kCUs) return {128, 128, 1};
-  const int64_t b = blocks(64, 128);
-  int64_t s = b >= kCUs ? 1 : kCUs / b;
-  if (s > kb / 8) s = kb / 8;  // at least eight steps of K a range
-  s = s > 8 ? 8 : s < 1 ? 1 : s;
-  // Two sets of waves in a workgroup, where a CU has but one: they shorten the
-  // steps' chains of waits (1620 x 776 x 3584: 17.0 -> 15.2 us; fp32 output,
-  // 1236 x 1382 x 5008: 37.8 -> 29.2) but cost 1 to 2 us at the ends (968 x
-  // 2052 x 864: 12.1 -> 18.5).
-  const bool sets = b * s <= kCUs && kb / s >= (exact ? 8 : 16);
-  return {64, 128, int(s), sets ? 2 : 1};
-}
-
-// Small tiles where they leave CUs free anyway (581 rows in 3 groups, K 2240, N
-// 792: 13.9 us against 16.0 and 15.5 with 128 x 128 and 256 x 256) and for few
-// rows a group; large ones from 192 (128 rows a group, E = 32, K = 4096, N =
-// 2048: 95, 85 and 92 us with the three tiles; 256 rows: 155, 141 and 111).
-Plan plan_grouped(int64_t T, int64_t N, int64_t K, int64_t E, bool exact) {
-  const int64_t rows = T / E;  // of an average group
-  const int64_t tiles64 = (T / 64 + E < T ? T / 64 + E : T) * ((N + 127) / 128), a_reads = (N + 15) / 16 * T * K;
-  if (K > 0 && tiles64 < kCUs && a_reads <= int64_t(40) << 20) return {16, 16, 1};
-  if (rows <= 64 || tiles64 <= kCUs) return {64, 128, 1, tiles64 <= kCUs && K >= (exact ? 1024 : 4096) ? 2 : 1};
-  if (rows <= 192 || exact) return {128, 128, 1};
-  return {256, 256, 1};
-}
 
 // Dynamic LDS above 64 KiB needs an attribute per kernel and device: set on the first launch there.
 template <typename Kernel>
@@ -114,7 +69,7 @@ hipError_t launch_rows(const Fp8Args &a, int64_t blocks, hipStream_t s) {
 }
 
 template <bool A_E5M2, bool B_ROWS, bool GROUPED>
-hipError_t launch(Fp8Args &a, const Plan &pl, bool exact, hipStream_t s, int32_t *status) {
+hipError_t launch(Fp8Args &a, const ProductPlan &pl, bool exact, hipStream_t s, int32_t *status) {
   a.tiles_n = int32_t((a.N + pl.bn - 1) / pl.bn);
   const int64_t tiles_m = GROUPED ? max_group_tiles(a.M, a.groups, pl.bm) : (int64_t(a.M) + pl.bm - 1) / pl.bm;
   a.tiles_m = int32_t(tiles_m);
@@ -154,16 +109,6 @@ int32_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t n_multiple) {
   return TSS_OK;
 }
 
-// Elements between the partial sums of two ranges: whole 16-byte pieces.
-int64_t slice_elements(int64_t M, int64_t N) { return (M * N + 3) / 4 * 4; }
-
-// K of a range: a multiple of 128; the ranges that hold any.
-void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
-  const int64_t kb = (K + 127) / 128, per = (kb + splits - 1) / splits;
-  *k_split = int32_t(per * 128);
-  *n = int32_t((kb + per - 1) / per);
-}
-
 }  // namespace
 
 extern "C" {
@@ -193,7 +138,7 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
   if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(sa, 4) || misaligned(sb, 4))
     return TSS_E_ALIGN;
   const bool exact = out_dtype == TSS_F32;
-  const Plan pl = K ? plan_product(M, N, K, exact) : Plan{64, 128, 1};
+  const ProductPlan pl = K ? plan_product(M, N, K, exact) : ProductPlan{64, 128, 1};
   Fp8Args a{};
   a.A = static_cast<const uint8_t *>(A);
   a.B = static_cast<const uint8_t *>(B);
@@ -257,7 +202,7 @@ int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t
   a.out_dtype = out_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool exact = out_dtype == TSS_F32;
-  const Plan pl = plan_grouped(T, N, K, E, exact);
+  const ProductPlan pl = plan_grouped_fp8(T, N, K, E, exact);
   const hipError_t err = a_dtype == TSS_E5M2 ? launch<true, false, true>(a, pl, exact, s, &st)
                                              : launch<false, false, true>(a, pl, exact, s, &st);
   if (st != TSS_OK) return st;

@@ -3,6 +3,7 @@
 #include <atomic>
 
 #include "grouped_kernel.h"
+#include "plans.h"
 
 using namespace tss;
 
@@ -182,32 +183,18 @@ hipError_t launch(GroupedArgs &a, hipStream_t s, int32_t *status) {
   return hipGetLastError();
 }
 
-// Few rows in an average group: the groups' weights are the cost, and small
-// tiles put more of their loads in flight.  Forward, E = 32, K = N = 2048,
-// 64 x 64 against 256 x 256 tiles: 16 rows a group 57 and 61 us, 64 rows 73
-// and 63, 256 rows 181 and 99; where the small ones fit the chip at once, 78
-// rows in 25 groups, K = 2208, N = 640: 22 and 38; 300 rows in 2, K = 4096, N =
-// 1024: 19 and 29; 323 rows in 3, K = 2016, N = 1952, 558 small tiles: 27 and 21.
 template <typename T, int GRP>
 hipError_t launch_rows(GroupedArgs &a, hipStream_t s, int32_t *status) {
-  // The kernel for few rows reads 3/16 of a byte for each of T K N from L2, at
-  // 5.5 TB/s, against 0.2 us for each 64 of K where the small tiles leave CUs
-  // free: T N up to about 1e5.  162 rows in 2 groups, K = 2560, N = 344: 10.1
-  // and 13.1 us; 64 rows in 32 groups, K = 4096, N = 2048: 89 and 83.
-  const int64_t rows64 = a.M / 64 + a.groups, tiles64 = (rows64 < a.M ? rows64 : a.M) * ((int64_t(a.N) + 63) / 64);
-  if (tiles64 <= 2 * kCUs && int64_t(a.M) * a.N <= int64_t(1) << 17) return launch_few<T, GRP>(a, s, status);
-  const int64_t rows = a.M / a.groups;  // of an average group
-  if (rows <= 32 || tiles64 <= (rows <= 128 ? 3 * kCUs : 7 * kCUs / 4))
-    return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
-  return launch<Tile256, Piece256, Piece128, T, GRP>(a, s, status);
+  switch (plan_grouped_rows(a.M, a.N, a.groups)) {
+    case 16: return launch_few<T, GRP>(a, s, status);
+    case 64: return launch<Tile64, Tile64, Tile64, T, GRP>(a, s, status);
+    default: return launch<Tile256, Piece256, Piece128, T, GRP>(a, s, status);
+  }
 }
 
-// With few rows to reduce over the writes are the cost.  E = 32, K = 4096,
-// N = 2048, 2 rows a group: 128 x 128 tiles 165 us, 256 x 256 178; K = N =
-// 2048, 64 rows a group 99 and 100, 256 rows 143 and 136.
 template <typename T>
 hipError_t launch_grad_b(GroupedArgs &a, hipStream_t s, int32_t *status) {
-  if (a.rows_total / a.groups <= 64) return launch<Tile128, Tile128, Tile128, T, kGroupGradB>(a, s, status);
+  if (plan_grad_b(a.rows_total, a.groups) == 128) return launch<Tile128, Tile128, Tile128, T, kGroupGradB>(a, s, status);
   return launch<Tile256, Piece256, Piece128, T, kGroupGradB>(a, s, status);
 }
 

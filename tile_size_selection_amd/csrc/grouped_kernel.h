@@ -16,6 +16,7 @@
 #pragma once
 #include "gemm_kernel.h"
 #include "groups.h"
+#include "plans.h"
 
 namespace tss {
 
@@ -396,15 +397,6 @@ __device__ __forceinline__ void grouped_tile_product(const GroupedArgs &p, char 
 // a CU; where the last round of kCUs tiles has few of them they are cut into
 // pieces, two of 128 x 256 or four of 128 x 128 (an element's sums are the
 // same in any of them).  Half == G: small tiles, all alike.
-constexpr int kCUs = 256;
-
-// Of ragged rows a group's last tile is often less than half full and its
-// empty pieces end at once, so a third more than a round may be launched.
-__host__ __device__ constexpr int tile_pieces(int rest, bool ragged) {
-  const int most = ragged ? kCUs * 4 / 3 : kCUs;
-  return rest * 4 <= most ? 4 : rest * 2 <= most ? 2 : 1;
-}
-
 template <typename G, typename Half, typename Quarter, typename T, int GRP>
 __global__ __launch_bounds__(G::THREADS) void grouped_gemm_kernel(GroupedArgs p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
