@@ -623,7 +623,11 @@ int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d);
 /*
  * q (rows x d in fp8 = TSS_E4M3 or TSS_E5M2) and its scales from x, with
  * blocks of block_rows (1 or 128) x 128.  gated: x has rows of 2 d elements,
- * gate then up, and silu(gate) * up is quantised.  x and q 16-byte aligned.
+ * gate then up, and silu(gate) * up is quantised: silu in fp32, off by 1.22
+ * |gate| + 8 halves of a unit for negative gates, 8 for positive ones, and 0
+ * for gates below about -87.  Blocks of 1 x 128 round as the value and scale
+ * in 64 bits do; their stored scale, and blocks of 128 x 128, keep that error.
+ * x and q 16-byte aligned.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
 int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, int32_t fp8,

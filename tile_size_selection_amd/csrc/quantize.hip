@@ -3,13 +3,13 @@
 //
 //   v = x,  or  v = silu(gate) up  with gate | up the two halves of a row of x
 //   scale = max(largest |v| of the block, 1e-30) / largest value of the type
-//   q = v / scale, rounded to nearest even (gated, 1 x 128: as in 64 bits)
+//   q = v / scale, rounded to nearest even (gated, 1 x 128: as in 64 bits, for gates above -87)
 //
 // scale is K-block-major, scale[column block][row or row block]: the matrix
 // products read the scales of one step of K for consecutive rows.
 // Memory-bound: an element is read once, kept in registers while its block's
 // maximum is found, and written in 8 bits.  bf16 to e4m3, 16400 x 2048: 17.5 us
-// (5.9 TB/s), gated 36.6 (4.6 TB/s: exp and reciprocal take 20 of it behind the
+// (5.9 TB/s), gated 38.3 (4.4 TB/s: exp and reciprocal take 20 of it behind the
 // loads); 128 x 128 blocks, 5000 x 8200: 22 us (5.6 TB/s).
 #include "rows.h"
 
@@ -19,13 +19,14 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// g / (1 + exp(-g)).  The argument of 2^t is off by half its ulp, so for g above
-// -22 the result is off by at most 16 units of fp32 (4 near 0); below about -88
-// exp overflows to infinity, and the result is its limit 0.  Two corrections
-// (t in two parts, the reciprocal's remainder) would make it one unit for 40
-// of the 124 vector cycles that an element then takes: 41 us against 36 at
-// 16400 x 2048, bf16.  Where 16 units could matter they are computed away
-// (quantize_rows_kernel).
+// g / (1 + exp(-g)).  The argument of 2^t is off by half its ulp and by the
+// constant's, so a negative g's result is off by 1.22 |g| + 8 halves of a unit
+// of fp32 (2^-24 of itself), a positive one's by 8; below about -87 the
+// reciprocal is less than the smallest normal number, and the result 0.  Two
+// corrections (t in two parts, the reciprocal's remainder) would make it one
+// unit for 40 of the 124 vector cycles that an element then takes: 41 us
+// against 38 at 16400 x 2048, bf16.  Where the error could matter it is
+// computed away (quantize_rows_kernel).
 __device__ __forceinline__ float silu(float g) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504088896340736f));
 }
@@ -53,20 +54,44 @@ struct Source {
       }
     }
   }
+  // the least of the lane's gates, or 0
+  __device__ __forceinline__ float least_gate() const {
+    float g[8], least = 0;
+    widen8(a, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) least = fminf(least, g[i]);
+    return least;
+  }
 };
 
-// How far a quotient's low 20 (e4m3) or 21 (e5m2) bits, the part that rounding
-// takes off a normal value, are past kNear units of fp32 below their half: at
-// most kNearSpan within kNear units of a rounding border.
-constexpr uint32_t kNear = 16;
+// The 8-bit values that 8 gated quotients can have, v * inv being off by at
+// most the errors of the value and of the block's largest one (silu's, for
+// gates from `gate` up) and a few roundings: the lower and the upper one in
+// magnitude.  They differ where a rounding border lies between.
 template <typename Q>
-constexpr int kKeptBits = __is_same(Q, E4M3) ? 12 : 11;
-template <typename Q>
-constexpr uint32_t kNearSpan = (2 * kNear) << kKeptBits<Q>;
-template <typename Q>
-__device__ __forceinline__ uint32_t past_border(float f) {
-  return (__builtin_bit_cast(uint32_t, f) << kKeptBits<Q>) - (((1u << (31 - kKeptBits<Q>)) - kNear) << kKeptBits<Q>);
-}
+struct Rounded {
+  u32x2 low, high;
+  __device__ __forceinline__ Rounded(const float (&v)[8], float inv, float gate) {
+    constexpr float half_unit = 0x1p-24f;
+    const float e = __builtin_fmaf(fmaxf(gate, -88.0f), -2.44f * half_unit, 21 * half_unit);
+    const float below = __builtin_fmaf(-e, inv, inv), above = __builtin_fmaf(e, inv, inv);
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[i] * below;
+    low = round8<Q>(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = v[i] * above;
+    high = round8<Q>(f);
+  }
+  __device__ __forceinline__ bool open() const { return ((low[0] ^ high[0]) | (low[1] ^ high[1])) != 0; }
+  // bit i: value i is open
+  __device__ __forceinline__ uint32_t which() const {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r |= uint32_t(((low[i / 4] ^ high[i / 4]) >> (i % 4 * 8) & 0xff) != 0) << i;
+    return r;
+  }
+};
 
 template <typename T>
 __device__ __forceinline__ float pick(const Raw8<T> &r, int i) {
@@ -107,23 +132,22 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(int rows, int d
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = max_abs(amax, v[i]);
     const BlockScale<Q> s(max16(amax));
-    float f[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = GATED ? v[i] * s.inv : s.quotient(v[i]);
+    u32x2 w;
     if constexpr (GATED) {
-      uint32_t least = ~0u;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) least = min(least, past_border<Q>(f[i]));
-      again |= uint32_t(least <= kNearSpan<Q>) << c;
+      const Rounded<Q> r(v, s.inv, min16(src[c].least_gate()));
+      again |= uint32_t(r.open()) << c;
+      w = r.low;
+    } else {
+      w = pack8(v, s);
     }
     if (row < rows && col < d) {
-      *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = round8<Q>(f);
+      *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = w;
       if (threadIdx.x % 16 == 0) scale[int64_t(col / kScaleBlock) * rows + row] = s.scale;
     }
   }
   if constexpr (GATED) {
-    // The values are computed, and up to 16 units of fp32 off.  Where that could
-    // round one the other way (one value in 30000) it is computed again in 64
+    // The values are computed, and some units of fp32 off.  Where that could
+    // round one the other way (one value in 20000) it is computed again in 64
     // bits, as is the value that sets the scale, from memory, once the
     // registers of the others are free.  A block with an infinity or a NaN
     // keeps its fp32 results.
@@ -138,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(int rows, int d
         const double g = pick(x.a, i);
         return g / (1.0 + exp(-g)) * double(pick(x.b, i));
       };
-      float v[8], f[8], amax = 0;
+      float v[8], amax = 0;
       x.values(v);
       int most = 0;
 #pragma unroll
@@ -147,25 +171,24 @@ __global__ __launch_bounds__(kThreads) void quantize_rows_kernel(int rows, int d
         amax = max_abs(amax, v[i]);
       }
       const BlockScale<Q> s(max16(amax));
-      uint32_t near = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        f[i] = v[i] * s.inv;
-        near |= uint32_t(past_border<Q>(f[i]) <= kNearSpan<Q>) << i;
-      }
+      const Rounded<Q> r(v, s.inv, min16(x.least_gate()));
+      const uint32_t open = r.which();
+      u32x2 w = r.low;
       double top = fmax(fabs(exact(most)), double(kSmallestAmax));
 #pragma unroll
       for (int m = 1; m < 16; m *= 2) top = fmax(top, __shfl_xor(top, m));
       const double inv = double(kLargest<Q>) / top;
 #pragma unroll 1
       for (int i = 0; i < 8; ++i) {
-        if (!__any(near >> i & 1)) continue;
+        if (!__any(open >> i & 1)) continue;
         const float t = float(exact(i) * inv);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = i == j && (near >> i & 1) ? t : f[j];
+        const float one[8] = {t, t, t, t, t, t, t, t};
+        const uint32_t at = open >> i & 1 ? 0xffu << (i % 4 * 8) : 0u, b = round8<Q>(one)[0] & at;
+        w[0] = i < 4 ? (w[0] & ~at) | b : w[0];
+        w[1] = i < 4 ? w[1] : (w[1] & ~at) | b;
       }
       if (row < rows && col < d && s.scale < __builtin_inff())
-        *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = round8<Q>(f);
+        *reinterpret_cast<u32x2 *>(q + int64_t(row) * d + col) = w;
     }
   }
 }

@@ -102,6 +102,13 @@ __device__ __forceinline__ float max16(float v) {
   return __builtin_elementwise_maximum(v, rot16<1>(v));
 }
 
+__device__ __forceinline__ float min16(float v) {
+  v = fminf(v, rot16<8>(v));
+  v = fminf(v, rot16<4>(v));
+  v = fminf(v, rot16<2>(v));
+  return fminf(v, rot16<1>(v));
+}
+
 __device__ __forceinline__ float sum64(float v) {
   v += rot16<8>(v);
   v += rot16<4>(v);
