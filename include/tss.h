@@ -54,6 +54,8 @@ enum {
   TSS_F16 = 1, TSS_BF16 = 2, TSS_F32 = 3,
   TSS_E4M3 = 4, TSS_E5M2 = 5  /* 8 bits, OCP: largest finite values 448 and 57344 */
 };
+/* Added to the out_dtype of an 8-bit product: sums in fp32 throughout (TSS_F32 has them without it). */
+enum { TSS_F32_SUMS = 0x100 };
 
 /* ---- instruction shapes (C3) -------------------------------------------- */
 enum {
@@ -640,10 +642,13 @@ int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, 
  * sa[ceil(K / 128)][M]; B is N x K (TSS_E4M3) with sb[ceil(K / 128)][N]
  * (b_block_rows 1) or sb[ceil(K / 128)][ceil(N / 128)] (128); C is M x N,
  * out_dtype TSS_F16, TSS_BF16 or TSS_F32.  Each block of 128 of K is summed by
- * the matrix cores, the blocks' sums are scaled and added in fp32.  For an
- * fp32 output the blocks are summed in fp32 too; for a 16-bit one the 8-bit
- * matrix instruction sums them, which is twice as fast and about 1.7e-5 of
- * the result's norm off.
+ * the matrix cores, the blocks' sums are scaled and added in fp32 (a block's
+ * two scales may be multiplied first: their product has to be an fp32 number).
+ * For an fp32 output the blocks are summed in fp32 too; for a 16-bit one the
+ * 8-bit matrix instruction sums them, which is twice as fast and about 1.7e-5
+ * of the result's norm off: it drops what is 2^-14 below the largest product
+ * beside it, which shows where large products cancel.  TSS_F16 or TSS_BF16 with
+ * TSS_F32_SUMS added takes fp32 sums for these too.
  * workspace: tss_gemm_fp8_workspace_size(M, N, K) bytes of device memory
  * (the partial sums of a product whose K is split over workgroups; may be
  * NULL when that is 0), 16-byte aligned, scratch.
@@ -676,7 +681,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
  * tss_gemm_grouped_fp8: C[rows of e] = (A sa)[rows of e] (B[e] sb[e])^T, A
  * T x K (a_dtype TSS_E4M3 or TSS_E5M2) with sa[ceil(K / 128)][T], B E x N x K
  * (TSS_E4M3) with sb[e][ceil(K / 128)][ceil(N / 128)]; out_dtype TSS_F16,
- * TSS_BF16 or TSS_F32 (sums as in tss_gemm_fp8); K a multiple of 16 below 2^22.
+ * TSS_BF16 or TSS_F32 (sums and TSS_F32_SUMS as in tss_gemm_fp8); K a multiple of 16 below 2^22.
  *
  * K and N multiples of 8; every tensor 16-byte aligned (sizes, sa, sb
  * 4-byte); A, C and one group's B below 2 GiB each.  T == 0 or N == 0: C is

@@ -51,6 +51,43 @@ def test_gemm_fp8_is_exact(size, a, b_rows):
     check_product(size, a, b_rows)
 
 
+@pytest.mark.parametrize("size", PRODUCTS)
+def test_gemm_fp8_with_fp32_sums_is_exact(size):
+    check_product(size, "e4m3", 128, ("bf16", "f16", "f32"), fp32_sums=True)
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("size", [(16, 128, 1024), (900, 1208, 1040), (1700, 1704, 528)])
+def test_products_whose_largest_terms_cancel(size, grouped):
+    # a pair of outlier columns in every block of 128 whose products cancel, beside values 2^-12 of theirs and less
+    M, N, K = size
+    g = U.gen(71)
+    A, B = U.normal(g, M, K) / 16, U.normal(g, N, K)
+    first = torch.arange(0, K, 128)
+    A[:, first], A[:, first + 9] = 256.0, 256.0
+    B[:, first] = 16.0
+    B[:, first + 9] = -16.0
+    A, B = A.float().to(U.TYPES["e4m3"]), B.float().to(U.TYPES["e4m3"])
+    a, b = A.double().to(CUDA), B.double().t().contiguous().to(CUDA)
+    want, terms = a @ b, a.abs() @ b.abs()
+    sa, sb = torch.ones(U.blocks(K), M, device=CUDA), torch.ones(U.blocks(K), U.blocks(N), device=CUDA)
+    for out in ("bf16", "f16"):
+        def call(**sums):
+            if grouped:
+                sizes = torch.tensor([M], dtype=torch.int32, device=CUDA)
+                return tss.gemm_grouped_fp8(A.to(CUDA), B.to(CUDA)[None], sa, sb[None], sizes, out_dtype=out, **sums).double()
+            return tss.gemm_fp8(A.to(CUDA), B.to(CUDA), sa, sb, out_dtype=out, **sums).double()
+        half, low = U.half_step(out)
+        # fp32: an addition for each term of a block, one a block, and a few more at the joins, of 2^-24 each
+        bound = terms * (128 + K / 128 + 20) * 2.0 ** -24
+        got = call(fp32_sums=True)
+        assert ((got - want).abs() <= bound * (1 + half) + want.abs() * half + low).all()
+        # the 8-bit instruction: each of a block's products keeps 2^-13 of the block's largest (256 * 16)
+        bound = bound + K * 2.0 ** -13 * 4096
+        got = call()
+        assert ((got - want).abs() <= bound * (1 + half) + want.abs() * half + low).all()
+
+
 @pytest.mark.parametrize("a", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("size", [(300, 24, 256), (1500, 1210, 144), (1001, 1001, 4112), (1700, 1704, 272), (2101, 2105, 272)])
 def test_gemm_fp8_takes_every_value(size, a):
@@ -85,8 +122,9 @@ def test_grouped_fp8_is_exact(case, a):
     dev = [t.to(CUDA) for t in (A, B, sa, sb)] + [torch.tensor(sizes, dtype=torch.int32, device=CUDA)]
     for out in ("f32", "bf16", "f16"):
         got = torch.full((T + 3, N), float("nan"), dtype=U.TYPES[out], device=CUDA)
-        tss.gemm_grouped_fp8(*dev, out_dtype=out, out=got[:T])
-        equal(got[:T], C, out)
+        for fp32_sums in (False, True):
+            tss.gemm_grouped_fp8(*dev, out_dtype=out, out=got[:T].fill_(float("nan")), fp32_sums=fp32_sums)
+            equal(got[:T], C, out)
         assert got[T:].isnan().all()
 
 

@@ -15,6 +15,7 @@ TSS_OK, TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_INFEASIBLE, TSS_E_HIP, TSS_E_
 TSS_E_SCRATCH = -7
 TSS_SCRATCH_BYTES = 64 << 20
 TSS_F16, TSS_BF16, TSS_F32, TSS_E4M3, TSS_E5M2 = 1, 2, 3, 4, 5
+TSS_F32_SUMS = 0x100
 LDS_PATTERN = {"b32": 1, "b128": 2, "tr_b64": 3, "gemm_a": 4, "gemm_a_plain": 5, "gemm_b": 6, "gemm_b_plain": 7}
 INSTR = {"mfma32": 1, "mfma16": 2, "mma": 16, "wgmma": 17, "simt": 18}
 INSTR_NAME = {v: k for k, v in INSTR.items()}

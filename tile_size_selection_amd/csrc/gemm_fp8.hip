@@ -16,7 +16,7 @@ bool misaligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t
 using Tile256 = Fp8Geometry<256, 256, 2, 8, 2>;   // with its pieces: large products
 using Piece256 = Fp8Geometry<128, 256, 3, 8, 2>;
 using Piece128 = Fp8Geometry<128, 128, 3, 8, 2>;  // also groups of middling size
-using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;   // fp32 outputs; two workgroups a CU
+using Tile128 = Fp8Geometry<128, 128, 2, 4, 2>;   // fp32 sums; two workgroups a CU
 using Tile64 = Fp8Geometry<64, 128, 3, 4, 1>;     // two workgroups a CU
 constexpr int kRoundsLds = Tile256::LDS_BYTES > Piece256::LDS_BYTES ? Tile256::LDS_BYTES : Piece256::LDS_BYTES;
 
@@ -93,6 +93,13 @@ hipError_t launch(Fp8Args &a, const ProductPlan &pl, bool exact, hipStream_t s, 
   return exact ? go(std::true_type{}) : go(std::false_type{});
 }
 
+// The output's type without the flag, and whether the sums are fp32.
+bool take_sums(int32_t &out_dtype) {
+  const bool asked = out_dtype & TSS_F32_SUMS;
+  out_dtype &= ~TSS_F32_SUMS;
+  return asked || out_dtype == TSS_F32;
+}
+
 int32_t check_types(int32_t a_dtype, int32_t out_dtype) {
   if (a_dtype != TSS_E4M3 && a_dtype != TSS_E5M2) return TSS_E_DTYPE;
   if (out_dtype != TSS_F16 && out_dtype != TSS_BF16 && out_dtype != TSS_F32) return TSS_E_DTYPE;
@@ -117,7 +124,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
   const int32_t st = check_sizes(M, N, K, 1);
   if (st != TSS_OK) return st;
   if (M == 0 || N == 0 || K == 0) return 0;
-  // the larger of what a 16-bit and an fp32 output take
+  // the larger of what the two ways of summing take
   int32_t n, ks, most = 1;
   for (bool exact : {false, true}) {
     split_ranges(K, plan_product(M, N, K, exact).splits, &n, &ks);
@@ -129,6 +136,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K) {
 int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const void *A, const void *B, const float *sa,
                      const float *sb, int32_t b_block_rows, void *C, int32_t out_dtype, void *workspace,
                      int64_t workspace_bytes, void *stream) {
+  const bool exact = take_sums(out_dtype);
   int32_t st = check_types(a_dtype, out_dtype);
   if (st == TSS_OK) st = check_sizes(M, N, K, 1);
   if (st != TSS_OK) return st;
@@ -137,7 +145,6 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
   if (!C || (K > 0 && (!A || !B || !sa || !sb))) return TSS_E_ARG;
   if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(sa, 4) || misaligned(sb, 4))
     return TSS_E_ALIGN;
-  const bool exact = out_dtype == TSS_F32;
   const ProductPlan pl = K ? plan_product(M, N, K, exact) : ProductPlan{64, 128, 1};
   Fp8Args a{};
   a.A = static_cast<const uint8_t *>(A);
@@ -158,7 +165,6 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
     if (misaligned(workspace, 16)) return TSS_E_ALIGN;
   }
   a.C = split ? workspace : C;
-  a.c_split = slice_elements(M, N);
   a.out_dtype = split ? TSS_F32 : out_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t err;
@@ -176,6 +182,7 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
 int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t a_dtype, const void *A,
                              const void *B, const float *sa, const float *sb, const int32_t *sizes, void *C,
                              int32_t out_dtype, void *stream) {
+  const bool exact = take_sums(out_dtype);
   int32_t st = check_types(a_dtype, out_dtype);
   if (st == TSS_OK) st = check_sizes(T, N, K, 8);
   if (st != TSS_OK) return st;
@@ -201,7 +208,6 @@ int32_t tss_gemm_grouped_fp8(int64_t T, int64_t E, int64_t K, int64_t N, int32_t
   a.k_split = a.K;
   a.out_dtype = out_dtype;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool exact = out_dtype == TSS_F32;
   const ProductPlan pl = plan_grouped_fp8(T, N, K, E, exact);
   const hipError_t err = a_dtype == TSS_E5M2 ? launch<true, false, true>(a, pl, exact, s, &st)
                                              : launch<false, false, true>(a, pl, exact, s, &st);

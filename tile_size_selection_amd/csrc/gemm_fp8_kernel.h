@@ -15,8 +15,9 @@
 // The 8-bit MFMA adds its products in groups with fewer bits than fp32: a
 // product 2^-14 of the largest beside it is lost (measured), which leaves the
 // result 1.7e-5 of its norm off, far below the rounding of a 16-bit output
-// (2^-9) but not of an fp32 one (plain fp32 sums: 8e-7).  With EXACT, taken
-// for fp32 outputs, the fragments are widened to fp16 (exactly: e4m3 and e5m2
+// (2^-9) but not of an fp32 one (plain fp32 sums: 8e-7), nor where large
+// products cancel.  With EXACT, taken for fp32 outputs and where the caller
+// asks for fp32 sums, the fragments are widened to fp16 (exactly: e4m3 and e5m2
 // are subsets of it) and multiplied by v_mfma_f32_16x16x32_f16, which adds in
 // fp32, at half the rate.
 //
@@ -35,14 +36,13 @@ struct Fp8Args {
   const uint8_t *B;   // [groups][N][K]
   const float *sa;    // [ceil(K / 128)][M]
   const float *sb;    // [groups][ceil(K / 128)][sb_cols]
-  void *C;            // [M][N]; split K: fp32 [splits][M][N], the slices c_split elements apart
+  void *C;            // [M][N]; split K: fp32 [splits][M][N], the slices slice_elements(M, N) apart
   const int32_t *sizes;  // grouped: rows of each group
   int32_t M, N, K, groups;
   int32_t sb_cols;    // N, or ceil(N / 128)
   int32_t tiles_m, tiles_n, splits;
   int32_t k_split;    // K of a range, a multiple of 128
   int32_t out_dtype;
-  int64_t c_split;    // split K: a multiple of 4, so that every slice starts on a 16-byte border
 };
 
 // A fragment: the 32 bytes that a lane holds of a block of 128 of K, as they
@@ -455,19 +455,15 @@ __device__ __forceinline__ void fp8_tile_product(const Fp8Args &p, const Fp8Tile
 
   auto store = [&](auto o) __attribute__((always_inline)) {
     using O = decltype(o);
-    O *C = static_cast<O *>(p.C) + t.split * p.c_split;
+    O *C = static_cast<O *>(p.C) + t.split * slice_elements(p.M, p.N);
     if (GROUPED || p.N % 8 == 0)
       store_tile<G, O>(acc, C, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
     else
       store_tile_unaligned<G, O>(acc, C, smem, t.row0, t.n0, wave, wr, wc, lane, t.row_end, p.N);
   };
-  if constexpr (EXACT) {  // taken for fp32 outputs
-    store(float{});
-  } else {
-    if (p.out_dtype == TSS_F32) store(float{});  // partial sums of a split K
-    else if (p.out_dtype == TSS_F16) store(_Float16{});
-    else store(__bf16{});
-  }
+  if (p.out_dtype == TSS_F32) store(float{});  // also the partial sums of a split K
+  else if (p.out_dtype == TSS_F16) store(_Float16{});
+  else store(__bf16{});
 }
 
 template <typename G, int KG, bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
@@ -604,7 +600,7 @@ __global__ __launch_bounds__(1024) void gemm_fp8_rows_kernel(Fp8Args p) {
         if (col + e < p.N) to[e] = v[e];
     }
   };
-  if constexpr (EXACT) put(float{});
+  if (EXACT && p.out_dtype == TSS_F32) put(float{});
   else if (p.out_dtype == TSS_F16) put(_Float16{});
   else put(__bf16{});
 }

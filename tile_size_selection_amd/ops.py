@@ -194,6 +194,10 @@ def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1,
     return out, scale
 
 
+def _out_type(out_dtype: str, fp32_sums: bool) -> int:
+    return _DT[out_dtype] | (C.TSS_F32_SUMS if fp32_sums else 0)
+
+
 def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
     n = C.lib().tss_gemm_fp8_workspace_size(M, N, K)
     if n < 0:
@@ -202,13 +206,15 @@ def gemm_fp8_workspace_size(M: int, N: int, K: int) -> int:
 
 
 @_streamed
-def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
+def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, fp32_sums: bool = False):
     """C = (A sa) @ (B sb)^T for 8-bit A (M, K), e4m3 or e5m2, and B (N, K),
     e4m3, with sa[ceil(K / 128)][M] and sb[ceil(K / 128)][N or ceil(N / 128)];
-    out_dtype 'bf16', 'f16' or 'f32' (fp32 sums throughout, at half the rate;
-    tss_gemm_fp8 in include/tss.h says how the sums of a 16-bit output
-    differ).  K a multiple of 16.  workspace: a device tensor of at least gemm_fp8_workspace_size bytes
-    (allocated here when one is needed and not given)."""
+    out_dtype 'bf16', 'f16' or 'f32'.  fp32_sums: sums in fp32 throughout, at
+    half the rate ('f32' always has them; without it a 16-bit output's blocks
+    of 128 are summed in fewer bits, which shows where large products cancel:
+    tss_gemm_fp8 in include/tss.h).  K a multiple of 16.  workspace: a device
+    tensor of at least gemm_fp8_workspace_size bytes (allocated here when one
+    is needed and not given)."""
     adt = _name(A, "A", ("e4m3", "e5m2"))
     _name(B, "B", ("e4m3",))
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
@@ -227,7 +233,7 @@ def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
         workspace = _workspace(workspace, need, A.device)
     _call("tss_gemm_fp8", C.lib().tss_gemm_fp8, (A, B, sa, sb, out, workspace),
           M, N, K, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), b_rows, out.data_ptr(),
-          _DT[out_dtype], _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+          _out_type(out_dtype, fp32_sums), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
 
 
@@ -290,11 +296,11 @@ def gemm_grouped_backward(dC, A, B, sizes, dA=None, dB=None, db_dtype: str = "f3
 
 
 @_streamed
-def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None):
+def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None, fp32_sums: bool = False):
     """C[rows of group e] = (A sa)[rows of e] @ (B[e] sb[e])^T: A (T, K), e4m3
     or e5m2, sorted by group, with sa[ceil(K / 128)][T]; B (E, N, K), e4m3,
     with sb[e][ceil(K / 128)][ceil(N / 128)]; sizes and the rows of no group
-    as in gemm_grouped.  K a multiple of 16, N of 8."""
+    as in gemm_grouped, fp32_sums as in gemm_fp8.  K a multiple of 16, N of 8."""
     adt = _name(A, "A", ("e4m3", "e5m2"))
     _name(B, "B", ("e4m3",))
     if A.dim() != 2 or B.dim() != 3 or A.shape[1] != B.shape[2]:
@@ -310,5 +316,5 @@ def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None):
     out = _out(out, "out", (T, N), _TORCH[out_dtype], A.device)
     _call("tss_gemm_grouped_fp8", C.lib().tss_gemm_grouped_fp8, (A, B, sa, sb, sizes, out),
           T, E, K, N, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), sizes.data_ptr(),
-          out.data_ptr(), _DT[out_dtype])
+          out.data_ptr(), _out_type(out_dtype, fp32_sums))
     return out
