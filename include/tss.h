@@ -598,8 +598,9 @@ int32_t tss_lds_probe(int32_t pattern, int32_t stride_words, int32_t iters, int3
  * scale[ceil(d / 128)][rows] (NULL otherwise).  residual_out (may be NULL):
  * h rounded to dtype; it may be residual or x itself.  y may be x when
  * out_dtype is dtype.  rstd (may be NULL): rows fp32, 1 / sqrt(...).
- * weight: d elements of dtype.  d <= 32768.  x, residual, weight, y and
- * residual_out 16-byte aligned.  rows == 0: nothing to do.
+ * weight: d elements of dtype.  d <= 32768; rows < 2^23, and where a row is
+ * wider than 16384, rows < 2^22.  x, residual, weight, y and residual_out
+ * 16-byte aligned.  rows == 0: nothing to do.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_UNSUPPORTED (d),
  * TSS_E_HIP.
  */
@@ -614,7 +615,7 @@ int32_t tss_rms_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, cons
  * through residual_out), and dweight[d] (fp32) = sum over rows of dy xhat,
  * added in a fixed order.  dx may be dy or dh.  workspace: device memory of
  * at least tss_rms_norm_backward_workspace_size(rows, d) bytes, 16-byte
- * aligned, scratch.  rows == 0: dweight is zero-filled.
+ * aligned, scratch.  rows < 2^23.  rows == 0: dweight is zero-filled.
  * Errors: as tss_rms_norm; TSS_E_ARG for a missing or small workspace.
  */
 int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
@@ -629,7 +630,8 @@ int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d);
  * |gate| + 8 halves of a unit for negative gates, 8 for positive ones, and 0
  * for gates below about -87.  Blocks of 1 x 128 round as the value and scale
  * in 64 bits do; their stored scale, and blocks of 128 x 128, keep that error.
- * x and q 16-byte aligned.
+ * x and q 16-byte aligned; rows * ceil(d / 512) < 2^28 with blocks of 1 x 128,
+ * rows * ceil(d / 128) < 2^30 with blocks of 128 x 128.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
 int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, int32_t fp8,

@@ -1,0 +1,33 @@
+"""More rows, columns and elements than a launch with a thread for each holds."""
+import pytest
+import torch
+
+import tile_size_selection_amd as tss
+import ops_util as U
+
+pytestmark = pytest.mark.gpu
+
+CUDA = torch.device("cuda:0")
+
+
+def test_norm_of_four_million_narrow_rows():
+    # a norm over each head: 32768 tokens of 128 heads, and some
+    rows, d = (1 << 22) + 5, 128
+    g = torch.Generator(device=CUDA)
+    g.manual_seed(1)
+    x = torch.randn(rows, d, generator=g, device=CUDA, dtype=torch.bfloat16)
+    w = (1 + 0.2 * torch.randn(d, generator=g, device=CUDA)).to(torch.bfloat16)
+    got = tss.rms_norm(x, w, rstd=True)
+    dx, dw = tss.rms_norm_backward(x, x, w, got.rstd)
+    for part in (slice(0, 9), slice(rows // 2, rows // 2 + 9), slice(rows - 9, rows)):
+        y, h, rstd = U.norm_forward(x[part].cpu(), None, w.cpu(), 1e-6)
+        assert ((got.y[part].double().cpu() - y).abs() <= y.abs() * (2.0 ** -8 + 2.0 ** -18)).all()
+        r = got.rstd[part].double().cpu()[:, None]
+        assert ((r[:, 0] - rstd).abs() <= rstd * 2.0 ** -18).all()
+        want, _ = U.norm_backward(x[part].cpu(), x[part].cpu(), w.cpu(), got.rstd[part].cpu(), None)
+        size = (h * w.cpu().double()).abs()
+        terms = r * (size + (h * r).abs() * (size * (h * r).abs()).mean(1, keepdim=True))
+        assert ((dx[part].double().cpu() - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -18 * terms).all()
+    # dw = sum of x^2 rstd, terms of one sign: 3072 workgroups' sums of 1366 rows each, then 200 partial sums at most
+    want = (x.double().square() * got.rstd.double()[:, None]).sum(0)
+    assert ((dw.double() - want).abs() <= want * (1366 + 200) * 2.0 ** -24).all()

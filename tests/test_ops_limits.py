@@ -4,7 +4,7 @@ touched, and Python calls with host tensors."""
 import pytest
 
 from tile_size_selection_amd import _capi as C
-from test_ops_refusals import ALIGN, ARG, DTYPE, GEMM, GROUPED8, _with
+from test_ops_refusals import ALIGN, ARG, BACK, DTYPE, GEMM, GROUPED8, NORM, ODD, QUANT, _with
 
 SUMS = C.TSS_F32_SUMS
 
@@ -15,3 +15,20 @@ SUMS = C.TSS_F32_SUMS
 def test_products_take_fp32_sums_of_their_output_types(change, status):
     assert C.lib().tss_gemm_fp8(*_with(GEMM, **change)) == status
     assert C.lib().tss_gemm_grouped_fp8(*_with(GROUPED8, **change)) == status
+
+
+# a misaligned operand shows that the sizes before it were taken
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=1 << 22, d=128), ALIGN), (dict(rows=(1 << 23) - 1, d=64), ALIGN), (dict(rows=1 << 23, d=8), ARG)])
+def test_norm_takes_many_narrow_rows(change, status):
+    assert C.lib().tss_rms_norm(*_with(NORM, x=ODD, **change)) == status
+    size = C.lib().tss_rms_norm_backward_workspace_size(change["rows"], change["d"])
+    assert size > 0 if status == ALIGN else size == ARG
+    assert C.lib().tss_rms_norm_backward(*_with(BACK, dy=ODD, ws_bytes=1 << 30, **change)) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(rows=1 << 27, d=512), ALIGN), (dict(rows=1 << 28, d=512), ARG), (dict(rows=1 << 27, d=520), ARG),
+    (dict(rows=1 << 29, d=128, block_rows=128), ALIGN), (dict(rows=1 << 30, d=128, block_rows=128), ARG)])
+def test_quantize_takes_what_a_launch_holds(change, status):
+    assert C.lib().tss_quantize_fp8(*_with(QUANT, q=ODD, **change)) == status

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kMaxChunks = 4;     // chunks of 8 elements per thread
 constexpr int kMaxThreads = 1024;
+constexpr int64_t kMaxRows = (int64_t(1) << 23) - 1;
 constexpr int64_t kMaxD = int64_t(kMaxChunks) * kMaxThreads * 8;
 
 // Sum over the wpr waves that share a row; red has one slot per wave.
@@ -235,11 +236,10 @@ __global__ void zero_f32_kernel(int n, float *p) {
 bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
 
 int32_t check_rows(int64_t rows, int64_t d, int32_t dtype) {
-  if (rows < 0 || d < 1 || rows > INT32_MAX) return TSS_E_ARG;
+  if (rows < 0 || d < 1 || rows > kMaxRows) return TSS_E_ARG;
   if (dtype != TSS_F16 && dtype != TSS_BF16 && dtype != TSS_F32) return TSS_E_DTYPE;
   if (d % 8) return TSS_E_ALIGN;
   if (d > kMaxD) return TSS_E_UNSUPPORTED;
-  if (rows * kMaxThreads > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
   return TSS_OK;
 }
 
@@ -258,7 +258,7 @@ RowShape row_shape(int64_t d, int chunks) {
 }
 
 template <typename T, bool FP8>
-void launch_norm(int64_t rows, int64_t d, const void *x, const void *residual, const void *weight, float eps, void *y,
+int32_t launch_norm(int64_t rows, int64_t d, const void *x, const void *residual, const void *weight, float eps, void *y,
                  float *scale, void *h, float *rstd, hipStream_t s) {
   // Few rows: a row's latency is all that counts, so it is spread over as
   // many threads as it has chunks.  Many rows: four chunks a thread keep
@@ -266,15 +266,17 @@ void launch_norm(int64_t rows, int64_t d, const void *x, const void *residual, c
   const RowShape f = row_shape(d, rows < 1024 ? 1 : 4);
   const int block = f.waves == 1 ? 256 : f.waves * 64;
   const int rpb = f.waves == 1 ? 4 : 1;
-  const dim3 grid(uint32_t((rows + rpb - 1) / rpb));
+  const int64_t blocks = (rows + rpb - 1) / rpb;
+  if (blocks * block > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(block), 0, s, int(rows), int(d), static_cast<const T *>(x),
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(block), 0, s, int(rows), int(d), static_cast<const T *>(x),
                        static_cast<const T *>(residual), static_cast<const T *>(weight), eps, y, scale,
                        static_cast<T *>(h), rstd, f.waves);
   };
   if (f.chunks == 1) go(rms_norm_kernel<T, FP8, 1>);
   else if (f.chunks == 2) go(rms_norm_kernel<T, FP8, 2>);
   else go(rms_norm_kernel<T, FP8, 4>);
+  return TSS_OK;
 }
 
 // Workgroups of the backward pass: 12 waves a CU and two workgroups at least,
@@ -322,17 +324,18 @@ int32_t tss_rms_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, cons
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto go = [&](auto t) {
     using T = decltype(t);
-    if (fp8) launch_norm<T, true>(rows, d, x, residual, weight, eps, y, scale, residual_out, rstd, s);
-    else launch_norm<T, false>(rows, d, x, residual, weight, eps, y, scale, residual_out, rstd, s);
+    st = fp8 ? launch_norm<T, true>(rows, d, x, residual, weight, eps, y, scale, residual_out, rstd, s)
+             : launch_norm<T, false>(rows, d, x, residual, weight, eps, y, scale, residual_out, rstd, s);
   };
   if (dtype == TSS_F16) go(_Float16{});
   else if (dtype == TSS_BF16) go(__bf16{});
   else go(float{});
+  if (st != TSS_OK) return st;
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 
 int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d) {
-  if (rows < 0 || d < 1) return TSS_E_ARG;
+  if (rows < 0 || d < 1 || rows > kMaxRows) return TSS_E_ARG;
   if (d % 8) return TSS_E_ALIGN;
   if (d > kMaxD) return TSS_E_UNSUPPORTED;
   return backward_blocks(rows, d) * d * 4;

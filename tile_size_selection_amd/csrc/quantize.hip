@@ -259,8 +259,10 @@ extern "C" int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, cons
     return TSS_E_DTYPE;
   if (d % 8) return TSS_E_ALIGN;
   if (rows == 0) return TSS_OK;
-  // the launch's thread count is 32 bits (either form has at most this many workgroups)
-  if ((rows + 15) / 16 * ((d + 127) / 128) * kThreads > int64_t(UINT32_MAX)) return TSS_E_ARG;
+  // the launch's thread count is 32 bits
+  const int64_t threads = block_rows == 1 ? (rows + 15) / 16 * ((d + kBlocks * kScaleBlock - 1) / (kBlocks * kScaleBlock)) * kThreads
+                                          : (rows + 127) / 128 * ((d + 127) / 128) * kBlockThreads;
+  if (threads > int64_t(UINT32_MAX)) return TSS_E_ARG;
   if (!x || !q || !scale) return TSS_E_ARG;
   if ((reinterpret_cast<uintptr_t>(x) & 15u) || (reinterpret_cast<uintptr_t>(q) & 15u)) return TSS_E_ALIGN;
   hipStream_t s = static_cast<hipStream_t>(stream);
