@@ -2,9 +2,11 @@
 before any device work: calls through the C ABI with addresses that are never
 touched, and Python calls with host tensors."""
 import pytest
+import torch
 
+import tile_size_selection_amd as tss
 from tile_size_selection_amd import _capi as C
-from test_ops_refusals import ALIGN, ARG, BACK, DTYPE, GEMM, GROUPED8, NORM, ODD, QUANT, _with
+from test_ops_refusals import ALIGN, ARG, BACK, DTYPE, GEMM, GROUPED8, NORM, ODD, QUANT, S, F8, _with, z
 
 SUMS = C.TSS_F32_SUMS
 
@@ -32,3 +34,26 @@ def test_norm_takes_many_narrow_rows(change, status):
     (dict(rows=1 << 29, d=128, block_rows=128), ALIGN), (dict(rows=1 << 30, d=128, block_rows=128), ARG)])
 def test_quantize_takes_what_a_launch_holds(change, status):
     assert C.lib().tss_quantize_fp8(*_with(QUANT, q=ODD, **change)) == status
+
+
+@pytest.mark.parametrize("call", [
+    lambda h: tss.gemm_fp8(out_dtype="bf16", A=z(4, 128, t=F8), B=z(8, 128, t=F8), sa=z(1, 4, t=S), sb=z(1, 1, t=S), stream=h),
+    lambda h: tss.rms_norm(eps=1e-5, x=z(4, 64), weight=z(64), stream=h),
+    lambda h: tss.quantize_fp8(gated=False, x=z(4, 64), stream=h),
+    lambda h: tss.quantize_fp8("x", stream=h)])
+def test_a_stream_wants_tensors_on_a_gpu_in_any_order_of_arguments(call):
+    with pytest.raises(ValueError, match="stream"):
+        call(1 << 20)
+
+
+def test_a_stream_of_another_gpu_is_refused(monkeypatch):
+    class Stream:
+        device = torch.device("cuda:1")
+
+    class Tensor(torch.Tensor):
+        device = torch.device("cuda:0")
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    x, w = z(4, 64).as_subclass(Tensor), z(64).as_subclass(Tensor)
+    with pytest.raises(ValueError, match="the stream is of cuda:1, the tensors are on cuda:0"):
+        tss.rms_norm(x, w, stream=Stream())

@@ -151,3 +151,16 @@ def test_thousands_of_groups():
     got = tss.gemm_grouped_fp8(dev[0].to(f8), dev[1].transpose(1, 2).contiguous().to(f8), ones(1, T), ones(E, 1, 1), dev[3],
                                out_dtype="f32")
     equal(got, C, "C of 8 bits")
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_calls_by_keyword_on_a_stream(handle):
+    g = U.gen(81)
+    A, B = ints(g, (40, 256), 3, "e4m3"), ints(g, (24, 256), 2, "e4m3")
+    ones = torch.ones(2, 40, device=CUDA), torch.ones(2, 1, device=CUDA)
+    a, b = A.to(CUDA), B.to(CUDA)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    C = tss.gemm_fp8(out_dtype="f32", A=a, B=b, sa=ones[0], sb=ones[1], stream=side.cuda_stream if handle else side)
+    torch.cuda.current_stream().wait_stream(side)
+    equal(C, A.double() @ B.double().t())

@@ -59,17 +59,21 @@ _raw_stream = getattr(getattr(torch, "_C", None), "_cuda_getCurrentRawStream", N
 
 
 def _streamed(f):
-    """f with stream=None or the stream to run on (a torch stream, or a HIP
-    stream's handle).  The stream is made current for the call, so that what
-    is allocated in it belongs to that stream too: a workspace freed on return
-    is reused behind the launch that uses it."""
+    """f with stream=None or the stream to run on (a torch stream of the
+    tensors' GPU, or a HIP stream's handle).  The stream is made current for
+    the call, so that what is allocated in it belongs to that stream too: a
+    workspace freed on return is reused behind the launch that uses it."""
     @functools.wraps(f)
     def call(*args, stream=None, **kwargs):
         if stream is None:
             return f(*args, **kwargs)
+        device = next((a.device for a in (*args, *kwargs.values()) if isinstance(a, torch.Tensor)), None)
+        if device is None or device.type != "cuda":
+            raise ValueError(f"stream= needs tensors on a GPU, not on {device}")
         if not isinstance(stream, torch.cuda.Stream):
-            first = args[0] if args else next(iter(kwargs.values()))
-            stream = torch.cuda.ExternalStream(stream, device=first.device)
+            stream = torch.cuda.ExternalStream(stream, device=device)
+        elif stream.device != device:
+            raise ValueError(f"the stream is of {stream.device}, the tensors are on {device}")
         with torch.cuda.stream(stream):
             return f(*args, **kwargs)
     return call
