@@ -655,7 +655,8 @@ int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, 
  * (the partial sums of a product whose K is split over workgroups; may be
  * NULL when that is 0), 16-byte aligned, scratch.
  * K a multiple of 16 and below 2^22, any N; A, B, C 16-byte aligned, sa and
- * sb 4-byte; each operand below 2 GiB.  M == 0 or N == 0: nothing to do.  K == 0: C is
+ * sb 4-byte; A and B below 2 GiB each, C of any size; fewer than 2^23 tiles of
+ * 64 x 128 of C (a launch's threads; more with M <= 16).  M == 0 or N == 0: nothing to do.  K == 0: C is
  * zero-filled (A, B, sa and sb may then be NULL).
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
@@ -686,7 +687,8 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
  * TSS_BF16 or TSS_F32 (sums and TSS_F32_SUMS as in tss_gemm_fp8); K a multiple of 16 below 2^22.
  *
  * K and N multiples of 8; every tensor 16-byte aligned (sizes, sa, sb
- * 4-byte); A, C and one group's B below 2 GiB each.  T == 0 or N == 0: C is
+ * 4-byte); A, one group's B, and C of 16-bit products below 2 GiB each; C of
+ * 8-bit ones below (min(T, T / 64 + E + 1) * ceil(N / 128)) 2^23 tiles.  T == 0 or N == 0: C is
  * empty; K == 0: C is zero-filled.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */

@@ -31,3 +31,29 @@ def test_norm_of_four_million_narrow_rows():
     # dw = sum of x^2 rstd, terms of one sign: 3072 workgroups' sums of 1366 rows each, then 200 partial sums at most
     want = (x.double().square() * got.rstd.double()[:, None]).sum(0)
     assert ((dw.double() - want).abs() <= want * (1366 + 200) * 2.0 ** -24).all()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_gemm_fp8_of_one_row_and_a_hundred_million_columns(out):
+    N, K = 100_000_003, 16
+    g = torch.Generator(device=CUDA)
+    g.manual_seed(2)
+    A = torch.randint(-2, 3, (1, K), generator=g, device=CUDA).float().to(torch.float8_e4m3fn)
+    B = torch.randint(-1, 2, (N, K), generator=g, device=CUDA, dtype=torch.int8).to(torch.float8_e4m3fn)
+    C = tss.gemm_fp8(A, B, torch.ones(1, 1, device=CUDA), torch.ones(1, U.blocks(N), device=CUDA), out_dtype=out)
+    for i in range(0, N, 1 << 23):
+        assert torch.equal(C[0, i:i + (1 << 23)].float(), B[i:i + (1 << 23)].float() @ A[0].float())
+
+
+@pytest.mark.parametrize("shape", [(65600, 65610), (66000, 65536)])
+def test_gemm_fp8_of_more_than_2_to_32_elements(shape):
+    (M, N), K = shape, 16
+    assert M * N > 1 << 32
+    g = torch.Generator(device=CUDA)
+    g.manual_seed(3)
+    A = torch.randint(-2, 3, (M, K), generator=g, device=CUDA, dtype=torch.int8).to(torch.float8_e4m3fn)
+    B = torch.randint(-1, 2, (N, K), generator=g, device=CUDA, dtype=torch.int8).to(torch.float8_e4m3fn)
+    C = tss.gemm_fp8(A, B, torch.ones(1, M, device=CUDA), torch.ones(1, U.blocks(N), device=CUDA))
+    b = B.float().t().contiguous()
+    for i in range(0, M, 4100):
+        assert torch.equal(C[i:i + 4100].float(), A[i:i + 4100].float() @ b)

@@ -57,3 +57,16 @@ def test_a_stream_of_another_gpu_is_refused(monkeypatch):
     x, w = z(4, 64).as_subclass(Tensor), z(64).as_subclass(Tensor)
     with pytest.raises(ValueError, match="the stream is of cuda:1, the tensors are on cuda:0"):
         tss.rms_norm(x, w, stream=Stream())
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(M=65536, N=65536, K=16, C=ODD), ALIGN), (dict(M=(1 << 27) - 1, N=40, K=16, A=ODD), ALIGN),
+    (dict(M=1 << 27, N=1, K=16), ARG), (dict(M=1, N=1 << 27, K=16), ARG), (dict(M=(1 << 31) - 1, N=1, K=0), ARG)])
+def test_gemm_fp8_takes_operands_below_2_gib_and_what_a_launch_holds(change, status):
+    assert C.lib().tss_gemm_fp8(*_with(GEMM, **change)) == status
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(T=16, E=16, N=(1 << 27) - 8, K=16), ARG), (dict(T=1 << 27, K=16), ARG), (dict(T=1 << 20, N=8192, B=ODD), ALIGN)])
+def test_grouped_fp8_takes_what_a_launch_holds(change, status):
+    assert C.lib().tss_gemm_grouped_fp8(*_with(GROUPED8, **change)) == status

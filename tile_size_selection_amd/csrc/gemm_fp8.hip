@@ -58,11 +58,15 @@ hipError_t launch_rounds(const Fp8Args &a, int64_t tiles, hipStream_t s) {
                     Tile256::THREADS, kRoundsLds, s);
 }
 
+// Waves of a workgroup of the kernel for few rows.
+int rows_waves(int64_t K) {
+  const int64_t nk = (K + 127) / 128, nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
+  return int(nw > 16 ? 16 : nw);
+}
+
 template <bool A_E5M2, bool B_ROWS, bool GROUPED, bool EXACT>
 hipError_t launch_rows(const Fp8Args &a, int64_t blocks, hipStream_t s) {
-  const int nk = (a.K + 127) / 128;
-  int nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
-  nw = nw > 16 ? 16 : nw;
+  const int nw = rows_waves(a.K);
   hipLaunchKernelGGL((gemm_fp8_rows_kernel<A_E5M2, B_ROWS, GROUPED, EXACT>), dim3(uint32_t(blocks)), dim3(nw * 64), nw * 1024, s,
                      a);
   return hipGetLastError();
@@ -74,7 +78,8 @@ hipError_t launch(Fp8Args &a, const ProductPlan &pl, bool exact, hipStream_t s, 
   const int64_t tiles_m = GROUPED ? max_group_tiles(a.M, a.groups, pl.bm) : (int64_t(a.M) + pl.bm - 1) / pl.bm;
   a.tiles_m = int32_t(tiles_m);
   const int64_t blocks = tiles_m * a.tiles_n * a.splits;
-  if (blocks * 1024 > int64_t(UINT32_MAX)) {  // the launch's thread count is 32 bits
+  // the launch's thread count is 32 bits (tiles: 512 threads at most, and a round's pieces)
+  if ((pl.bn == 16 ? blocks * rows_waves(a.K) * 64 : (blocks + 2 * kCUs) * 512) > int64_t(UINT32_MAX)) {
     *status = TSS_E_ARG;
     return hipSuccess;
   }
@@ -109,10 +114,9 @@ int32_t check_types(int32_t a_dtype, int32_t out_dtype) {
 int32_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t n_multiple) {
   if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return TSS_E_ARG;
   if (K % 16 || N % n_multiple) return TSS_E_ALIGN;
-  if (M * K >= kTwoGiB || N * K >= kTwoGiB || M * N * 2 >= kTwoGiB * 4) return TSS_E_ARG;
-  // the kernels' byte offsets are 32 bits: 256 rows of K, and a row of scales for each 128 of K
-  if (K >= int64_t(1) << 22) return TSS_E_ARG;
-  if ((K + 127) / 128 * 4 * (M > N ? M : N) >= kTwoGiB) return TSS_E_ARG;
+  // the kernels' byte offsets into A, B and the scales are 32 bits (the scales of 2 GiB of values take 640 MiB at most:
+  // K is at least 16), as are those of 256 rows of K
+  if (M * K >= kTwoGiB || N * K >= kTwoGiB || K >= int64_t(1) << 22) return TSS_E_ARG;
   return TSS_OK;
 }
 
