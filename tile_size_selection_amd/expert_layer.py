@@ -21,18 +21,30 @@ from .ops import (gemm_grouped, gemm_grouped_backward, gemm_grouped_fp8, quantiz
 
 class Routing(NamedTuple):
     """Rows sorted by expert: row i of a grouped product is token token[i],
-    which gives its result the weight weight[i]; sizes: rows per expert."""
+    which gives its result the weight weight[i]; sizes: rows per expert;
+    row[t][j]: the row of token t's choice j."""
     token: "torch.Tensor"
     weight: "torch.Tensor"
     sizes: "torch.Tensor"
+    row: "torch.Tensor"
 
 
 def route(expert, weight, experts: int) -> Routing:
-    """Routing of expert (tokens, top) integers and weight (tokens, top)."""
+    """Routing of expert (tokens, top) integers and weight (tokens, top).  An
+    expert outside 0 .. experts - 1 is a dropped choice: its row comes last, is
+    in no expert's group and adds nothing."""
     flat = expert.reshape(-1)
+    flat = torch.where((flat >= 0) & (flat < experts), flat, experts)
     order = torch.argsort(flat, stable=True)
+    row = torch.empty_like(order).scatter_(0, order, torch.arange(order.numel(), device=order.device))
     sizes = (flat[None, :] == torch.arange(experts, device=flat.device)[:, None]).sum(1, dtype=torch.int32)
-    return Routing(order // expert.shape[1], weight.reshape(-1)[order], sizes)
+    return Routing(order // expert.shape[1], weight.reshape(-1)[order], sizes, row.view(expert.shape))
+
+
+def join(rows, r: Routing):
+    """Each token's sum over its choices' rows, in the order of the choices
+    (without atomics: the same bits on every run), in float32."""
+    return rows.float()[r.row].sum(1)
 
 
 class Fp8Weights(NamedTuple):
@@ -60,8 +72,7 @@ def forward_fp8(x, residual, w: Fp8Weights, r: Routing):
     up = gemm_grouped_fp8(rows, w.w1, n.scale[:, r.token].contiguous(), w.s1, r.sizes)
     act, scale = quantize_fp8(up, gated=True)
     y = gemm_grouped_fp8(act, w.w2, scale, w.s2, r.sizes, out_dtype="f32")
-    out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
-    return out.index_add_(0, r.token, y * r.weight[:, None]).to(x.dtype), n.h
+    return join(y * r.weight[:, None], r).to(x.dtype), n.h
 
 
 class Saved(NamedTuple):
@@ -81,9 +92,7 @@ def forward(x, residual, norm, w1, w2, r: Routing):
     gate, lin = up.float().chunk(2, 1)
     act = (torch.nn.functional.silu(gate) * lin).to(x.dtype)
     y = gemm_grouped(act, w2, r.sizes, out_dtype="f32")
-    out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
-    out = out.index_add_(0, r.token, y * r.weight[:, None]).to(x.dtype)
-    return out, n.h, Saved(n.h, n.rstd, rows, up, act)
+    return join(y * r.weight[:, None], r).to(x.dtype), n.h, Saved(n.h, n.rstd, rows, up, act)
 
 
 def backward(dout, dh, norm, w1, w2, r: Routing, s: Saved):
@@ -96,8 +105,7 @@ def backward(dout, dh, norm, w1, w2, r: Routing, s: Saved):
     da = dact.float()
     dup = torch.cat([da * lin * sig * (1 + gate * (1 - sig)), da * gate * sig], 1).to(dout.dtype)
     drows, dw1 = gemm_grouped_backward(dup, s.rows, w1, r.sizes)
-    dn = torch.zeros(s.h.shape, dtype=torch.float32, device=dout.device).index_add_(0, r.token, drows.float())
-    dx, dnorm = rms_norm_backward(dn.to(dout.dtype), s.h, norm, s.rstd, dh)
+    dx, dnorm = rms_norm_backward(join(drows, r).to(dout.dtype), s.h, norm, s.rstd, dh)
     return dx, dnorm, dw1, dw2
 
 
