@@ -57,3 +57,19 @@ def test_quantize_gated_rounds_as_in_64_bits(kind, fp8, dtype):
     assert sure.double().mean() > 0.9
     bad = (q.float() != want) & sure
     assert not bad.any(), f"{int(bad.sum())} differ, first at {bad.nonzero()[:4].tolist()}"
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("fp8", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_quantize_rounds_as_fp32_division_does(dtype, fp8, block_rows):
+    # scale = amax / largest and q = value / scale in fp32, each rounded as IEEE division is (on the CPU: on the GPU
+    # torch multiplies by a constant divisor's reciprocal); many values of a 16-bit type lie exactly on a border
+    rows, d = 1500, 4104
+    g = U.gen(91)
+    x = (U.normal(g, rows, d) * torch.exp(0.7 * U.normal(g, d))).to(U.TYPES[dtype])
+    q, s = tss.quantize_fp8(x.to(CUDA), fp8, block_rows=block_rows)
+    scale = U.block_amax(x.float(), block_rows).clamp(min=1e-30) / torch.tensor(U.LARGEST[fp8])
+    assert torch.equal(s.cpu(), scale)
+    want = (x.float() / U.spread(scale, rows, d, block_rows)).to(U.TYPES[fp8])
+    assert torch.equal(q.float().cpu(), want.float())

@@ -122,8 +122,7 @@ __device__ __forceinline__ float sum64(float v) {
 // the quotient is the product with the reciprocal, corrected once by its
 // remainder, which rounds it as a division does for 2 more operations an
 // element (the bare product moves some of the values that lie on a rounding
-// border of the 8-bit type, as many of those of a 16-bit type do: 2.6e-3
-// against 2.2e-3 of the norm on bf16 weights).  |v| <= amax keeps the
+// border of the 8-bit type, as many of those of a 16-bit type do).  |v| <= amax keeps the
 // quotient below the halfway point past the largest value, so the conversion
 // needs no clamp.
 template <typename Q>
