@@ -21,9 +21,10 @@
 // are subsets of it) and multiplied by v_mfma_f32_16x16x32_f16, which adds in
 // fp32, at half the rate.
 //
-// Two kernels: gemm_fp8_tile_kernel stages BM x 128 and BN x 128 tiles of the
-// operands through LDS; gemm_fp8_rows_kernel, for few rows, streams B from
-// memory straight into registers.
+// Three kernels: gemm_fp8_tile_kernel stages BM x 128 and BN x 128 tiles of the
+// operands through LDS; gemm_fp8_rounds_kernel does so with the last round's
+// tiles in pieces; gemm_fp8_rows_kernel, for few rows, streams B from memory
+// straight into registers.
 #pragma once
 #include "grouped_kernel.h"
 
@@ -164,7 +165,7 @@ __device__ __forceinline__ Fp8Tile fp8_tile(const Fp8Args &p, int lane) {
 // bytes of memory, so that whole 16-byte pieces of memory are written from
 // aligned pieces of LDS; the elements of the pieces at a row's ends are
 // written one by one (their other elements are another wave's).  Measured at
-// 8192 x 8191 x 512, bf16: 4-byte words 118 us, see gemm_fp8.hip for this.
+// 8192 x 8191 x 512, bf16: 4-byte words 118 us, this 80 to 90 (N 8192: 66).
 template <typename G, typename O, typename Acc>
 __device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::TN], O *C, char *smem, int m0, int n0,
                                                      int wave, int wr, int wc, int lane, int M, int N) {
@@ -223,7 +224,8 @@ __device__ __forceinline__ void store_tile_unaligned(const Acc (&acc)[G::TM][G::
 // The sums of one group of MFMAs are scaled while the next group's run.
 // Measured at 8192^3 (e4m3, 128 x 128 scales of B, bf16 out) on one box: all of
 // a step's fragments read and copies spread over it behind the barrier 482 us,
-// copies in its first half 449-459, this 439 (2.50 PFLOP/s).  Of 459 us,
+// copies in its first half 449-459, this 439; 440 to 475 (2.3 to 2.5 PFLOP/s)
+// over boxes and inputs.  Of 459 us,
 // leaving out the copies took 62, the scaling 47, the fragment reads 118; the
 // MFMAs alone took 271.
 //

@@ -9,8 +9,8 @@
 //     over the group's rows, so the A operand is copied and read like the
 //     GEMM's B, with the transpose read.
 // Bound by the matrix cores where groups are large: 16384 rows, 8 groups, K =
-// 4096, N = 2048, bf16: forward 239 us (1.15 PFLOP/s; one library product of
-// 8192^3: 1.16), dA 248, dB 244 (fp32, 268 MB written).
+// 4096, N = 2048, bf16: forward 239 us (1.15 PFLOP/s; the GEMM's 8192^3: 1.50,
+// the library's 1.39), dA 248, dB 244 (fp32, 268 MB written).
 // A body of its own: with these modes in the GEMM's, the convolution's kernel
 // came out 7% slower.
 #pragma once

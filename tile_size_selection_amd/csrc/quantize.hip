@@ -8,9 +8,10 @@
 // scale is K-block-major, scale[column block][row or row block]: the matrix
 // products read the scales of one step of K for consecutive rows.
 // Memory-bound: an element is read once, kept in registers while its block's
-// maximum is found, and written in 8 bits.  bf16 to e4m3, 16400 x 2048: 17.5 us
-// (5.9 TB/s), gated 38.3 (4.4 TB/s: exp and reciprocal take 20 of it behind the
-// loads); 128 x 128 blocks, 5000 x 8200: 22 us (5.6 TB/s).
+// maximum is found, and written in 8 bits.  bf16 to e4m3 with inputs that are in
+// no cache, 16400 x 2048: 22.7 us (4.5 TB/s), gated 38.3 (4.4 TB/s: exp and
+// reciprocal take 20 of it behind the loads), gated with 128 x 128 blocks 36.1;
+// 128 x 128 blocks, 5000 x 8200: 26.5 us (4.65 TB/s; a large copy: 5.0).
 #include "rows.h"
 
 using namespace tss;
