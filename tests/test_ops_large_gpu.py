@@ -28,7 +28,7 @@ def test_norm_of_four_million_narrow_rows():
         size = (h * w.cpu().double()).abs()
         terms = r * (size + (h * r).abs() * (size * (h * r).abs()).mean(1, keepdim=True))
         assert ((dx[part].double().cpu() - want).abs() <= want.abs() * 2.0 ** -8 + 2.0 ** -18 * terms).all()
-    # dw = sum of x^2 rstd, terms of one sign: 3072 workgroups' sums of 1366 rows each, then 200 partial sums at most
+    # dw = sum of x^2 rstd, terms of one sign: a workgroup (12 a CU) sums 1366 rows, then 200 partial sums at most
     want = (x.double().square() * got.rstd.double()[:, None]).sum(0)
     assert ((dw.double() - want).abs() <= want * (1366 + 200) * 2.0 ** -24).all()
 

@@ -164,3 +164,48 @@ def test_calls_by_keyword_on_a_stream(handle):
     C = tss.gemm_fp8(out_dtype="f32", A=a, B=b, sa=ones[0], sb=ones[1], stream=side.cuda_stream if handle else side)
     torch.cuda.current_stream().wait_stream(side)
     equal(C, A.double() @ B.double().t())
+
+
+@pytest.mark.parametrize("fp32_sums", [False, True])
+@pytest.mark.parametrize("size", [(16, 136, 256), (1500, 1210, 272), (1001, 1001, 4112), (1700, 1704, 272), (2101, 2105, 272)])
+def test_gemm_fp8_nan_stays_in_its_row_and_column(size, fp32_sums):
+    M, N, K = size
+    g = U.gen(82)
+    A, B = ints(g, (M, K), 3, "e4m3"), ints(g, (N, K), 2, "e4m3")
+    sa, sb = powers(g, U.blocks(K), M), powers(g, U.blocks(K), U.blocks(N))
+    A[7, K - 1] = float("nan")
+    sa[0, 9] = float("nan")
+    B[N - 3, 5] = float("nan")
+    C = tss.gemm_fp8(*(t.to(CUDA) for t in (A, B, sa, sb)), fp32_sums=fp32_sums)
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[7] = want[9] = True
+    want[:, N - 3] = True
+    assert torch.equal(C.isnan().cpu(), want)
+
+
+def test_replayed_products_follow_their_inputs():
+    # K in ranges with one and two sets of waves, one round of 128 x 128 tiles, and pieces of a last round
+    g = U.gen(83)
+    cases = []
+    for M, N, K in ((513, 510, 8192), (1001, 1001, 4112), (1700, 1704, 272), (2101, 2105, 272)):
+        cases.append([t.to(CUDA) for t in (ints(g, (M, K), 3, "e4m3"), ints(g, (N, K), 2, "e4m3"), powers(g, U.blocks(K), M),
+                                           powers(g, U.blocks(K), U.blocks(N)))])
+
+    def step():
+        return [tss.gemm_fp8(*c, out_dtype=out, fp32_sums=s) for c in cases for out, s in (("f32", False), ("bf16", False), ("bf16", True))]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kept = step()
+    for _ in range(4):
+        for c in cases:
+            c[2].mul_(2)
+        graph.replay()
+        torch.cuda.synchronize()
+        for got, want in zip(kept, step()):
+            assert torch.equal(got, want)
