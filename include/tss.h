@@ -52,7 +52,8 @@ enum {
 /* ---- element types ------------------------------------------------------- */
 enum {
   TSS_F16 = 1, TSS_BF16 = 2, TSS_F32 = 3,
-  TSS_E4M3 = 4, TSS_E5M2 = 5  /* 8 bits, OCP: largest finite values 448 and 57344 */
+  TSS_E4M3 = 4, TSS_E5M2 = 5, /* 8 bits, OCP: largest finite values 448 and 57344 */
+  TSS_I8 = 6                  /* 8-bit integers, -127 .. 127 where the library writes them */
 };
 /* Added to the out_dtype of an 8-bit product: sums in fp32 throughout (TSS_F32 has them without it). */
 enum { TSS_F32_SUMS = 0x100 };
@@ -637,6 +638,133 @@ int64_t tss_rms_norm_backward_workspace_size(int64_t rows, int64_t d);
 int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, int32_t fp8,
                          int32_t block_rows, void *q, float *scale, void *stream);
 
+/*
+ * h = x + residual; y = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) *
+ * weight + bias, row by row.  residual and bias may be NULL.  y: out_dtype
+ * dtype, or TSS_I8 with scale[rows] (NULL otherwise): scale = max(largest |y|
+ * of the row, 1e-30) / 127, the value y / scale rounded to nearest even; of a
+ * row with a NaN or an infinity scale is not finite.  residual_out (may be
+ * NULL): h rounded to dtype; it may be residual or x itself.  y may be x when
+ * out_dtype is dtype.  mean, rstd (may be NULL): rows fp32, the mean and
+ * 1 / sqrt(...).  weight, bias: d elements of dtype.  d <= 32768; rows * d
+ * below about 2^35 and rows < 2^31 (a launch's threads).  x, residual, weight,
+ * bias, y and residual_out 16-byte aligned.  rows == 0: nothing to do.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_UNSUPPORTED (d),
+ * TSS_E_HIP.
+ */
+int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, const void *residual, const void *weight,
+                       const void *bias, float eps, int32_t out_dtype, void *y, float *scale, void *residual_out,
+                       float *mean, float *rstd, void *stream);
+
+/*
+ * Gradients of tss_layer_norm from dy, its h, mean and rstd:
+ *   dx = dh + rstd (g - mean(g) - xhat mean(g xhat)),  g = dy weight,  xhat = (h - mean) rstd
+ * (the gradient of x and of residual; dh, which may be NULL, is what arrives
+ * through residual_out), dweight[d] (fp32) = sum over rows of dy xhat and
+ * dbias[d] (fp32; may be NULL) = sum over rows of dy, added in a fixed order.
+ * dx may be dy or dh.  workspace: device memory of at least
+ * tss_layer_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned,
+ * scratch.  rows == 0: dweight and dbias are zero-filled.
+ * Errors: as tss_layer_norm; TSS_E_ARG for a missing or small workspace.
+ */
+int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
+                                const void *weight, const float *mean, const float *rstd, const void *dh, void *dx,
+                                float *dweight, float *dbias, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t tss_layer_norm_backward_workspace_size(int64_t rows, int64_t d);
+
+/*
+ * q (rows x d, 8-bit integers -127 .. 127) and scale[rows] from x, or with
+ * gated from silu(gate) * up in fp32 where x has rows of 2 d elements, gate
+ * then up: scale = max(largest |value| of the row, 1e-30) / 127, q = value /
+ * scale rounded to nearest even, as fp32 division rounds.  A row with a NaN or
+ * an infinity has that as its scale; its finite values are 0.  d <= 32768 (of q);
+ * x and q 16-byte aligned, scale 4-byte.  rows == 0: nothing to do.
+ * Errors: as tss_layer_norm.
+ */
+int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, void *q, float *scale,
+                          void *stream);
+
+/*
+ * The norm over n tensors, sqrt(sum of all elements' squares), to *norm (fp32,
+ * device memory), and, unless out is NULL, the tensors scaled to at most
+ * max_norm: out[i] = grads[i] * min(1, max_norm / (norm + 1e-6)), the product
+ * in fp32, rounded once.  The arrays grads, sizes (elements), dtypes (TSS_F16,
+ * TSS_BF16 or TSS_F32) and out are host memory and read before the call
+ * returns; what grads and out point to is device memory, each tensor without
+ * gaps and aligned to its elements (to 16 bytes for the full rate), out[i] of
+ * grads[i]'s type.  out[i] may be grads[i]; otherwise no output may overlap
+ * another output or an input.  Squares are added in 64 bits and a fixed order.
+ * A norm that is NaN makes every output NaN; an infinite one multiplies by 0.
+ * max_norm >= 0 (not read when out is NULL).  At most 2^40 elements in all.
+ * workspace: device memory of at least tss_clip_grad_norm_workspace_size(n,
+ * sizes) bytes, 8-byte aligned, scratch.  n == 0: the norm is 0.
+ * Errors: TSS_E_ARG (also overlapping outputs), TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_clip_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                           float max_norm, void *const *out, float *norm, void *workspace, int64_t workspace_bytes,
+                           void *stream);
+int64_t tss_clip_grad_norm_workspace_size(int64_t n, const int64_t *sizes);
+
+/* ---- rows sorted by expert -------------------------------------------------
+ * The router gives each of `tokens` tokens `top` choices; choice i = t * top +
+ * j.  There are tokens * top rows, sorted by expert (a token's choices of one
+ * expert in their order, and the experts' rows in the tokens' order).  A
+ * choice outside 0 .. E - 1 is dropped: it comes behind all routed rows.
+ */
+
+/*
+ * sizes[E]: rows of each expert (what the grouped products take).  row[tokens]
+ * [top]: each choice's row, for a dropped one the complement (~place, which is
+ * negative) of its place behind the routed rows.  choice[tokens * top]: each
+ * row's choice, behind the routed rows the complement of the dropped ones.
+ * expert: tokens x top integers of expert_bits (32 or 64) bits.  1 <= E <=
+ * 4096, tokens * top <= 2^30.  workspace: device memory of at least
+ * tss_sort_by_expert_workspace_size bytes, 4-byte aligned, scratch (may be
+ * NULL when that is 0).  tokens == 0: sizes is zero-filled.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE (expert_bits), TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_sort_by_expert(int64_t tokens, int64_t top, int64_t E, const void *expert, int32_t expert_bits,
+                           int32_t *sizes, int32_t *row, int32_t *choice, void *workspace, int64_t workspace_bytes,
+                           void *stream);
+int64_t tss_sort_by_expert_workspace_size(int64_t tokens, int64_t top, int64_t E);
+
+/*
+ * rows[row[t][j]] = x[t], the rows of dropped choices zero: x tokens x d of
+ * any of the library's types (TSS_I8 too), d a multiple of 8.  scale_blocks >
+ * 0: scale[scale_blocks][tokens] goes along, to scale_out[scale_blocks][tokens
+ * * top] (zero for dropped choices; choice is read for these only, and may be
+ * NULL without them).  x and rows 16-byte aligned; fewer than 2^32 pieces of 16
+ * (or, where a row is no multiple of 16 bytes, 8) bytes in x and scale rows.
+ * In every call here row must have been made for these tokens and top; entries
+ * past the rows count as dropped choices without a place.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_gather_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, const void *x, const int32_t *row,
+                        const int32_t *choice, void *rows, const float *scale, int64_t scale_blocks, float *scale_out,
+                        void *stream);
+
+/*
+ * y[t] = sum over j of weight[t][j] rows[row[t][j]] in fp32 and the order of
+ * j, rounded once; dropped choices' rows and weights are not read.  weight:
+ * fp32, or NULL for 1 (then y is the gradient of tss_gather_rows).  dtype (of
+ * rows) and out_dtype: the same of TSS_F16, TSS_BF16 and TSS_F32, or one of
+ * them TSS_F32.  rows and y 16-byte aligned, d a multiple of 8.
+ * Errors: as tss_gather_rows.
+ */
+int32_t tss_combine_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, const void *rows, const int32_t *row,
+                         const float *weight, int32_t out_dtype, void *y, void *stream);
+
+/*
+ * Gradients of tss_combine_rows: drows[row[t][j]] = weight[t][j] dy[t] (dtype;
+ * dropped choices' rows zero) and dweight[t][j] (fp32) = <dy[t],
+ * rows[row[t][j]]> (dropped: zero).  dtype: of dy and drows; rows_dtype: dtype
+ * or TSS_F32.  drows may be rows when the types are the same.  d <= 32768.
+ * Errors: as tss_gather_rows, TSS_E_UNSUPPORTED (d).
+ */
+int32_t tss_combine_rows_backward(int64_t tokens, int64_t top, int64_t d, int32_t dtype, const void *dy,
+                                  int32_t rows_dtype, const void *rows, const int32_t *row, const float *weight,
+                                  void *drows, float *dweight, void *stream);
+
 /* ---- 8-bit and grouped products -------------------------------------------- */
 
 /*
@@ -664,6 +792,23 @@ int32_t tss_gemm_fp8(int64_t M, int64_t N, int64_t K, int32_t a_dtype, const voi
                      const float *sb, int32_t b_block_rows, void *C, int32_t out_dtype, void *workspace,
                      int64_t workspace_bytes, void *stream);
 int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * C = (A sa) (B sb)^T on 8-bit integers: A is M x K with sa[M], B is N x K
+ * with sb[N], any values -128 .. 127; C is M x N, out_dtype TSS_F16, TSS_BF16
+ * or TSS_F32.  The sums over K are exact (32-bit integers); each is rounded to
+ * fp32, multiplied by sa and then by sb, and rounded to out_dtype.
+ * workspace: tss_gemm_int8_workspace_size(M, N, K) bytes of device memory (the
+ * partial sums of a product whose K is split over workgroups; may be NULL when
+ * that is 0), 16-byte aligned, scratch.
+ * K a multiple of 16 below 2^17, any M and N; A, B, C 16-byte aligned, sa and
+ * sb 4-byte; A and B below 2 GiB each; fewer than 2^23 tiles of 64 x 128 of C.
+ * M == 0 or N == 0: nothing to do.  K == 0: C is zero-filled.
+ * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ */
+int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void *B, const float *sa, const float *sb,
+                      void *C, int32_t out_dtype, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t tss_gemm_int8_workspace_size(int64_t M, int64_t N, int64_t K);
 
 /*
  * Products grouped by expert: the T rows of A (and C) are sorted by group,

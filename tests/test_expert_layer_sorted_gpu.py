@@ -1,0 +1,120 @@
+"""The expert layer whose rows the library sorts, gathers and joins, as it is
+used: an 8-bit forward pass, training steps with either norm, clipped, and a
+shared expert in 8-bit integers, against the same layer in float64."""
+import pytest
+import torch
+
+from tile_size_selection_amd import expert_layer as X
+
+pytestmark = pytest.mark.gpu
+
+CUDA = torch.device("cuda:0")
+BF16 = torch.bfloat16
+
+
+class Data:
+    def __init__(self, seed, tokens=150, width=272, hidden=144, experts=6, top=3):
+        g = torch.Generator()
+        g.manual_seed(seed)
+        normal = lambda *s: torch.randn(*s, generator=g, dtype=torch.float64)  # noqa: E731
+        self.x, self.residual, self.dout, self.dh = (normal(tokens, width).to(BF16) for _ in range(4))
+        self.norm, self.bias = (1 + 0.2 * normal(width)).to(BF16), (0.2 * normal(width)).to(BF16)
+        self.w1 = (normal(experts, width, 2 * hidden) / width ** 0.5).to(BF16)
+        self.w2 = (normal(experts, hidden, width) / hidden ** 0.5).to(BF16)
+        self.expert = torch.topk(normal(tokens, experts - 1), top, 1).indices  # the last expert gets no rows
+        self.expert[torch.rand(tokens, top, generator=g) < 0.1] = -1
+        self.weight = torch.softmax(normal(tokens, top), 1).float()
+        self.dev = {k: v.to(CUDA) for k, v in vars(self).items()}
+
+    def args(self):
+        return [self.dev[k] for k in ("x", "residual", "norm", "w1", "w2", "expert", "weight")]
+
+
+def off(got, want):
+    return float((got.double().cpu() - want.detach()).norm() / want.detach().norm())
+
+
+@pytest.mark.parametrize("layer_norm", [False, True])
+def test_training_step(layer_norm):
+    s = Data(3)
+    bias = s.dev["bias"] if layer_norm else None
+    leaves = [t.double().requires_grad_() for t in (s.x, s.norm, s.w1, s.w2, s.weight)]
+    b = s.bias.double().requires_grad_() if layer_norm else None
+    out, h = X.reference(leaves[0], s.residual.double(), leaves[1], leaves[2], leaves[3], s.expert, leaves[4],
+                         1e-5 if layer_norm else 1e-6, b)
+    grads = torch.autograd.grad([out, h], leaves + ([b] if layer_norm else []), [s.dout.double(), s.dh.double()])
+
+    got, got_h, kept = X.forward_sorted(*s.args(), bias)
+    g = X.backward_sorted(s.dev["dout"], s.dev["dh"], s.dev["norm"], s.dev["w1"], s.dev["w2"], s.dev["weight"], kept)
+    pairs = [("out", got, out), ("h", got_h, h), ("dx", g.x, grads[0]), ("dnorm", g.norm, grads[1]), ("dW1", g.w1, grads[2]),
+             ("dW2", g.w2, grads[3]), ("dweight", g.weight, grads[4])] + ([("dbias", g.bias, grads[5])] if layer_norm else [])
+    # a chain of at most 8 roundings to bf16 (2^-8 each, and of random signs over the norm)
+    for what, a, want in pairs:
+        assert off(a, want) <= 8 * 2.0 ** -8, what
+    assert (g.w1[-1] == 0).all() and (g.w2[-1] == 0).all() and (g.weight[s.dev["expert"] < 0] == 0).all()
+
+    params = [grads[1], grads[2], grads[3]] + ([grads[5]] if layer_norm else [])
+    total = float(torch.stack([t.norm() for t in params]).norm())
+    again, clipped, norm = X.train_step(*s.args(), s.dev["dout"], s.dev["dh"], total / 4, bias)
+    assert torch.equal(again, got) and abs(float(norm) - total) <= 8 * 2.0 ** -8 * total
+    for a, want in ((clipped.norm, g.norm), (clipped.w1, g.w1), (clipped.w2, g.w2)):
+        assert torch.allclose(a, want * (total / 4 / float(norm)), rtol=2.0 ** -21, atol=0)
+    assert torch.equal(clipped.x, g.x) and torch.equal(clipped.weight, g.weight)
+
+
+def test_8_bit_forward_passes():
+    s = Data(5)
+    out, h = X.reference(s.x.double(), s.residual.double(), s.norm.double(), s.w1.double(), s.w2.double(), s.expert, s.weight.double())
+    w8 = X.quantize_weights(s.dev["norm"], s.dev["w1"], s.dev["w2"])
+    got, got_h = X.forward_fp8_sorted(s.dev["x"], s.dev["residual"], w8, s.dev["expert"], s.dev["weight"])
+    # 8 bits: four roundings to e4m3 (2^-4 each)
+    assert off(got, out) <= 4 * 2.0 ** -4 and off(got_h, h) <= 2.0 ** -8
+    old, _ = X.forward_fp8(s.dev["x"], s.dev["residual"], w8, X.route(s.dev["expert"], s.dev["weight"], 6))
+    # the same rows and products; the sums in fp32 in the same order, with one rounding fewer a term
+    assert ((got.double() - old.double()).abs() <= old.double().abs() * 2.0 ** -7 + 1e-5).all()
+
+
+def test_shared_expert():
+    s = Data(7)
+    one = torch.zeros(150, 1, dtype=torch.int64)
+    out, h = X.reference(s.x.double(), s.residual.double(), s.norm.double(), s.w1[:1].double(), s.w2[:1].double(), one,
+                         torch.ones(150, 1, dtype=torch.float64), 1e-5, s.bias.double())
+    w = X.quantize_shared(s.dev["norm"], s.dev["bias"], s.dev["w1"][0], s.dev["w2"][0])
+    got, got_h = X.shared_int8(s.dev["x"], s.dev["residual"], w)
+    # four roundings to int8: half a step of a row's largest / 127, a sixth of 1 / 127 over a row whose largest is at most
+    # six times its spread: 6 / 127 / sqrt(12) each
+    assert off(got, out) <= 4 * 6 / 127 / 12 ** 0.5 and off(got_h, h) <= 2.0 ** -8
+    assert torch.equal(X.shared_int8(s.dev["x"], s.dev["residual"], w)[0], got)
+
+
+def test_no_tokens():
+    s = Data(9, tokens=0)
+    out, h, kept = X.forward_sorted(*s.args())
+    g = X.backward_sorted(s.dev["dout"], s.dev["dh"], s.dev["norm"], s.dev["w1"], s.dev["w2"], s.dev["weight"], kept)
+    assert out.shape == (0, 272) and g.x.shape == (0, 272) and (g.w1 == 0).all() and (g.norm == 0).all()
+
+
+def test_a_step_in_a_graph():
+    """Both passes and the clipping captured once; replays on new tokens and choices give an eager step's bits."""
+    s = Data(11)
+
+    def step():
+        out, g, norm = X.train_step(*s.args(), s.dev["dout"], s.dev["dh"], 1.0, s.dev["bias"])
+        return [out, norm, *g]
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for seed in (13, 14, 15):
+        new = Data(seed).dev
+        for k in ("x", "residual", "expert", "weight", "dout"):
+            s.dev[k].copy_(new[k])
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want))

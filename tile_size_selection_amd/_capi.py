@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(_HERE, "libtss.so")
 TSS_OK, TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_INFEASIBLE, TSS_E_HIP, TSS_E_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
 TSS_E_SCRATCH = -7
 TSS_SCRATCH_BYTES = 64 << 20
-TSS_F16, TSS_BF16, TSS_F32, TSS_E4M3, TSS_E5M2 = 1, 2, 3, 4, 5
+TSS_F16, TSS_BF16, TSS_F32, TSS_E4M3, TSS_E5M2, TSS_I8 = 1, 2, 3, 4, 5, 6
 TSS_F32_SUMS = 0x100
 LDS_PATTERN = {"b32": 1, "b128": 2, "tr_b64": 3, "gemm_a": 4, "gemm_a_plain": 5, "gemm_b": 6, "gemm_b_plain": 7}
 INSTR = {"mfma32": 1, "mfma16": 2, "mma": 16, "wgmma": 17, "simt": 18}
@@ -70,7 +70,11 @@ EXPORTS = ["tss_device_gfx950", "tss_device_pages", "tss_device_query", "tss_eva
            "tss_splitk_plan", "tss_conv_splitk_plan", "tss_conv2d_splitk_noalloc",
            "tss_rms_norm", "tss_rms_norm_backward", "tss_rms_norm_backward_workspace_size", "tss_quantize_fp8",
            "tss_gemm_fp8", "tss_gemm_fp8_workspace_size", "tss_gemm_grouped", "tss_gemm_grouped_backward",
-           "tss_gemm_grouped_fp8"]
+           "tss_gemm_grouped_fp8",
+           "tss_layer_norm", "tss_layer_norm_backward", "tss_layer_norm_backward_workspace_size", "tss_quantize_int8",
+           "tss_gemm_int8", "tss_gemm_int8_workspace_size", "tss_clip_grad_norm", "tss_clip_grad_norm_workspace_size",
+           "tss_sort_by_expert", "tss_sort_by_expert_workspace_size", "tss_gather_rows", "tss_combine_rows",
+           "tss_combine_rows_backward"]
 
 _lib = None
 
@@ -124,6 +128,19 @@ def lib():
     L.tss_gemm_grouped.argtypes = [i64] * 4 + [i32, vp, vp, vp, vp, i32, vp]
     L.tss_gemm_grouped_backward.argtypes = [i64] * 4 + [i32] + [vp] * 6 + [i32, vp]
     L.tss_gemm_grouped_fp8.argtypes = [i64] * 4 + [i32] + [vp] * 6 + [i32, vp]
+    L.tss_layer_norm.argtypes = [i64, i64, i32] + [vp] * 4 + [ctypes.c_float, i32] + [vp] * 6
+    L.tss_layer_norm_backward.argtypes = [i64, i64, i32] + [vp] * 10 + [i64, vp]
+    L.tss_layer_norm_backward_workspace_size.argtypes = [i64, i64]
+    L.tss_quantize_int8.argtypes = [i64, i64, i32, vp, i32, vp, vp, vp]
+    L.tss_gemm_int8.argtypes = [i64, i64, i64] + [vp] * 5 + [i32, vp, i64, vp]
+    L.tss_gemm_int8_workspace_size.argtypes = [i64, i64, i64]
+    L.tss_clip_grad_norm.argtypes = [i64, P(vp), P(i64), P(i32), ctypes.c_float, P(vp), vp, vp, i64, vp]
+    L.tss_clip_grad_norm_workspace_size.argtypes = [i64, P(i64)]
+    L.tss_sort_by_expert.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i64, vp]
+    L.tss_sort_by_expert_workspace_size.argtypes = [i64, i64, i64]
+    L.tss_gather_rows.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.tss_combine_rows.argtypes = [i64, i64, i64, i32, vp, vp, vp, i32, vp, vp]
+    L.tss_combine_rows_backward.argtypes = [i64, i64, i64, i32, vp, i32] + [vp] * 6
     L.tss_status_string.argtypes = [i32]
     L.tss_status_string.restype = ctypes.c_char_p
     for n in EXPORTS:
@@ -135,6 +152,10 @@ def lib():
     L.tss_conv2d_nhwc_workspace_size.restype = i64
     L.tss_rms_norm_backward_workspace_size.restype = i64
     L.tss_gemm_fp8_workspace_size.restype = i64
+    L.tss_layer_norm_backward_workspace_size.restype = i64
+    L.tss_gemm_int8_workspace_size.restype = i64
+    L.tss_clip_grad_norm_workspace_size.restype = i64
+    L.tss_sort_by_expert_workspace_size.restype = i64
     _lib = L
     return L
 

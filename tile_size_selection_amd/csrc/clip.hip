@@ -1,0 +1,305 @@
+// The norm over many tensors, and the tensors scaled to at most a given norm:
+//
+//   norm = sqrt(sum of all elements' squares),  out = g * min(1, max_norm / (norm + 1e-6))
+//
+// Bound by memory: every element is read for the norm, and read again and
+// written to be scaled.  Squares are added in 64 bits: their sum neither
+// overflows nor loses what many elements add to few, and the rate of 64-bit
+// FMAs is far above memory's.  Each workgroup adds a piece of a tensor, the
+// pieces' sums are added in a fixed order by every workgroup that scales (the
+// same bits on every run, and one launch fewer than with a pass of its own).
+// The tensors' addresses travel in the kernel's arguments, kTable at a time:
+// no copy from host memory, so a captured graph holds all that it needs.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "row_launch.h"
+
+using namespace tss;
+
+namespace {
+
+constexpr int kTable = 128;
+constexpr int kClipThreads = 256;
+constexpr float kNormEps = 1e-6f;
+
+struct ClipTable {
+  const void *in[kTable];
+  void *out[kTable];
+  int64_t n[kTable];
+  uint32_t first[kTable + 1];  // a tensor's first piece, in this table
+  uint8_t type[kTable];
+  int32_t count;
+  int32_t piece;               // elements of a piece, a multiple of 2048
+  uint32_t base;               // the table's first piece among all
+};
+static_assert(sizeof(ClipTable) <= 3840, "kernel arguments are 4 KiB");
+
+// The tensor that piece `at` of the table belongs to (its index is uniform over the workgroup).
+__device__ __forceinline__ int tensor_of(const ClipTable &t, uint32_t at) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= at) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ double sum64d(double v) {
+#pragma unroll
+  for (int m = 1; m < 64; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Sum over the workgroup, to every thread; red: one slot a wave.
+__device__ __forceinline__ double group_sum(double v, double *red) {
+  v = sum64d(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = 0;
+#pragma unroll
+  for (int i = 0; i < kClipThreads / 64; ++i) s += red[i];
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ double piece_squares(const T *g, int64_t from, int64_t end, bool wide) {
+  double s = 0;
+  if (wide) {
+    const int64_t whole = from + (end - from) / 8 * 8;
+    int64_t i = from + threadIdx.x * 8;
+    for (; i + 3 * kClipThreads * 8 < whole; i += 4 * kClipThreads * 8) {
+      Raw8<T> r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float f[8];
+        widen8(r[u], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) s = __builtin_fma(double(f[k]), double(f[k]), s);
+      }
+    }
+    for (; i < whole; i += kClipThreads * 8) {
+      float f[8];
+      widen8(load8(g + i), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s = __builtin_fma(double(f[k]), double(f[k]), s);
+    }
+    from = whole;
+  }
+  for (int64_t i = from + threadIdx.x; i < end; i += kClipThreads) {
+    const double f = double(float(g[i]));
+    s = __builtin_fma(f, f, s);
+  }
+  return s;
+}
+
+template <typename T>
+__device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, int64_t end, bool wide, float factor) {
+  if (wide) {
+    const int64_t whole = from + (end - from) / 8 * 8;
+    int64_t i = from + threadIdx.x * 8;
+    for (; i + 3 * kClipThreads * 8 < whole; i += 4 * kClipThreads * 8) {
+      Raw8<T> r[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float f[8];
+        widen8(r[u], f);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[k] *= factor;
+        store8(out + i + u * kClipThreads * 8, f);
+      }
+    }
+    for (; i < whole; i += kClipThreads * 8) {
+      float f[8];
+      widen8(load8(g + i), f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[k] *= factor;
+      store8(out + i, f);
+    }
+    from = whole;
+  }
+  for (int64_t i = from + threadIdx.x; i < end; i += kClipThreads) out[i] = (T)(float(g[i]) * factor);
+}
+
+// f(element type, tensor's index, first element, end) of piece `at`.
+template <typename F>
+__device__ __forceinline__ void with_piece(const ClipTable &t, uint32_t at, F f) {
+  const int k = tensor_of(t, at);
+  const int64_t from = int64_t(at - t.first[k]) * t.piece, end = min(t.n[k], from + t.piece);
+  if (t.type[k] == TSS_F32) f(float{}, k, from, end);
+  else if (t.type[k] == TSS_F16) f(_Float16{}, k, from, end);
+  else f(__bf16{}, k, from, end);
+}
+
+__device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+__global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(ClipTable t, double *partial) {
+  __shared__ double red[kClipThreads / 64];
+  double s = 0;
+  with_piece(t, blockIdx.x, [&](auto v, int k, int64_t from, int64_t end) {
+    using T = decltype(v);
+    s = piece_squares(static_cast<const T *>(t.in[k]), from, end, aligned16(t.in[k]));
+  });
+  s = group_sum(s, red);
+  if (threadIdx.x == 0) partial[t.base + blockIdx.x] = s;
+}
+
+// All pieces' sums, in a fixed order.
+__device__ __forceinline__ double total_squares(const double *partial, uint32_t pieces, double *red) {
+  double s = 0;
+  for (uint32_t i = threadIdx.x; i < pieces; i += kClipThreads) s += partial[i];
+  return group_sum(s, red);
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *partial, uint32_t pieces, float *norm) {
+  __shared__ double red[kClipThreads / 64];
+  const double s = total_squares(partial, pieces, red);
+  if (threadIdx.x == 0) *norm = float(sqrt(s));
+}
+
+__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t, const double *partial, uint32_t pieces,
+                                                                  uint32_t in_table, float max_norm, float *norm) {
+  __shared__ double red[kClipThreads / 64];
+  const double n = sqrt(total_squares(partial, pieces, red));
+  if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(n);
+  const double q = double(max_norm) / (n + double(kNormEps));
+  const float factor = q > 1 ? 1.0f : float(q);  // a NaN comes through
+  // The last pieces first: the norm's pass has left them in the caches.
+  for (uint32_t i = blockIdx.x; i < in_table; i += gridDim.x)
+    with_piece(t, in_table - 1 - i, [&](auto v, int k, int64_t from, int64_t end) {
+      using T = decltype(v);
+      if (factor == 1.0f && t.out[k] == t.in[k]) return;
+      piece_scale(static_cast<const T *>(t.in[k]), static_cast<T *>(t.out[k]), from, end,
+                  aligned16(t.in[k]) && aligned16(t.out[k]), factor);
+    });
+}
+
+int bytes_of(int32_t dtype) { return dtype == TSS_F32 ? 4 : dtype == TSS_F16 || dtype == TSS_BF16 ? 2 : 0; }
+
+// Elements of a piece: about 2048 pieces in all (eight workgroups a CU), of at least 4096 elements.
+struct Pieces {
+  int64_t piece, count;
+};
+int32_t cut(int64_t n, const int64_t *sizes, Pieces *out) {
+  if (n < 0 || n > INT32_MAX || (n > 0 && !sizes)) return TSS_E_ARG;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (sizes[i] < 0 || sizes[i] > int64_t(1) << 40) return TSS_E_ARG;
+    total += sizes[i];
+    if (total > int64_t(1) << 40) return TSS_E_ARG;
+  }
+  int64_t piece = (total / 2048 + 2047) / 2048 * 2048;
+  if (piece < 4096) piece = 4096;
+  if (piece > int64_t(1) << 30) return TSS_E_ARG;
+  int64_t count = 0;
+  for (int64_t i = 0; i < n; ++i) count += (sizes[i] + piece - 1) / piece;
+  if (count > int64_t(1) << 24) return TSS_E_ARG;
+  *out = {piece, count};
+  return TSS_OK;
+}
+
+// An output may be its own input; apart from that no output overlaps another
+// output or an input.
+bool overlapping(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int32_t *types) {
+  struct Span {
+    uintptr_t begin, end;
+    bool written;
+  };
+  std::vector<Span> spans;
+  spans.reserve(size_t(2 * n));
+  for (int64_t i = 0; i < n; ++i) {
+    if (sizes[i] == 0) continue;
+    const uintptr_t bytes = uintptr_t(sizes[i]) * bytes_of(types[i]);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), b = reinterpret_cast<uintptr_t>(out[i]);
+    spans.push_back({b, b + bytes, true});
+    if (a != b) spans.push_back({a, a + bytes, false});
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span &a, const Span &b) { return a.begin < b.begin; });
+  uintptr_t written = 0, read = 0;  // the furthest ends so far
+  for (const Span &s : spans) {
+    if (s.begin < written || (s.written && s.begin < read)) return true;
+    (s.written ? written : read) = std::max(s.written ? written : read, s.end);
+  }
+  return false;
+}
+
+int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes, float max_norm,
+             void *const *out, float *norm, void *workspace, int64_t workspace_bytes, hipStream_t s) {
+  Pieces c;
+  const int32_t st = cut(n, sizes, &c);
+  if (st != TSS_OK) return st;
+  if (!norm || (n > 0 && (!grads || !dtypes))) return TSS_E_ARG;
+  if (out && !(max_norm >= 0)) return TSS_E_ARG;
+  for (int64_t i = 0; i < n; ++i) {
+    const int size = bytes_of(dtypes[i]);
+    if (!size) return TSS_E_DTYPE;
+    if (sizes[i] > 0 && (!grads[i] || (out && !out[i]))) return TSS_E_ARG;
+    if (reinterpret_cast<uintptr_t>(grads[i]) % size || (out && reinterpret_cast<uintptr_t>(out[i]) % size)) return TSS_E_ALIGN;
+  }
+  if (reinterpret_cast<uintptr_t>(norm) % 4 || reinterpret_cast<uintptr_t>(workspace) % 8) return TSS_E_ALIGN;
+  if (c.count && (!workspace || workspace_bytes < c.count * 8)) return TSS_E_ARG;
+  if (out && overlapping(n, grads, out, sizes, dtypes)) return TSS_E_ARG;
+  double *partial = static_cast<double *>(workspace);
+  // f(table, its pieces) for the tensors, kTable at a time; empty ones are left out
+  auto tables = [&](auto f) {
+    ClipTable t{};
+    t.piece = int32_t(c.piece);
+    uint32_t done = 0;
+    for (int64_t i = 0; i <= n; ++i) {
+      if (i < n && sizes[i] > 0) {
+        const int k = t.count++;
+        t.in[k] = grads[i];
+        t.out[k] = out ? out[i] : nullptr;
+        t.n[k] = sizes[i];
+        t.type[k] = uint8_t(dtypes[i]);
+        t.first[k + 1] = t.first[k] + uint32_t((sizes[i] + c.piece - 1) / c.piece);
+      }
+      if (t.count == kTable || (i == n && t.count)) {
+        t.base = done;
+        f(t, t.first[t.count]);
+        done += t.first[t.count];
+        t.count = 0;
+      }
+    }
+  };
+  tables([&](const ClipTable &t, uint32_t pieces) {
+    hipLaunchKernelGGL(clip_squares_kernel, dim3(pieces), dim3(kClipThreads), 0, s, t, partial);
+  });
+  if (!out || c.count == 0) {
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kClipThreads), 0, s, partial, uint32_t(c.count), norm);
+  } else {
+    tables([&](const ClipTable &t, uint32_t pieces) {
+      hipLaunchKernelGGL(clip_scale_kernel, dim3(pieces < 2048 ? pieces : 2048), dim3(kClipThreads), 0, s, t, partial,
+                         uint32_t(c.count), pieces, max_norm, norm);
+    });
+  }
+  return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t tss_clip_grad_norm_workspace_size(int64_t n, const int64_t *sizes) {
+  Pieces c;
+  const int32_t st = cut(n, sizes, &c);
+  return st != TSS_OK ? st : c.count * 8;
+}
+
+int32_t tss_clip_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
+                           float max_norm, void *const *out, float *norm, void *workspace, int64_t workspace_bytes,
+                           void *stream) {
+  try {
+    return clip(n, grads, sizes, dtypes, max_norm, out, norm, workspace, workspace_bytes, static_cast<hipStream_t>(stream));
+  } catch (const std::bad_alloc &) {
+    return TSS_E_ARG;
+  }
+}
+
+}  // extern "C"

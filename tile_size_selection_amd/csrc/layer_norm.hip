@@ -1,0 +1,394 @@
+// Layer norm of x + residual and its gradients.
+//
+//   h = x + residual                        (fp32; written rounded to x's type)
+//   m = mean(h),  r = 1 / sqrt(mean((h - m)^2) + eps)
+//   y = (h - m) r w + b                     (from the fp32 h; x's type, or int8 with a scale for the row)
+//
+// With xhat = (h - m) r and g = dy w:
+//   dx = dh + r (g - mean(g) - xhat mean(g xhat))   (= the residual's gradient)
+//   dw = sum over rows of dy xhat,  db = sum over rows of dy
+//
+// Both are bound by memory: every element is read and written once and stays
+// in registers between the row's reductions and its output.  The squares are
+// summed about a first mean; the mean's own error, which that second sum
+// shows, is taken out again, so that a mean far from zero costs no digits.
+#include "row_launch.h"
+
+using namespace tss;
+
+namespace {
+
+// ---- forward ----
+
+struct NormArgs {
+  int rows, d, wpr;
+  const void *x, *residual, *weight, *bias;
+  float eps;
+  void *y;
+  float *scale;
+  void *h;
+  float *mean, *rstd;
+};
+
+// A row is held by L neighbouring lanes, or (L == 64) by wpr waves, one row
+// per workgroup where wpr > 1; lane t of it holds columns (c * lanes + t) * 8
+// .. + 7 for c < CH.
+template <typename T, bool INT8, int CH, int L>
+__global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
+  __shared__ float red[4][kMaxThreads / 64];
+  const int wave = threadIdx.x >> 6, wpr = L == 64 ? p.wpr : 1;
+  const int lanes = L * wpr;
+  const int t = L < 64 ? threadIdx.x % L : wpr == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int row = xcd_run(blockIdx.x, gridDim.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
+  if (row >= p.rows) return;  // wpr > 1: one row, the whole workgroup
+  const int d = p.d;
+  const int64_t base = int64_t(row) * d;
+  const T *x = static_cast<const T *>(p.x), *residual = static_cast<const T *>(p.residual);
+  const T *weight = static_cast<const T *>(p.weight), *bias = static_cast<const T *>(p.bias);
+  auto col_of = [&](int c) __attribute__((always_inline)) { return (c * lanes + t) * 8; };
+  // sums over the row; `slot`: each use its own
+  auto row_sum = [&](float v, int slot) __attribute__((always_inline)) {
+    v = sum_lanes<L>(v);
+    if (L < 64 || wpr == 1) return v;
+    if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
+    __syncthreads();
+    float s = 0;
+    for (int i = 0; i < wpr; ++i) s += red[slot][i];
+    return s;
+  };
+
+  Raw8<T> xr[CH], rr[CH], wr[CH], br[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = col_of(c);
+    const bool in = col < d;
+    xr[c] = in ? load8(x + base + col) : zero8<T>();
+    rr[c] = in && residual ? load8(residual + base + col) : zero8<T>();
+    wr[c] = in ? load8(weight + col) : zero8<T>();
+    br[c] = in && bias ? load8(bias + col) : zero8<T>();
+  }
+  float h[CH][8], sum = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    widen8(xr[c], h[c]);
+    if (residual) {
+      float r[8];
+      widen8(rr[c], r);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+    }
+    if (p.h && col_of(c) < d) store8(static_cast<T *>(p.h) + base + col_of(c), h[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum += h[c][i];
+  }
+  const float inv_d = 1.0f / float(d);
+  const float mean0 = row_sum(sum, 0) * inv_d;
+  float rest = 0, sq = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const bool in = col_of(c) < d;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[c][i] = in ? h[c][i] - mean0 : 0.0f;
+      rest += h[c][i];
+      sq += h[c][i] * h[c][i];
+    }
+  }
+  const float off = row_sum(rest, 1) * inv_d;  // the mean of h - mean0: what mean0 lacks
+  const float var = fmaxf(row_sum(sq, 2) * inv_d - off * off, 0.0f);
+  // a NaN in the row has to come through the max above
+  const float r = var == var && off == off ? 1.0f / __builtin_sqrtf(var + p.eps) : off;
+  if (t == 0) {
+    if (p.mean) p.mean[row] = mean0 + off;
+    if (p.rstd) p.rstd[row] = r;
+  }
+  float amax = 0;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    float w[8], b[8];
+    widen8(wr[c], w);
+    widen8(br[c], b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      h[c][i] = (h[c][i] - off) * r * w[i] + b[i];
+      if constexpr (INT8) amax = max_abs(amax, h[c][i]);  // columns past the row: w = b = 0
+    }
+    if constexpr (!INT8)
+      if (col_of(c) < d) store8(static_cast<T *>(p.y) + base + col_of(c), h[c]);
+  }
+  if constexpr (INT8) {
+    amax = max_lanes<L>(amax);
+    if (L == 64 && wpr > 1) {
+      if ((threadIdx.x & 63) == 0) red[3][wave] = amax;
+      __syncthreads();
+      for (int i = 0; i < wpr; ++i) amax = __builtin_elementwise_maximum(amax, red[3][i]);
+    }
+    const BlockScale<I8> s(amax);
+    if (t == 0) p.scale[row] = s.scale;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (col_of(c) < d)
+        *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(p.y) + base + col_of(c)) = pack8(h[c], s);
+  }
+}
+
+template <typename T, bool INT8>
+int32_t launch_norm(const NormArgs &a, hipStream_t s) {
+  const Team f = team_of(a.d, a.rows < 1024 ? 1 : 4);
+  const int block = f.waves == 1 ? 256 : f.waves * 64, rpb = f.waves == 1 ? 256 / f.lanes : 1;
+  const int64_t blocks = (int64_t(a.rows) + rpb - 1) / rpb;
+  if (blocks * block > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
+  NormArgs p = a;
+  p.wpr = f.waves;
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(block), 0, s, p); };
+  if (f.lanes == 8) go(layer_norm_kernel<T, INT8, 1, 8>);
+  else if (f.lanes == 16) go(layer_norm_kernel<T, INT8, 1, 16>);
+  else if (f.lanes == 32) go(layer_norm_kernel<T, INT8, 1, 32>);
+  else if (f.chunks == 1) go(layer_norm_kernel<T, INT8, 1, 64>);
+  else if (f.chunks == 2) go(layer_norm_kernel<T, INT8, 2, 64>);
+  else go(layer_norm_kernel<T, INT8, 4, 64>);
+  return TSS_OK;
+}
+
+// ---- backward ----
+
+struct BackArgs {
+  int rows, d;
+  const void *dy, *h, *weight;
+  const float *mean, *rstd;
+  const void *dh;
+  void *dx;
+  float *partial;  // [2][workgroups][d]: shares of dw and of db
+};
+
+constexpr int kNarrowThreads = 256;
+
+// Teams of L lanes, or (L == 64) the whole workgroup, take a row each, a
+// launch's teams apart; a lane keeps its columns' shares of dw and db in
+// registers over its rows, a workgroup joins its teams' and writes them to its
+// own slice of the workspace (added up in a fixed order afterwards: no
+// atomics, the same bits on every run).  D rows' loads are in flight while a
+// row is reduced and written.
+template <typename T, int CH, int D, int L>
+__global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_norm_backward_kernel(BackArgs p) {
+  constexpr bool kNarrow = L < 64;
+  __shared__ float red[2][2][kMaxThreads / 64];
+  const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  const int lanes = kNarrow ? L : int(blockDim.x), t = threadIdx.x % lanes;
+  const int teams = kNarrow ? kNarrowThreads / L : 1;
+  const int stride = gridDim.x * teams, first = blockIdx.x * teams + threadIdx.x / lanes;
+  const int rows = p.rows, d = p.d;
+  const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
+  T *dx = static_cast<T *>(p.dx);
+  auto col_of = [&](int c) __attribute__((always_inline)) { return (c * lanes + t) * 8; };
+  float w[CH][8], dw[CH][8], db[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    widen8(col_of(c) < d ? load8(static_cast<const T *>(p.weight) + col_of(c)) : zero8<T>(), w[c]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0;
+  }
+  Raw8<T> a[D][CH], b[D][CH], e[D][CH];
+  float mean[D], rstd[D];
+  auto load_row = [&](int s, int64_t row) __attribute__((always_inline)) {
+    const int64_t base = row * d;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const int col = col_of(c);
+      const bool in = col < d && row < rows;
+      a[s][c] = in ? load8(dy + base + col) : zero8<T>();
+      b[s][c] = in ? load8(hh + base + col) : zero8<T>();
+      e[s][c] = in && dh ? load8(dh + base + col) : zero8<T>();
+    }
+    mean[s] = row < rows ? p.mean[row] : 0.0f;
+    rstd[s] = row < rows ? p.rstd[row] : 0.0f;
+  };
+#pragma unroll
+  for (int s = 0; s < D; ++s) load_row(s, int64_t(first) + int64_t(s) * stride);
+  const float inv_d = 1.0f / float(d);
+  int slot = 0;
+  for (int64_t row0 = first; row0 < rows; row0 += int64_t(D) * stride) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      const int64_t row = row0 + int64_t(s) * stride;
+      if (row >= rows) break;
+      const float m = mean[s], r = rstd[s];
+      Raw8<T> ca[CH], cb[CH], ce[CH];
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        ca[c] = a[s][c];
+        cb[c] = b[s][c];
+        ce[c] = e[s][c];
+      }
+      load_row(s, row + int64_t(D) * stride);
+      float sg = 0, sx = 0;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        float g[8], x[8];
+        widen8(ca[c], g);
+        widen8(cb[c], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // columns past the row: g = w = 0
+          const float gx = (x[i] - m) * r * g[i];
+          dw[c][i] += gx;
+          db[c][i] += g[i];
+          sg += g[i] * w[c][i];
+          sx += gx * w[c][i];
+        }
+      }
+      sg = sum_lanes<L>(sg);
+      sx = sum_lanes<L>(sx);
+      if (!kNarrow && nw > 1) {
+        // two sets of slots: a wave writes the next row's while others may still read this row's
+        if ((threadIdx.x & 63) == 0) {
+          red[slot][0][wave] = sg;
+          red[slot][1][wave] = sx;
+        }
+        __syncthreads();
+        sg = sx = 0;
+        for (int i = 0; i < nw; ++i) {
+          sg += red[slot][0][i];
+          sx += red[slot][1][i];
+        }
+        slot ^= 1;
+      }
+      sg *= inv_d;
+      sx *= inv_d;
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        if (col_of(c) >= d) continue;
+        float g[8], x[8], o[8];
+        widen8(ca[c], g);
+        widen8(cb[c], x);
+        widen8(ce[c], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[c][i] - sg - (x[i] - m) * r * sx);
+        store8(dx + row * d + col_of(c), o);
+      }
+    }
+  }
+  float *pw = p.partial + int64_t(blockIdx.x) * d, *pb = pw + int64_t(gridDim.x) * d;
+  if constexpr (kNarrow) {
+    // the lanes of a wave that hold the same columns, then the waves in order
+    __shared__ float join[2][kNarrowThreads / 64][L * 8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int k = L; k < 64; k *= 2) {
+        dw[0][i] += __shfl_xor(dw[0][i], k);
+        db[0][i] += __shfl_xor(db[0][i], k);
+      }
+      if ((threadIdx.x & 63) < L) {
+        join[0][wave][t * 8 + i] = dw[0][i];
+        join[1][wave][t * 8 + i] = db[0][i];
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += kNarrowThreads) {
+      float vw = 0, vb = 0;
+#pragma unroll
+      for (int i = 0; i < kNarrowThreads / 64; ++i) {
+        vw += join[0][i][c];
+        vb += join[1][i][c];
+      }
+      pw[c] = vw;
+      pb[c] = vb;
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      if (col_of(c) < d) {
+        store8(pw + col_of(c), dw[c]);
+        store8(pb + col_of(c), db[c]);
+      }
+  }
+}
+
+// Workgroups of the backward pass: 12 waves a CU and two workgroups at least,
+// but each adds 16 bytes a column (its shares of dw and db, written and read)
+// to the 8 a column that a row of 16-bit elements moves, so no more than one
+// for every 8 rows where that still gives every CU one.
+int64_t backward_blocks(int64_t rows, int64_t d) {
+  constexpr int64_t cus = 256;
+  const Team f = team_of(d, 1);
+  const int64_t teams = f.lanes < 64 ? kNarrowThreads / f.lanes : 1;
+  const int64_t per_cu = f.lanes < 64 ? 4 : 12 / f.waves, fill = cus * (per_cu > 2 ? per_cu : 2);
+  const int64_t turns = (rows + teams - 1) / teams;  // a workgroup takes `teams` rows at a time
+  const int64_t n = turns / 8 < cus ? cus : turns / 8 > fill ? fill : turns / 8;
+  return turns < n ? turns : n;
+}
+
+template <typename T>
+void launch_backward(const BackArgs &a, hipStream_t s) {
+  const Team f = team_of(a.d, 1);
+  const dim3 grid(uint32_t(backward_blocks(a.rows, a.d))), block(f.lanes < 64 ? kNarrowThreads : f.waves * 64);
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
+  if (f.lanes == 8) go(layer_norm_backward_kernel<T, 1, 2, 8>);
+  else if (f.lanes == 16) go(layer_norm_backward_kernel<T, 1, 2, 16>);
+  else if (f.lanes == 32) go(layer_norm_backward_kernel<T, 1, 2, 32>);
+  else if (f.chunks == 1) go(layer_norm_backward_kernel<T, 1, 2, 64>);
+  else if (f.chunks == 2) go(layer_norm_backward_kernel<T, 2, 1, 64>);
+  else go(layer_norm_backward_kernel<T, 4, 1, 64>);
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, const void *residual, const void *weight,
+                       const void *bias, float eps, int32_t out_dtype, void *y, float *scale, void *residual_out,
+                       float *mean, float *rstd, void *stream) {
+  int32_t st = check_rows(rows, d, dtype, INT32_MAX);
+  if (st != TSS_OK) return st;
+  if (out_dtype != dtype && out_dtype != TSS_I8) return TSS_E_DTYPE;
+  if (!(eps >= 0)) return TSS_E_ARG;
+  if (rows == 0) return TSS_OK;
+  if (!x || !weight || !y || (out_dtype == TSS_I8 && !scale)) return TSS_E_ARG;
+  if (misaligned(x) || misaligned(residual) || misaligned(weight) || misaligned(bias) || misaligned(y) ||
+      misaligned(residual_out))
+    return TSS_E_ALIGN;
+  const NormArgs a{int(rows), int(d), 1, x, residual, weight, bias, eps, y, scale, residual_out, mean, rstd};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    st = out_dtype == TSS_I8 ? launch_norm<T, true>(a, s) : launch_norm<T, false>(a, s);
+  };
+  if (dtype == TSS_F16) go(_Float16{});
+  else if (dtype == TSS_BF16) go(__bf16{});
+  else go(float{});
+  if (st != TSS_OK) return st;
+  return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
+}
+
+int64_t tss_layer_norm_backward_workspace_size(int64_t rows, int64_t d) {
+  const int32_t st = check_rows(rows, d, TSS_F32, INT32_MAX);
+  return st != TSS_OK ? st : backward_blocks(rows, d) * d * 8;
+}
+
+int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
+                                const void *weight, const float *mean, const float *rstd, const void *dh, void *dx,
+                                float *dweight, float *dbias, void *workspace, int64_t workspace_bytes, void *stream) {
+  const int32_t st = check_rows(rows, d, dtype, INT32_MAX);
+  if (st != TSS_OK) return st;
+  if (!dweight) return TSS_E_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (rows == 0) {
+    for (float *out : {dweight, dbias})
+      if (out) hipLaunchKernelGGL(zero_f32_kernel, dim3(uint32_t((d + 255) / 256)), dim3(256), 0, s, int(d), out);
+    return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
+  }
+  if (!dy || !h || !weight || !mean || !rstd || !dx) return TSS_E_ARG;
+  if (!workspace || workspace_bytes < tss_layer_norm_backward_workspace_size(rows, d)) return TSS_E_ARG;
+  if (misaligned(dy) || misaligned(h) || misaligned(weight) || misaligned(dh) || misaligned(dx) ||
+      misaligned(workspace))
+    return TSS_E_ALIGN;
+  float *partial = static_cast<float *>(workspace);
+  const BackArgs a{int(rows), int(d), dy, h, weight, mean, rstd, dh, dx, partial};
+  if (dtype == TSS_F16) launch_backward<_Float16>(a, s);
+  else if (dtype == TSS_BF16) launch_backward<__bf16>(a, s);
+  else launch_backward<float>(a, s);
+  launch_column_sums(backward_blocks(rows, d), d, partial, dweight, dbias, s);
+  return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
+}
+
+}  // extern "C"

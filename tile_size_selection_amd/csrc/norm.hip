@@ -15,16 +15,11 @@
 // residual: 106 us, to e4m3 96, with rstd 107.  One row of 4096: 2.6 us.  Rows
 // narrower than a wave's 512 columns leave its lanes idle: 2^20 x 128, bf16, 338
 // us (1.6 TB/s), backward 356 (3.0 TB/s).
-#include "rows.h"
+#include "row_launch.h"
 
 using namespace tss;
 
 namespace {
-
-constexpr int kMaxChunks = 4;     // chunks of 8 elements per thread
-constexpr int kMaxThreads = 1024;
-constexpr int64_t kMaxRows = (int64_t(1) << 23) - 1;
-constexpr int64_t kMaxD = int64_t(kMaxChunks) * kMaxThreads * 8;
 
 // Sum over the wpr waves that share a row; red has one slot per wave.
 __device__ __forceinline__ float row_sum(float v, float *red, int wave, int wpr) {
@@ -198,68 +193,6 @@ __global__ __launch_bounds__(kMaxThreads) void rms_norm_backward_kernel(int rows
   }
 }
 
-// dw[col] = sum of n partials: a workgroup takes 4 L columns; its groups of L
-// lanes add every (1024 / L)th partial, a wave's groups are joined by shuffles
-// and the 16 waves' sums in order.  L = 8 reads whole lines; narrow rows take
-// L = 2, which gives them four times the workgroups.
-constexpr int kReduceBlock = 1024;
-template <int L>
-__global__ __launch_bounds__(kReduceBlock) void rms_norm_dweight_kernel(int n, int d, const float *partial, float *dw) {
-  __shared__ f32x4 s[kReduceBlock / 64][L];
-  const int g = threadIdx.x / L, l = threadIdx.x % L;
-  const int col = (blockIdx.x * L + l) * 4;
-  float acc[4] = {0, 0, 0, 0};
-  if (col < d) {
-#pragma unroll 4
-    for (int p = g; p < n; p += kReduceBlock / L) {
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(partial + int64_t(p) * d + col);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] += v[i];
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int m = L; m < 64; m *= 2) acc[i] += __shfl_xor(acc[i], m);
-  if (threadIdx.x % 64 < L) s[threadIdx.x / 64][l] = f32x4{acc[0], acc[1], acc[2], acc[3]};
-  __syncthreads();
-  const int c = threadIdx.x;
-  if (c < 4 * L && blockIdx.x * 4 * L + c < d) {
-    float sum = 0;
-    for (int i = 0; i < kReduceBlock / 64; ++i) sum += s[i][c / 4][c % 4];
-    dw[blockIdx.x * 4 * L + c] = sum;
-  }
-}
-
-__global__ void zero_f32_kernel(int n, float *p) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = 0;
-}
-
-bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-int32_t check_rows(int64_t rows, int64_t d, int32_t dtype) {
-  if (rows < 0 || d < 1 || rows > kMaxRows) return TSS_E_ARG;
-  if (dtype != TSS_F16 && dtype != TSS_BF16 && dtype != TSS_F32) return TSS_E_DTYPE;
-  if (d % 8) return TSS_E_ALIGN;
-  if (d > kMaxD) return TSS_E_UNSUPPORTED;
-  return TSS_OK;
-}
-
-// Waves and chunks of a row of d columns held by whole workgroups of `most` chunks a thread.
-struct RowShape {
-  int waves, chunks;
-};
-RowShape row_shape(int64_t d, int chunks) {
-  const int64_t c8 = d / 8;
-  int waves = int((c8 + int64_t(64) * chunks - 1) / (int64_t(64) * chunks));
-  while (waves > kMaxThreads / 64) {
-    chunks *= 2;
-    waves = int((c8 + int64_t(64) * chunks - 1) / (int64_t(64) * chunks));
-  }
-  return {waves, chunks};
-}
-
 template <typename T, bool FP8>
 int32_t launch_norm(int64_t rows, int64_t d, const void *x, const void *residual, const void *weight, float eps, void *y,
                  float *scale, void *h, float *rstd, hipStream_t s) {
@@ -364,12 +297,7 @@ int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void
   if (dtype == TSS_F16) launch_backward<_Float16>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
   else if (dtype == TSS_BF16) launch_backward<__bf16>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
   else launch_backward<float>(rows, d, dy, h, weight, rstd, dh, dx, partial, s);
-  auto reduce = [&](auto kernel, int64_t cols) {
-    hipLaunchKernelGGL(kernel, dim3(uint32_t((d + cols - 1) / cols)), dim3(kReduceBlock), 0, s,
-                       int(backward_blocks(rows, d)), int(d), partial, dweight);
-  };
-  if (d > 2048) reduce(rms_norm_dweight_kernel<8>, 32);
-  else reduce(rms_norm_dweight_kernel<2>, 8);
+  launch_column_sums(backward_blocks(rows, d), d, partial, dweight, nullptr, s);
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 

@@ -60,6 +60,13 @@ inline void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
   *n = int32_t((kb + per - 1) / per);
 }
 
+// A product of 8-bit integers: as an 8-bit floating-point one.
+inline ProductPlan plan_int8(int64_t M, int64_t N, int64_t K) {
+  ProductPlan p = plan_product(M, N, K, false);
+  p.sets = 1;
+  return p;
+}
+
 // 8-bit products grouped by expert.
 // Small tiles where they leave CUs free anyway (581 rows in 3 groups, K 2240, N
 // 792: 13.9 us against 16.0 and 15.5 with 128 x 128 and 256 x 256) and for few

@@ -20,8 +20,9 @@ constexpr float kSmallestAmax = 1e-30f;   // a block's largest magnitude is take
 
 struct E4M3 {};
 struct E5M2 {};
+struct I8 {};  // -127 .. 127
 template <typename Q>
-constexpr float kLargest = __is_same(Q, E4M3) ? 448.0f : 57344.0f;
+constexpr float kLargest = __is_same(Q, E4M3) ? 448.0f : __is_same(Q, I8) ? 127.0f : 57344.0f;
 
 // 8 consecutive elements as they are in memory: 16 bytes (fp16, bf16) or 32
 // (fp32), loaded with 16-byte accesses and widened when they are used.
@@ -118,6 +119,31 @@ __device__ __forceinline__ float sum64(float v) {
   return v + __shfl_xor(v, 32);
 }
 
+// Sum (largest magnitude) over L neighbouring lanes, L a power of two; every
+// lane gets the same bits.
+template <int CTRL>
+__device__ __forceinline__ float lane_swap(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <int L, typename F>
+__device__ __forceinline__ float over_lanes(float v, F join) {
+  if constexpr (L >= 2) v = join(v, lane_swap<0xb1>(v));    // lanes 1 0 3 2 of four
+  if constexpr (L >= 4) v = join(v, lane_swap<0x4e>(v));    // 2 3 0 1
+  if constexpr (L >= 8) v = join(v, lane_swap<0x141>(v));   // eight mirrored
+  if constexpr (L >= 16) v = join(v, lane_swap<0x140>(v));  // sixteen mirrored
+  if constexpr (L >= 32) v = join(v, __shfl_xor(v, 16));
+  if constexpr (L >= 64) v = join(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float sum_lanes(float v) {
+  return over_lanes<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float max_lanes(float v) {
+  return over_lanes<L>(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
+}
+
 // A block's scale = amax / largest value of the type, and what v / scale takes:
 // the quotient is the product with the reciprocal, corrected once by its
 // remainder, which rounds it as a division does for 2 more operations an
@@ -149,7 +175,14 @@ __device__ __forceinline__ u32x2 round8(const float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     int w = 0;
-    if constexpr (__is_same(Q, E4M3)) {
+    if constexpr (__is_same(Q, I8)) {
+      // 1.5 * 2^23 added: the sum's last byte is the rounded quotient in two's complement; 0 of infinities and NaN
+      uint32_t b[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = __builtin_bit_cast(uint32_t, f[4 * i + j] + 0x1.8p23f);
+      const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
+      w = int(lo | hi);
+    } else if constexpr (__is_same(Q, E4M3)) {
       w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i], f[4 * i + 1], w, false);
       w = __builtin_amdgcn_cvt_pk_fp8_f32(f[4 * i + 2], f[4 * i + 3], w, true);
     } else {

@@ -1,23 +1,26 @@
-"""Row operators (root-mean-square norm, quantisation to 8 bits) and the 8-bit
-and grouped matrix products: argument checks and marshalling only, as in
+"""Row operators (root-mean-square and layer norm, quantisation to 8 bits), the
+8-bit and grouped matrix products, and the gradients' norm and clipping: argument checks and marshalling only, as in
 api.py; the work is libtss.so's (include/tss.h documents each entry point).
 
 Each call takes stream=, the stream to run on (the current one without it).
-Element types are named 'f16', 'bf16', 'f32', 'e4m3' and 'e5m2'.  Scales of
-8-bit tensors are float32, one for each block of 1 or 128 rows x 128 columns,
-column-block-major: scale[column block][row or row block]."""
+Element types are named 'f16', 'bf16', 'f32', 'e4m3', 'e5m2' and 'i8'.  Scales
+of 8-bit floating-point tensors are float32, one for each block of 1 or 128
+rows x 128 columns, column-block-major: scale[column block][row or row block];
+those of 8-bit integers one for each row: scale[row]."""
 from __future__ import annotations
 
+import ctypes
 import functools
-from typing import NamedTuple, Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 from . import _capi as C
 from .api import _workspace, torch
 
-_DT = {"f16": C.TSS_F16, "bf16": C.TSS_BF16, "f32": C.TSS_F32, "e4m3": C.TSS_E4M3, "e5m2": C.TSS_E5M2}
+_DT = {"f16": C.TSS_F16, "bf16": C.TSS_BF16, "f32": C.TSS_F32, "e4m3": C.TSS_E4M3, "e5m2": C.TSS_E5M2,
+       "i8": C.TSS_I8}
 if torch is not None:
     _TORCH = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32,
-              "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+              "e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2, "i8": torch.int8}
     _NAME = {v: k for k, v in _TORCH.items()}
 
 
@@ -174,6 +177,89 @@ def rms_norm_backward(dy, h, weight, rstd, dh=None, dx=None, dweight=None,
     return dx, dweight
 
 
+class LayerNorm(NamedTuple):
+    y: "torch.Tensor"
+    scale: Optional["torch.Tensor"]  # i8 output only
+    h: Optional["torch.Tensor"]      # x + residual; None without a residual
+    mean: Optional["torch.Tensor"]   # mean(h) and 1 / sqrt(mean((h - mean)^2) + eps), where asked for
+    rstd: Optional["torch.Tensor"]
+
+
+@_streamed
+def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, out_dtype: Optional[str] = None, out=None,
+               scale=None, residual_out=None, stats=None) -> LayerNorm:
+    """h = x + residual (x without one); y = (h - mean(h)) / sqrt(mean((h -
+    mean(h))^2) + eps) * weight + bias (0 without one) over the last dimension
+    of x (rows, d), d a multiple of 8 up to 32768; fp32 inside.  out_dtype: x's
+    type (the default) or 'i8', with a scale for each row (as quantize_int8
+    gives).  h comes back rounded to x's type (residual_out may be residual
+    itself).  stats: True, or a pair of float32 tensors of `rows`, to get the
+    mean and rstd that the backward pass takes.  out, scale, residual_out:
+    outputs to write into, else allocated."""
+    dt = _name(x, "x", ("f16", "bf16", "f32"))
+    if x.dim() != 2:
+        raise ValueError("x must be (rows, d)")
+    rows, d = x.shape
+    od = _choice(out_dtype or dt, "out_dtype", (dt, "i8"))
+    _given(x, "x", (rows, d), x.dtype)
+    _given(weight, "weight", (d,), x.dtype)
+    if bias is not None:
+        _given(bias, "bias", (d,), x.dtype)
+    out = _out(out, "out", (rows, d), _TORCH[od], x.device)
+    if od == "i8":
+        scale = _out(scale, "scale", (rows,), torch.float32, x.device)
+    elif scale is not None:
+        raise ValueError("scale is only for out_dtype 'i8'")
+    if residual is not None:
+        _given(residual, "residual", (rows, d), x.dtype)
+        residual_out = _out(residual_out, "residual_out", (rows, d), x.dtype, x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    mean = rstd = None
+    if stats is not None and stats is not False:
+        mean, rstd = (None, None) if stats is True else stats
+        mean = _out(mean, "mean", (rows,), torch.float32, x.device)
+        rstd = _out(rstd, "rstd", (rows,), torch.float32, x.device)
+    _call("tss_layer_norm", C.lib().tss_layer_norm, (x, weight, bias, out, residual, scale, residual_out, mean, rstd),
+          rows, d, _DT[dt], x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), eps, _DT[od], out.data_ptr(),
+          _ptr(scale), _ptr(residual_out), _ptr(mean), _ptr(rstd))
+    return LayerNorm(out, scale, residual_out, mean, rstd)
+
+
+@_streamed
+def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=None, dbias=None, workspace=None):
+    """(dx, dweight, dbias) of layer_norm from its h (or x, without a residual),
+    mean and rstd: with xhat = (h - mean) rstd and g = dy weight, dx = dh + rstd
+    (g - mean(g) - xhat mean(g xhat)), the gradient of both x and residual (dh:
+    the gradient that arrives through h; it may be None), dweight = sum over
+    rows of dy xhat and dbias = sum over rows of dy in float32, the same bits on
+    every run.  dbias False: not computed, None comes back.  dx may be dy or dh."""
+    dt = _name(dy, "dy", ("f16", "bf16", "f32"))
+    if dy.dim() != 2:
+        raise ValueError("dy must be (rows, d)")
+    rows, d = dy.shape
+    _given(dy, "dy", (rows, d), dy.dtype)
+    _given(h, "h", (rows, d), dy.dtype)
+    _given(weight, "weight", (d,), dy.dtype)
+    _given(mean, "mean", (rows,), torch.float32)
+    _given(rstd, "rstd", (rows,), torch.float32)
+    if dh is not None:
+        _given(dh, "dh", (rows, d), dy.dtype)
+    dx = _out(dx, "dx", (rows, d), dy.dtype, dy.device)
+    dweight = _out(dweight, "dweight", (d,), torch.float32, dy.device)
+    dbias = None if dbias is False else _out(dbias, "dbias", (d,), torch.float32, dy.device)
+    need = C.lib().tss_layer_norm_backward_workspace_size(rows, d)
+    if need < 0:
+        C.check(int(need), "tss_layer_norm_backward_workspace_size")
+    workspace = _workspace(workspace, need, dy.device)
+    _call("tss_layer_norm_backward", C.lib().tss_layer_norm_backward,
+          (dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace),
+          rows, d, _DT[dt], dy.data_ptr(), h.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dh),
+          dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+    return dx, dweight, dbias
+
+
 @_streamed
 def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1, out=None,
                  scale=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
@@ -195,6 +281,25 @@ def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1,
     scale = _out(scale, "scale", (_blocks(d), rows if block_rows == 1 else _blocks(rows)), torch.float32, x.device)
     _call("tss_quantize_fp8", C.lib().tss_quantize_fp8, (x, out, scale),
           rows, d, _DT[dt], x.data_ptr(), int(gated), _DT[fp8], block_rows, out.data_ptr(), scale.data_ptr())
+    return out, scale
+
+
+@_streamed
+def quantize_int8(x, gated: bool = False, out=None, scale=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
+    """(q, scale) of x (rows, d), or with gated of silu(gate) * up where x is
+    (rows, 2 d), gate then up: q int8 in -127 .. 127 and scale (rows,) float32,
+    the row's largest magnitude / 127.  d a multiple of 8 up to 32768."""
+    dt = _name(x, "x", ("f16", "bf16", "f32"))
+    if x.dim() != 2 or (gated and x.shape[1] % 2):
+        raise ValueError("x must be (rows, d), or (rows, 2 d) with gated")
+    rows, d = x.shape
+    _given(x, "x", (rows, d), x.dtype)
+    if gated:
+        d //= 2
+    out = _out(out, "out", (rows, d), torch.int8, x.device)
+    scale = _out(scale, "scale", (rows,), torch.float32, x.device)
+    _call("tss_quantize_int8", C.lib().tss_quantize_int8, (x, out, scale),
+          rows, d, _DT[dt], x.data_ptr(), int(gated), out.data_ptr(), scale.data_ptr())
     return out, scale
 
 
@@ -238,6 +343,40 @@ def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, fp
     _call("tss_gemm_fp8", C.lib().tss_gemm_fp8, (A, B, sa, sb, out, workspace),
           M, N, K, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), b_rows, out.data_ptr(),
           _out_type(out_dtype, fp32_sums), _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out
+
+
+def gemm_int8_workspace_size(M: int, N: int, K: int) -> int:
+    n = C.lib().tss_gemm_int8_workspace_size(M, N, K)
+    if n < 0:
+        C.check(int(n), "tss_gemm_int8_workspace_size")
+    return int(n)
+
+
+@_streamed
+def gemm_int8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
+    """C = (A sa) @ (B sb)^T for int8 A (M, K) with sa (M,), one scale for each
+    token, and int8 B (N, K) with sb (N,), one for each channel; the sums over K
+    are exact.  out_dtype 'bf16', 'f16' or 'f32'.  K a multiple of 16 below
+    2^17.  workspace: a device tensor of at least gemm_int8_workspace_size bytes
+    (allocated here when one is needed and not given)."""
+    _name(A, "A", ("i8",))
+    _name(B, "B", ("i8",))
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError(f"shape mismatch {tuple(A.shape)} x {tuple(B.shape)}^T")
+    (M, K), N = A.shape, B.shape[0]
+    _given(A, "A", (M, K), A.dtype)
+    _given(B, "B", (N, K), B.dtype)
+    _choice(out_dtype, "out_dtype", ("bf16", "f16", "f32"))
+    _given(sa, "sa", (M,), torch.float32)
+    _given(sb, "sb", (N,), torch.float32)
+    out = _out(out, "out", (M, N), _TORCH[out_dtype], A.device)
+    need = gemm_int8_workspace_size(M, N, K)
+    if need:
+        workspace = _workspace(workspace, need, A.device)
+    _call("tss_gemm_int8", C.lib().tss_gemm_int8, (A, B, sa, sb, out, workspace),
+          M, N, K, A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), out.data_ptr(), _DT[out_dtype],
+          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
     return out
 
 
@@ -322,3 +461,76 @@ def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None, fp3
           T, E, K, N, _DT[adt], A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), sizes.data_ptr(),
           out.data_ptr(), _out_type(out_dtype, fp32_sums))
     return out
+
+
+def _dense(t, what: str):
+    """t, checked: its elements lie in memory without gaps, in any order of
+    its dimensions."""
+    if not t.is_contiguous():
+        step = 1
+        for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
+            if stride != step:
+                raise ValueError(f"{what} must lie in memory without gaps, not with strides {t.stride()}")
+            step *= size
+    return t
+
+
+def _clip(grads, max_norm: float, out, norm, workspace, where: str):
+    grads = list(grads)
+    types = [_DT[_name(t, "a gradient", ("f16", "bf16", "f32"))] for t in grads]
+    for t in grads:
+        _dense(t, "a gradient")
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+        for t, o in zip(grads, out):
+            if o is not t and (o.shape != t.shape or o.dtype != t.dtype or o.stride() != t.stride()):
+                raise ValueError(f"an output must have its gradient's shape, type and strides, {t.dtype} "
+                                 f"{tuple(t.shape)} {t.stride()}, not {o.dtype} {tuple(o.shape)} {o.stride()}")
+    if not grads and norm is None:
+        raise ValueError("without tensors norm must be given")
+    device = grads[0].device if grads else norm.device
+    norm = _out(norm, "norm", (), torch.float32, device)
+    n = len(grads)
+    sizes = (C.i64 * n)(*[t.numel() for t in grads])
+    need = C.lib().tss_clip_grad_norm_workspace_size(n, sizes)
+    if need < 0:
+        C.check(int(need), where)
+    workspace = _workspace(workspace, need, device)
+    pointers = lambda ts: (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])  # noqa: E731
+    _call(where, C.lib().tss_clip_grad_norm, (norm, workspace, *grads, *(out or ())),
+          n, pointers(grads), sizes, (C.i32 * n)(*types), max_norm, None if out is None else pointers(out),
+          norm.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return norm
+
+
+def _list_streamed(f):
+    """_streamed for calls whose first argument is a sequence of tensors."""
+    @functools.wraps(f)
+    def call(grads, *args, stream=None, **kwargs):
+        grads = list(grads)
+        if stream is None:
+            return f(grads, *args, **kwargs)
+        first = next(iter(grads), kwargs.get("norm"))
+        return _streamed(lambda _first: f(grads, *args, **kwargs))(first, stream=stream)
+    return call
+
+
+@_list_streamed
+def grad_norm(grads: Sequence["torch.Tensor"], norm=None, workspace=None):
+    """The norm over all elements of the tensors (f16, bf16, f32, mixed), a
+    float32 scalar on the GPU: squares are added in 64 bits, in a fixed order.
+    norm: the scalar to write into, else allocated."""
+    return _clip(grads, 0.0, None, norm, workspace, "tss_clip_grad_norm")
+
+
+@_list_streamed
+def clip_grad_norm(grads: Sequence["torch.Tensor"], max_norm: float, out=None, norm=None, workspace=None):
+    """Scales the tensors, in place or into out (a tensor for each, of its
+    shape, type and strides), to a norm of at most max_norm: every element times
+    min(1, max_norm / (norm + 1e-6)) in float32, rounded once.  Returns grad_norm's
+    norm; nothing is read back to the host.  A NaN norm makes every element
+    NaN, an infinite one multiplies by 0.  Tensors must lie in memory without
+    gaps, and none may be given twice or overlap another that is written."""
+    return _clip(grads, max_norm, grads if out is None else out, norm, workspace, "tss_clip_grad_norm")
