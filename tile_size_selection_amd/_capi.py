@@ -135,7 +135,7 @@ def lib():
     L.tss_gemm_int8.argtypes = [i64, i64, i64] + [vp] * 5 + [i32, vp, i64, vp]
     L.tss_gemm_int8_workspace_size.argtypes = [i64, i64, i64]
     L.tss_clip_grad_norm.argtypes = [i64, P(vp), P(i64), P(i32), ctypes.c_float, P(vp), vp, vp, i64, vp]
-    L.tss_clip_grad_norm_workspace_size.argtypes = [i64, P(i64)]
+    L.tss_clip_grad_norm_workspace_size.argtypes = [i64, vp]
     L.tss_sort_by_expert.argtypes = [i64, i64, i64, vp, i32, vp, vp, vp, vp, i64, vp]
     L.tss_sort_by_expert_workspace_size.argtypes = [i64, i64, i64]
     L.tss_gather_rows.argtypes = [i64, i64, i64, i32, vp, vp, vp, vp, vp, i64, vp, vp]
@@ -158,6 +158,23 @@ def lib():
     L.tss_sort_by_expert_workspace_size.restype = i64
     _lib = L
     return L
+
+
+_bound = None
+
+
+def bind():
+    """The entry points as functions that take tensors (csrc/bind.cpp)."""
+    global _bound
+    if _bound is None:
+        lib()
+        try:
+            from . import _bind
+        except ImportError as e:
+            raise ImportError(f"{_HERE}/_bind.so is missing or does not load: build it with `python -m "
+                              "tile_size_selection_amd.build` (it is required; there is no fallback)") from e
+        _bound = _bind
+    return _bound
 
 
 class TssError(RuntimeError):

@@ -6,7 +6,9 @@ Each instantiation unit under csrc/inst is compiled by its own hipcc process
 for --offload-arch=gfx950; the objects are linked into
 tile_size_selection_amd/libtss.so, which is what the Python binding loads.
 The planner's command line, csrc/tss_plan.c, is built against that library
-into tile_size_selection_amd/tss_plan (a host program: gcc, C ABI only).
+into tile_size_selection_amd/tss_plan (a host program: gcc, C ABI only), and
+the compiled binding, csrc/bind.cpp, into tile_size_selection_amd/_bind.so (a
+Python extension: g++, torch's headers).
 --units recompiles only the sources whose file names contain one of the
 given strings (the other objects are linked as they are).
 """
@@ -19,6 +21,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 import time
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +30,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtss.so")
 CLI = os.path.join(PKG, "tss_plan")
+BIND = os.path.join(PKG, "_bind.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # -packed-fp32-ops off: compiler-made v_pk_{add,mul,fma}_f32 are avoided.
@@ -113,6 +117,26 @@ def build_cli(verbose: bool = True) -> str:
     return CLI
 
 
+def build_bind(verbose: bool = True) -> str:
+    """_bind.so: the entry points as Python functions that take tensors."""
+    import torch
+    at = os.path.dirname(torch.__file__)
+    tmp = BIND + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(at, "include"),
+           "-isystem", os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-L", PKG, "-l:libtss.so",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stderr}")
+    os.replace(tmp, BIND)
+    if verbose:
+        print(f"built {os.path.relpath(BIND, ROOT)}", flush=True)
+    return BIND
+
+
 def build(incremental: bool = False, jobs: int = 0, verbose: bool = True, units=None) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
     todo = []
@@ -141,6 +165,9 @@ def build(incremental: bool = False, jobs: int = 0, verbose: bool = True, units=
         print(f"built {os.path.relpath(LIB, ROOT)} ({len(todo)} units compiled) in {time.time() - t0:.1f}s",
               flush=True)
     build_cli(verbose)
+    newest = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "bind.cpp"), os.path.join(ROOT, "include", "tss.h")))
+    if not ((incremental or units is not None) and os.path.exists(BIND) and os.path.getmtime(BIND) > newest):
+        build_bind(verbose)
     return LIB
 
 

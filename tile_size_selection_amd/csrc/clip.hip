@@ -5,9 +5,10 @@
 // Bound by memory: every element is read for the norm, and read again and
 // written to be scaled.  Squares are added in 64 bits: their sum neither
 // overflows nor loses what many elements add to few, and the rate of 64-bit
-// FMAs is far above memory's.  Each workgroup adds a piece of a tensor, the
-// pieces' sums are added in a fixed order by every workgroup that scales (the
-// same bits on every run, and one launch fewer than with a pass of its own).
+// FMAs is far above memory's.  The elements are dealt evenly to the workgroups,
+// wherever tensors begin and end; the workgroups' sums are added in a fixed
+// order by every workgroup that scales (the same bits on every run, and one
+// launch fewer than with a pass of its own).
 // The tensors' addresses travel in the kernel's arguments, kTable at a time:
 // no copy from host memory, so a captured graph holds all that it needs.
 #include <algorithm>
@@ -22,21 +23,24 @@ namespace {
 
 constexpr int kTable = 128;
 constexpr int kClipThreads = 256;
+constexpr int kUnit = kClipThreads * 8;     // elements; a tensor's last unit may be short
+constexpr uint32_t kClipGroups = 2048;      // eight workgroups a CU
+constexpr int kTogether = 2;                // loads a thread has in flight
+constexpr int64_t kStreamed = int64_t(1) << 28;  // bytes of output from which on it passes the caches by
 constexpr float kNormEps = 1e-6f;
 
 struct ClipTable {
   const void *in[kTable];
   void *out[kTable];
   int64_t n[kTable];
-  uint32_t first[kTable + 1];  // a tensor's first piece, in this table
+  uint32_t first[kTable + 1];  // a tensor's first unit, in this table
   uint8_t type[kTable];
   int32_t count;
-  int32_t piece;               // elements of a piece, a multiple of 2048
-  uint32_t base;               // the table's first piece among all
+  uint32_t base;               // the table's first sum among all
 };
 static_assert(sizeof(ClipTable) <= 3840, "kernel arguments are 4 KiB");
 
-// The tensor that piece `at` of the table belongs to (its index is uniform over the workgroup).
+// The tensor that unit `at` of the table belongs to (uniform over the workgroup).
 __device__ __forceinline__ int tensor_of(const ClipTable &t, uint32_t at) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
@@ -70,12 +74,12 @@ __device__ __forceinline__ double piece_squares(const T *g, int64_t from, int64_
   if (wide) {
     const int64_t whole = from + (end - from) / 8 * 8;
     int64_t i = from + threadIdx.x * 8;
-    for (; i + 3 * kClipThreads * 8 < whole; i += 4 * kClipThreads * 8) {
-      Raw8<T> r[4];
+    for (; i + (kTogether - 1) * kClipThreads * 8 < whole; i += kTogether * kClipThreads * 8) {
+      Raw8<T> r[kTogether];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
+      for (int u = 0; u < kTogether; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kTogether; ++u) {
         float f[8];
         widen8(r[u], f);
 #pragma unroll
@@ -98,21 +102,23 @@ __device__ __forceinline__ double piece_squares(const T *g, int64_t from, int64_
 }
 
 template <typename T>
-__device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, int64_t end, bool wide, float factor) {
+__device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, int64_t end, bool wide, bool stream,
+                                            float factor) {
   if (wide) {
     const int64_t whole = from + (end - from) / 8 * 8;
     int64_t i = from + threadIdx.x * 8;
-    for (; i + 3 * kClipThreads * 8 < whole; i += 4 * kClipThreads * 8) {
-      Raw8<T> r[4];
+    for (; i + (kTogether - 1) * kClipThreads * 8 < whole; i += kTogether * kClipThreads * 8) {
+      Raw8<T> r[kTogether];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
+      for (int u = 0; u < kTogether; ++u) r[u] = load8(g + i + u * kClipThreads * 8);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kTogether; ++u) {
         float f[8];
         widen8(r[u], f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= factor;
-        store8(out + i + u * kClipThreads * 8, f);
+        if (stream) store8_streamed(out + i + u * kClipThreads * 8, f);
+        else store8(out + i + u * kClipThreads * 8, f);
       }
     }
     for (; i < whole; i += kClipThreads * 8) {
@@ -127,14 +133,21 @@ __device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, in
   for (int64_t i = from + threadIdx.x; i < end; i += kClipThreads) out[i] = (T)(float(g[i]) * factor);
 }
 
-// f(element type, tensor's index, first element, end) of piece `at`.
+// f(element type, tensor's index, first element, end) of each tensor in the
+// range of workgroup `group` of `groups`.
 template <typename F>
-__device__ __forceinline__ void with_piece(const ClipTable &t, uint32_t at, F f) {
-  const int k = tensor_of(t, at);
-  const int64_t from = int64_t(at - t.first[k]) * t.piece, end = min(t.n[k], from + t.piece);
-  if (t.type[k] == TSS_F32) f(float{}, k, from, end);
-  else if (t.type[k] == TSS_F16) f(_Float16{}, k, from, end);
-  else f(__bf16{}, k, from, end);
+__device__ __forceinline__ void with_range(const ClipTable &t, uint32_t group, uint32_t groups, F f) {
+  const uint64_t units = t.first[t.count];
+  uint32_t at = uint32_t(units * group / groups);
+  const uint32_t end = uint32_t(units * (group + 1) / groups);
+  for (int k = tensor_of(t, at); at < end; ++k) {
+    const uint32_t upto = min(end, t.first[k + 1]);
+    const int64_t from = int64_t(at - t.first[k]) * kUnit, to = min(t.n[k], int64_t(upto - t.first[k]) * kUnit);
+    if (t.type[k] == TSS_F32) f(float{}, k, from, to);
+    else if (t.type[k] == TSS_F16) f(_Float16{}, k, from, to);
+    else f(__bf16{}, k, from, to);
+    at = upto;
+  }
 }
 
 __device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -142,66 +155,75 @@ __device__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_c
 __global__ __launch_bounds__(kClipThreads) void clip_squares_kernel(ClipTable t, double *partial) {
   __shared__ double red[kClipThreads / 64];
   double s = 0;
-  with_piece(t, blockIdx.x, [&](auto v, int k, int64_t from, int64_t end) {
+  with_range(t, blockIdx.x, gridDim.x, [&](auto v, int k, int64_t from, int64_t end) {
     using T = decltype(v);
-    s = piece_squares(static_cast<const T *>(t.in[k]), from, end, aligned16(t.in[k]));
+    s += piece_squares(static_cast<const T *>(t.in[k]), from, end, aligned16(t.in[k]));
   });
   s = group_sum(s, red);
   if (threadIdx.x == 0) partial[t.base + blockIdx.x] = s;
 }
 
-// All pieces' sums, in a fixed order.
-__device__ __forceinline__ double total_squares(const double *partial, uint32_t pieces, double *red) {
+// All workgroups' sums, in a fixed order.
+__device__ __forceinline__ double total_squares(const double *partial, uint32_t sums, double *red) {
   double s = 0;
-  for (uint32_t i = threadIdx.x; i < pieces; i += kClipThreads) s += partial[i];
+  for (uint32_t i = threadIdx.x; i < sums; i += kClipThreads) s += partial[i];
   return group_sum(s, red);
 }
 
-__global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *partial, uint32_t pieces, float *norm) {
+__global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *partial, uint32_t sums, float *norm) {
   __shared__ double red[kClipThreads / 64];
-  const double s = total_squares(partial, pieces, red);
+  const double s = total_squares(partial, sums, red);
   if (threadIdx.x == 0) *norm = float(sqrt(s));
 }
 
-__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t, const double *partial, uint32_t pieces,
-                                                                  uint32_t in_table, float max_norm, float *norm) {
+__global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t, const double *partial, uint32_t sums,
+                                                                  float max_norm, float *norm, bool stream) {
   __shared__ double red[kClipThreads / 64];
-  const double n = sqrt(total_squares(partial, pieces, red));
+  const double n = sqrt(total_squares(partial, sums, red));
   if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(n);
   const double q = double(max_norm) / (n + double(kNormEps));
   const float factor = q > 1 ? 1.0f : float(q);  // a NaN comes through
-  // The last pieces first: the norm's pass has left them in the caches.
-  for (uint32_t i = blockIdx.x; i < in_table; i += gridDim.x)
-    with_piece(t, in_table - 1 - i, [&](auto v, int k, int64_t from, int64_t end) {
-      using T = decltype(v);
-      if (factor == 1.0f && t.out[k] == t.in[k]) return;
-      piece_scale(static_cast<const T *>(t.in[k]), static_cast<T *>(t.out[k]), from, end,
-                  aligned16(t.in[k]) && aligned16(t.out[k]), factor);
-    });
+  // The last elements first: the norm's pass has left them in the caches.
+  with_range(t, gridDim.x - 1 - blockIdx.x, gridDim.x, [&](auto v, int k, int64_t from, int64_t end) {
+    using T = decltype(v);
+    if (factor == 1.0f && t.out[k] == t.in[k]) return;
+    piece_scale(static_cast<const T *>(t.in[k]), static_cast<T *>(t.out[k]), from, end,
+                aligned16(t.in[k]) && aligned16(t.out[k]), stream, factor);
+  });
 }
 
 int bytes_of(int32_t dtype) { return dtype == TSS_F32 ? 4 : dtype == TSS_F16 || dtype == TSS_BF16 ? 2 : 0; }
 
-// Elements of a piece: about 2048 pieces in all (eight workgroups a CU), of at least 4096 elements.
-struct Pieces {
-  int64_t piece, count;
-};
-int32_t cut(int64_t n, const int64_t *sizes, Pieces *out) {
+constexpr int64_t kMostElements = int64_t(1) << 40;
+
+uint32_t groups_of(uint32_t units) { return units < kClipGroups ? units : kClipGroups; }
+
+// Calls f(first tensor, one past the last, units) for the tables: kTable tensors that are not empty, or the last of them.
+template <typename F>
+int32_t each_table(int64_t n, const int64_t *sizes, F f) {
   if (n < 0 || n > INT32_MAX || (n > 0 && !sizes)) return TSS_E_ARG;
-  int64_t total = 0;
+  int64_t total = 0, begin = 0, units = 0;
+  int count = 0;
   for (int64_t i = 0; i < n; ++i) {
-    if (sizes[i] < 0 || sizes[i] > int64_t(1) << 40) return TSS_E_ARG;
-    total += sizes[i];
-    if (total > int64_t(1) << 40) return TSS_E_ARG;
+    if (sizes[i] < 0 || sizes[i] > kMostElements || (total += sizes[i]) > kMostElements) return TSS_E_ARG;
+    if (sizes[i] > 0) {
+      ++count;
+      units += (sizes[i] + kUnit - 1) / kUnit;
+    }
+    if (count == kTable || (i == n - 1 && count)) {
+      f(begin, i + 1, uint32_t(units));
+      begin = i + 1;
+      units = count = 0;
+    }
   }
-  int64_t piece = (total / 2048 + 2047) / 2048 * 2048;
-  if (piece < 4096) piece = 4096;
-  if (piece > int64_t(1) << 30) return TSS_E_ARG;
-  int64_t count = 0;
-  for (int64_t i = 0; i < n; ++i) count += (sizes[i] + piece - 1) / piece;
-  if (count > int64_t(1) << 24) return TSS_E_ARG;
-  *out = {piece, count};
   return TSS_OK;
+}
+
+// The workgroups' sums of all tables.
+int64_t count_sums(int64_t n, const int64_t *sizes) {
+  int64_t sums = 0;
+  const int32_t st = each_table(n, sizes, [&](int64_t, int64_t, uint32_t units) { sums += groups_of(units); });
+  return st != TSS_OK ? st : sums;
 }
 
 // An output may be its own input; apart from that no output overlaps another
@@ -231,52 +253,49 @@ bool overlapping(int64_t n, const void *const *in, void *const *out, const int64
 
 int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes, float max_norm,
              void *const *out, float *norm, void *workspace, int64_t workspace_bytes, hipStream_t s) {
-  Pieces c;
-  const int32_t st = cut(n, sizes, &c);
-  if (st != TSS_OK) return st;
+  const int64_t sums = count_sums(n, sizes);
+  if (sums < 0) return int32_t(sums);
   if (!norm || (n > 0 && (!grads || !dtypes))) return TSS_E_ARG;
   if (out && !(max_norm >= 0)) return TSS_E_ARG;
+  int64_t bytes = 0;
   for (int64_t i = 0; i < n; ++i) {
     const int size = bytes_of(dtypes[i]);
     if (!size) return TSS_E_DTYPE;
+    bytes += sizes[i] * size;
     if (sizes[i] > 0 && (!grads[i] || (out && !out[i]))) return TSS_E_ARG;
     if (reinterpret_cast<uintptr_t>(grads[i]) % size || (out && reinterpret_cast<uintptr_t>(out[i]) % size)) return TSS_E_ALIGN;
   }
   if (reinterpret_cast<uintptr_t>(norm) % 4 || reinterpret_cast<uintptr_t>(workspace) % 8) return TSS_E_ALIGN;
-  if (c.count && (!workspace || workspace_bytes < c.count * 8)) return TSS_E_ARG;
+  if (sums && (!workspace || workspace_bytes < sums * 8)) return TSS_E_ARG;
   if (out && overlapping(n, grads, out, sizes, dtypes)) return TSS_E_ARG;
   double *partial = static_cast<double *>(workspace);
-  // f(table, its pieces) for the tensors, kTable at a time; empty ones are left out
-  auto tables = [&](auto f) {
+  // launch(table, its workgroups) for each table
+  auto tables = [&](auto launch) {
     ClipTable t{};
-    t.piece = int32_t(c.piece);
-    uint32_t done = 0;
-    for (int64_t i = 0; i <= n; ++i) {
-      if (i < n && sizes[i] > 0) {
+    each_table(n, sizes, [&](int64_t begin, int64_t end, uint32_t units) {
+      t.count = 0;
+      for (int64_t i = begin; i < end; ++i) {
+        if (sizes[i] == 0) continue;
         const int k = t.count++;
         t.in[k] = grads[i];
         t.out[k] = out ? out[i] : nullptr;
         t.n[k] = sizes[i];
         t.type[k] = uint8_t(dtypes[i]);
-        t.first[k + 1] = t.first[k] + uint32_t((sizes[i] + c.piece - 1) / c.piece);
+        t.first[k + 1] = t.first[k] + uint32_t((sizes[i] + kUnit - 1) / kUnit);
       }
-      if (t.count == kTable || (i == n && t.count)) {
-        t.base = done;
-        f(t, t.first[t.count]);
-        done += t.first[t.count];
-        t.count = 0;
-      }
-    }
+      launch(t, groups_of(units));
+      t.base += groups_of(units);
+    });
   };
-  tables([&](const ClipTable &t, uint32_t pieces) {
-    hipLaunchKernelGGL(clip_squares_kernel, dim3(pieces), dim3(kClipThreads), 0, s, t, partial);
+  tables([&](const ClipTable &t, uint32_t groups) {
+    hipLaunchKernelGGL(clip_squares_kernel, dim3(groups), dim3(kClipThreads), 0, s, t, partial);
   });
-  if (!out || c.count == 0) {
-    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kClipThreads), 0, s, partial, uint32_t(c.count), norm);
+  if (!out || sums == 0) {
+    hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kClipThreads), 0, s, partial, uint32_t(sums), norm);
   } else {
-    tables([&](const ClipTable &t, uint32_t pieces) {
-      hipLaunchKernelGGL(clip_scale_kernel, dim3(pieces < 2048 ? pieces : 2048), dim3(kClipThreads), 0, s, t, partial,
-                         uint32_t(c.count), pieces, max_norm, norm);
+    tables([&](const ClipTable &t, uint32_t groups) {
+      hipLaunchKernelGGL(clip_scale_kernel, dim3(groups), dim3(kClipThreads), 0, s, t, partial, uint32_t(sums), max_norm,
+                         norm, bytes >= kStreamed);
     });
   }
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
@@ -287,9 +306,8 @@ int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const in
 extern "C" {
 
 int64_t tss_clip_grad_norm_workspace_size(int64_t n, const int64_t *sizes) {
-  Pieces c;
-  const int32_t st = cut(n, sizes, &c);
-  return st != TSS_OK ? st : c.count * 8;
+  const int64_t sums = count_sums(n, sizes);
+  return sums < 0 ? sums : sums * 8;
 }
 
 int32_t tss_clip_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,

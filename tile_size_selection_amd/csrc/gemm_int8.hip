@@ -89,25 +89,42 @@ constexpr int64_t kMostK = (int64_t(1) << 17) - 1;  // 2^14 of a product, 2^31 o
 
 bool off_by(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
 
-using Tile256 = Int8Geometry<256, 256, 2, 8, 2>;
-using Tile128 = Int8Geometry<128, 128, 3, 8, 2>;
+using Tile256 = Int8Geometry<256, 256, 2, 8, 2>;  // with its pieces: large products
+using Piece256 = Int8Geometry<128, 256, 3, 8, 2>;
+using Tile128 = Int8Geometry<128, 128, 3, 8, 2>;  // also one round of its own
 using Tile64 = Int8Geometry<64, 128, 3, 4, 1>;  // two workgroups a CU
 
-template <typename G>
-hipError_t launch_tile(const Int8Args &a, int64_t blocks, hipStream_t s) {
-  // Dynamic LDS above 64 KiB needs an attribute per kernel and device: set on the first launch there.
-  static std::atomic<uint64_t> attr_set{0};
+constexpr int kRoundsLds = Tile256::LDS_BYTES > Piece256::LDS_BYTES ? Tile256::LDS_BYTES : Piece256::LDS_BYTES;
+
+// Dynamic LDS above 64 KiB needs an attribute per kernel and device: set on the first launch there.
+template <typename Kernel>
+hipError_t launch_lds(Kernel kernel, std::atomic<uint64_t> &attr_set, const Int8Args &a, int64_t blocks, int threads,
+                      int lds, hipStream_t s) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
   if (!bit || !(attr_set.load(std::memory_order_acquire) & bit)) {
-    e = hipFuncSetAttribute((const void *)gemm_int8_tile_kernel<G>, hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
+    e = hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, 163840);
     if (e != hipSuccess) return e;
     attr_set.fetch_or(bit, std::memory_order_acq_rel);
   }
-  hipLaunchKernelGGL(gemm_int8_tile_kernel<G>, dim3(uint32_t(blocks)), dim3(G::THREADS), G::LDS_BYTES, s, a);
+  hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(threads), lds, s, a);
   return hipGetLastError();
+}
+
+template <typename G, int KG>
+hipError_t launch_tile(const Int8Args &a, int64_t blocks, hipStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};
+  return launch_lds(gemm_int8_tile_kernel<G, KG>, attr_set, a, blocks, KG * G::THREADS, KG * G::LDS_BYTES, s);
+}
+
+hipError_t launch_rounds(const Int8Args &a, int64_t tiles, hipStream_t s) {
+  static std::atomic<uint64_t> attr_set{0};
+  const int64_t whole = tiles / kCUs * kCUs, rest = tiles - whole;
+  if (rest == 0 || tile_pieces(int(rest), false) == 1) return launch_tile<Tile256, 1>(a, tiles, s);
+  return launch_lds(gemm_int8_rounds_kernel<Tile256, Piece256, Tile128>, attr_set, a,
+                    whole + rest * tile_pieces(int(rest), false), Tile256::THREADS, kRoundsLds, s);
 }
 
 // Waves of a workgroup of the kernel for few rows.
@@ -213,7 +230,8 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   a.out_dtype = split ? kInt8Sums : out_dtype;
   const int64_t tiles_m = (M + pl.bm - 1) / pl.bm, tiles_n = (N + pl.bn - 1) / pl.bn, blocks = tiles_m * tiles_n * a.splits;
   const int threads = pl.bn == 16 ? rows_waves(K) * 64 : 512;
-  if (blocks * threads > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
+  // the launch's thread count is 32 bits (tiles: 512 threads at most, and a round's pieces)
+  if ((blocks + 2 * kCUs) * threads > int64_t(UINT32_MAX)) return TSS_E_ARG;
   a.tiles_m = int32_t(tiles_m);
   a.tiles_n = int32_t(tiles_n);
   hipError_t err;
@@ -221,11 +239,11 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
     hipLaunchKernelGGL(gemm_int8_rows_kernel, dim3(uint32_t(blocks)), dim3(threads), threads * 16, s, a);
     err = hipGetLastError();
   } else if (pl.bm == 256) {
-    err = launch_tile<Tile256>(a, blocks, s);
+    err = launch_rounds(a, blocks, s);
   } else if (pl.bm == 128) {
-    err = launch_tile<Tile128>(a, blocks, s);
+    err = launch_tile<Tile128, 1>(a, blocks, s);
   } else {
-    err = launch_tile<Tile64>(a, blocks, s);
+    err = pl.sets == 2 ? launch_tile<Tile64, 2>(a, blocks, s) : launch_tile<Tile64, 1>(a, blocks, s);
   }
   if (err == hipSuccess && split) err = launch_join(a, C, out_dtype, s);
   return err == hipSuccess ? TSS_OK : TSS_E_HIP;

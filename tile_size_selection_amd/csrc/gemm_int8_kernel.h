@@ -9,9 +9,10 @@
 // joined without a rounding.  As in the 16-bit kernel the B fragment is the
 // MFMA's row operand: a lane holds 4 consecutive columns of one row of C.
 //
-// Two kernels: gemm_int8_tile_kernel stages BM x 128 and BN x 128 tiles of the
-// operands through LDS; gemm_int8_rows_kernel, for few rows, streams B from
-// memory straight into registers.
+// Three kernels: gemm_int8_tile_kernel stages BM x 128 and BN x 128 tiles of the
+// operands through LDS; gemm_int8_rounds_kernel does so with the last round's
+// tiles in pieces; gemm_int8_rows_kernel, for few rows, streams B from memory
+// straight into registers.
 #pragma once
 #include "gemm_fp8_kernel.h"
 
@@ -68,6 +69,19 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) {
   return v;
 }
 
+struct Int8Tile {
+  int row0, n0, split;
+};
+
+// Tile `id` of the product, bm x bn.
+template <int BM, int BN>
+__device__ __forceinline__ Int8Tile int8_tile_at(const Int8Args &p, int id) {
+  const int mn = p.tiles_m * p.tiles_n, split = id / mn, in = id - split * mn;
+  constexpr int GM = 4;  // tile rows that share an XCD's run of tiles
+  const int span = GM * p.tiles_n, first = in / span * GM, gm = min(p.tiles_m - first, GM), r = in % span;
+  return {(first + r % gm) * BM, r / gm * BN, split};
+}
+
 // One tile's product.  A step of K (128) runs in two halves around its
 // barrier, as in the 8-bit floating-point kernel:
 //   1. rows 0 .. TM/2-1; as a row ends, its A fragment is replaced by that of
@@ -76,18 +90,23 @@ __device__ __forceinline__ float scaled_sum(int sum, float sa, float sb) {
 //   2. rows TM/2 .., column by column; as a column ends, its B fragment is
 //      replaced by the next step's, and after the last column the A fragments
 //      are; the slot is refilled meanwhile.
-template <typename G>
-__global__ __launch_bounds__(G::THREADS) void gemm_int8_tile_kernel(Int8Args p) {
-  extern __shared__ __attribute__((aligned(1024))) char smem[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+//
+// KG > 1: as many sets of G::NW waves share the tile, each taking a range of K
+// with a ring of its own; their sums are added at the end.  It fills a CU where
+// there are too few tiles for two workgroups each.
+template <typename G, int KG>
+__device__ __forceinline__ void int8_tile_product(const Int8Args &p, const Int8Tile &t, char *smem0) {
+  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int set = KG > 1 ? wave_all / G::NW : 0, wave = KG > 1 ? wave_all % G::NW : wave_all;
   const int wr = wave / G::WN, wc = wave % G::WN;
-  const int id = xcd_run(blockIdx.x, gridDim.x), mn = p.tiles_m * p.tiles_n;
-  const int split = id / mn, at = id - split * mn;
-  constexpr int GM = 4;  // tile rows that share an XCD's run of tiles
-  const int span = GM * p.tiles_n, first = at / span * GM, gm = min(p.tiles_m - first, GM), r = at % span;
-  const int row0 = (first + r % gm) * G::BM, n0 = r / gm * G::BN;
-  const int rows = min(G::BM, p.M - row0), cols = min(G::BN, p.N - n0);
-  const int kbeg = split * p.k_split, K = max(0, min(p.k_split, p.K - kbeg)), nk = (K + 127) / 128;
+  char *smem = smem0 + set * G::LDS_BYTES;
+  const int row0 = t.row0, n0 = t.n0, rows = min(G::BM, p.M - row0), cols = min(G::BN, p.N - n0);
+  int kbeg = t.split * p.k_split, K = max(0, min(p.k_split, p.K - kbeg));
+  const int steps = (K + KG * 128 - 1) / (KG * 128);  // of every set; past a set's end they add zeros
+  if constexpr (KG > 1) {
+    kbeg += set * steps * 128;
+    K = max(0, min(K - set * steps * 128, steps * 128));
+  }
 
   const i32x4 rsA = buffer_rsrc(p.A + int64_t(row0) * p.K + kbeg, K ? uint32_t(rows - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
   const i32x4 rsB = buffer_rsrc(p.B + int64_t(n0) * p.K + kbeg, K ? uint32_t(cols - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
@@ -138,7 +157,7 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_tile_kernel(Int8Args p) 
     for (int j = 0; j < TN; ++j) fb[j] = frag(stb + j * 16 * 128);
   }
   int slot = 0;
-  for (int kt = 0; kt < nk; ++kt) {
+  for (int kt = 0; kt < steps; ++kt) {
     const int next = slot + 1 == ST ? 0 : slot + 1;
     const char *sta = smem + slot * G::STAGE_BYTES + wr * G::WTM * 128;
     const char *stn = smem + next * G::STAGE_BYTES;
@@ -171,6 +190,34 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_tile_kernel(Int8Args p) 
     slot = next;
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
+  if constexpr (KG > 1) {
+    typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
+    lds_i32x4 *sums = (lds_i32x4 *)smem0;  // [set - 1][MFMA tile][wave][lane]
+    static_assert((KG - 1) * TM * TN * G::NW * 1024 <= KG * G::LDS_BYTES, "the sets' sums fit");
+    block_barrier();
+    if (set > 0) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sums[(((set - 1) * TM * TN + i * TN + j) * G::NW + wave) * 64 + lane] = acc[i][j];
+      wait_vmcnt_lgkm0<0>();
+    }
+    block_barrier();
+    if (set > 0) {
+      block_barrier();  // the one that the store begins with
+      return;
+    }
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+          const i32x4 v = sums[((g * TM * TN + i * TN + j) * G::NW + wave) * 64 + lane];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
+        }
+    wait_vmcnt_lgkm0<0>();
+  }
 
   f32x4 out[TM][TN];
   const bool sums = p.out_dtype == kInt8Sums;
@@ -196,13 +243,41 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_tile_kernel(Int8Args p) 
   }
   auto store = [&](auto o) __attribute__((always_inline)) {
     using O = decltype(o);
-    O *C = static_cast<O *>(p.C) + split * slice_elements(p.M, p.N);
+    O *C = static_cast<O *>(p.C) + t.split * slice_elements(p.M, p.N);
     if (p.N % 8 == 0) store_tile<G, O>(out, C, smem, row0, n0, wave, wr, wc, lane, p.M, p.N);
     else store_tile_unaligned<G, O>(out, C, smem, row0, n0, wave, wr, wc, lane, p.M, p.N);
   };
   if (p.out_dtype == TSS_F16) store(_Float16{});
   else if (p.out_dtype == TSS_BF16) store(__bf16{});
   else store(float{});  // fp32, and 32-bit sums as they are
+}
+
+template <typename G, int KG>
+__global__ __launch_bounds__(G::THREADS *KG) void gemm_int8_tile_kernel(Int8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  int8_tile_product<G, KG>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(blockIdx.x, gridDim.x)), smem);
+}
+
+// Large products: one workgroup fills a CU, and the last round's tiles are cut
+// into pieces (tile_pieces).
+template <typename G, typename Half, typename Quarter>
+__global__ __launch_bounds__(G::THREADS) void gemm_int8_rounds_kernel(Int8Args p) {
+  extern __shared__ __attribute__((aligned(1024))) char smem[];
+  static_assert(G::THREADS == Half::THREADS && G::THREADS == Quarter::THREADS && Half::BM * 2 == G::BM &&
+                    Quarter::BM * 2 == G::BM && Half::BN == G::BN && Quarter::BN * 2 == G::BN, "pieces of a tile");
+  const int bid = blockIdx.x, n = p.tiles_m * p.tiles_n;
+  const int whole = n / kCUs * kCUs, rest = n - whole, pieces = tile_pieces(rest, false);
+  if (bid < whole) {
+    int8_tile_product<G, 1>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(bid, whole)), smem);
+    return;
+  }
+  const int piece = xcd_run(bid - whole, rest * pieces), part = piece % pieces;
+  Int8Tile t = int8_tile_at<G::BM, G::BN>(p, whole + piece / pieces);
+  t.row0 += (pieces == 2 ? part : part / 2) * Half::BM;
+  if (pieces == 4) t.n0 += part % 2 * Quarter::BN;
+  if (t.row0 >= p.M || t.n0 >= p.N) return;
+  if (pieces == 2) int8_tile_product<Half, 1>(p, t, smem);
+  else int8_tile_product<Quarter, 1>(p, t, smem);
 }
 
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it

@@ -24,18 +24,22 @@ namespace {
 // ---- the sort ----
 
 constexpr int kSortThreads = 1024;
-constexpr int kSortCounters = 16000;       // LDS counters, 64 KB
-constexpr int64_t kOneGroup = 8192;        // choices that one workgroup sorts by itself
+constexpr int kSortCounters = 9600;        // LDS counters
+constexpr int64_t kOneGroup = 4096;        // choices that one workgroup sorts by itself
+constexpr int kHeld = 8192;                // choices whose bins a workgroup keeps
+constexpr int64_t kScannedCounts = 8192;   // more counts than these are added up by a launch of their own
 
 struct SortArgs {
   const void *expert;
   int n, E;
   int per_group;      // choices of a workgroup, a multiple of 64
+  int placing;        // waves that share them
+  bool scanned;
   int32_t *sizes, *row, *choice;
-  uint32_t *counts;   // [workgroups][E + 1]
+  uint32_t *counts;   // [workgroups + 1][E + 1]
 };
 
-// Waves of a sorting workgroup: as many as have counters of their own.
+// Waves that place choices: as many as have counters of their own.
 __host__ __device__ constexpr int sort_waves(int E) {
   const int w = kSortCounters / (E + 1);
   return w >= 16 ? 16 : w >= 8 ? 8 : w >= 4 ? 4 : w >= 2 ? 2 : 1;
@@ -46,13 +50,6 @@ template <typename I>
 __device__ __forceinline__ int bin_of(const SortArgs &p, int i) {
   const I e = static_cast<const I *>(p.expert)[i];
   return e >= 0 && e < I(p.E) ? int(e) : p.E;
-}
-
-// Counts a wave's choices [from, end) into its counters (zeroed by the caller).
-template <typename I>
-__device__ __forceinline__ void count_choices(const SortArgs &p, int from, int end, int lane, uint32_t *mine) {
-  for (int i0 = from; i0 < end; i0 += 64)
-    if (i0 + lane < end) atomicAdd(&mine[bin_of<I>(p, i0 + lane)], 1u);
 }
 
 template <typename I>
@@ -67,87 +64,171 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortArgs p) {
   for (int b = threadIdx.x; b < bins; b += blockDim.x) p.counts[int64_t(blockIdx.x) * bins + b] = count[b];
 }
 
+// Each bin's counts become its choices in the workgroups before; the row
+// behind the last holds the totals.  For many bins or workgroups: else every
+// placing workgroup adds them up by itself, which saves a launch.
+__global__ __launch_bounds__(256) void sort_scan_kernel(int groups, int bins, uint32_t *counts) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= bins) return;
+  uint32_t sum = 0;
+  for (int g0 = 0; g0 < groups; g0 += 16) {
+    uint32_t c[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) c[u] = g0 + u < groups ? counts[int64_t(g0 + u) * bins + b] : 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+      if (g0 + u < groups) counts[int64_t(g0 + u) * bins + b] = sum;
+      sum += c[u];
+    }
+  }
+  counts[int64_t(groups) * bins + b] = sum;
+}
+
 // Places: a bin begins behind all smaller bins, a workgroup's part of it
 // behind those of the workgroups before it, a wave's behind those of its
 // workgroup's earlier waves; within a wave 64 choices at a time, each behind
 // the lanes before it that have the same bin.
-template <typename I>
+template <typename I, bool MANY>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
-  extern __shared__ uint32_t lds[];
-  __shared__ uint32_t wave_sum[kSortThreads / 64];
-  const int bins = p.E + 1, nw = blockDim.x >> 6, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  uint32_t *count = lds;  // [waves][bins]
-  for (int b = threadIdx.x; b < nw * bins; b += blockDim.x) count[b] = 0;
-  __syncthreads();
-  const int per_wave = (p.per_group / nw + 63) / 64 * 64;
-  const int group_end = min(int64_t(p.n), (int64_t(blockIdx.x) + 1) * p.per_group);
-  const int from = min(group_end, int(blockIdx.x) * p.per_group + wave * per_wave), end = min(group_end, from + per_wave);
+  extern __shared__ uint32_t count[];  // [placing waves][bins]
+  __shared__ uint32_t wave_sum[kSortThreads / 64], share[2][MANY ? kSortThreads : 1];
+  __shared__ uint16_t held_bins[kHeld];
+  const int bins = p.E + 1, wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int groups = MANY ? gridDim.x : 1, group = MANY ? blockIdx.x : 0;  // not MANY: one workgroup sorts all
+  const int placing = p.placing;
+  const int per_wave = p.per_group / placing;  // a multiple of 64
+  const int group_end = min(int64_t(p.n), (int64_t(group) + 1) * p.per_group);
+  const int from = wave < placing ? min(group_end, group * p.per_group + wave * per_wave) : group_end;
+  const int end = min(group_end, from + per_wave);
   uint32_t *mine = count + wave * bins;
-  count_choices<I>(p, from, end, lane, mine);
-  __syncthreads();
-  // the waves' counters become the waves' first places, bin by bin, 1024 bins at a time
-  uint32_t before_bins = 0;
-  for (int b0 = 0; b0 < bins; b0 += blockDim.x) {
-    const int b = b0 + threadIdx.x;
-    uint32_t total = 0, before = 0;  // of all workgroups; of those before this one
-    if (b < bins) {
-      if (gridDim.x > 1) {
+  // Bins b0 .. b0 + width - 1 of the workgroups (few bins: the threads share the
+  // workgroups among them): in all, and of those before this one.
+  int width = kSortThreads;
+  while (width / 2 >= bins) width /= 2;
+  const int parts = kSortThreads / width, at = threadIdx.x & (width - 1), part = threadIdx.x / width;
+  uint32_t total = 0, before = 0;
+  auto add_groups = [&](int b) __attribute__((always_inline)) {
+    total = before = 0;
+    if (b >= bins) return;
+    if (p.scanned) {
+      total = p.counts[int64_t(groups) * bins + b];
+      before = p.counts[int64_t(group) * bins + b];
+    } else {
 #pragma unroll 8
-        for (int g = 0; g < int(gridDim.x); ++g) {
-          const uint32_t c = p.counts[int64_t(g) * bins + b];
-          total += c;
-          before += g < int(blockIdx.x) ? c : 0;
-        }
-      } else {
-        for (int w = 0; w < nw; ++w) total += count[w * bins + b];
+      for (int g = part; g < groups; g += parts) {
+        const uint32_t c = p.counts[int64_t(g) * bins + b];
+        total += c;
+        before += g < group ? c : 0;
       }
+    }
+  };
+  const bool shared = MANY && !p.scanned && parts > 1;
+  if constexpr (MANY) add_groups(p.scanned ? threadIdx.x : at);
+  for (int b = threadIdx.x; b < placing * bins; b += kSortThreads) count[b] = 0;
+  if (shared) {
+    share[0][threadIdx.x] = total;
+    share[1][threadIdx.x] = before;
+  }
+  __syncthreads();
+  // the bins are kept for the second time, if the workgroup's fit
+  const bool held = !MANY || p.per_group <= kHeld;
+  uint16_t *kept_bins = held_bins - group * p.per_group;
+#pragma unroll 4
+  for (int i = from + lane; i < end; i += 64) {
+    const int b = bin_of<I>(p, i);
+    if (held) kept_bins[i] = uint16_t(b);
+    atomicAdd(&mine[b], 1u);
+  }
+  if (shared) {
+    total = before = 0;
+    if (part == 0)
+      for (int i = 0; i < parts; ++i) {
+        total += share[0][i * width + at];
+        before += share[1][i * width + at];
+      }
+  }
+  __syncthreads();
+  // the waves' counters become the waves' first places, bin by bin
+  uint32_t before_bins = 0;
+  for (int b0 = 0; b0 < bins; b0 += kSortThreads) {
+    const int b = b0 + threadIdx.x;
+    if constexpr (!MANY) {
+      total = 0;
+      if (b < bins)
+#pragma unroll 4
+        for (int w = 0; w < placing; ++w) total += count[w * bins + b];
+    } else if (b0 > 0) {
+      add_groups(b);  // as many bins as threads: none is shared
     }
     uint32_t upto = scan64(total, 0x7fffffffu, lane);
     if (lane == 63) wave_sum[wave] = upto;
     __syncthreads();
     uint32_t all = 0;
-    for (int w = 0; w < nw; ++w) {
+#pragma unroll 4
+    for (int w = 0; w < kSortThreads / 64; ++w) {
       const uint32_t s = wave_sum[w];
       upto += w < wave ? s : 0;
       all += s;
     }
     if (b < bins) {
-      uint32_t at = before_bins + upto - total + before;
-      for (int w = 0; w < nw; ++w) {
-        const uint32_t c = count[w * bins + b];
-        count[w * bins + b] = at;
-        at += c;
+      uint32_t first = before_bins + upto - total + before;
+#pragma unroll 1
+      for (int w0 = 0; w0 < placing; w0 += 4) {
+        uint32_t c[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) c[u] = w0 + u < placing ? count[(w0 + u) * bins + b] : 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (w0 + u < placing) count[(w0 + u) * bins + b] = first;
+          first += c[u];
+        }
       }
-      if (blockIdx.x == 0 && b < p.E) p.sizes[b] = int32_t(total);
+      if (group == 0 && b < p.E) p.sizes[b] = int32_t(total);
     }
     before_bins += all;
     __syncthreads();
   }
+#pragma unroll 1
   for (int i0 = from; i0 < end; i0 += 64) {
     const int i = i0 + lane;
     const bool in = i < end;
-    const int b = in ? bin_of<I>(p, i) : bins;
+    const int b = !in ? bins : held ? kept_bins[i] : bin_of<I>(p, i);
     uint64_t same = __ballot(in);  // the lanes with this lane's bin
+#pragma unroll 1
     for (int bit = 1; bit < bins; bit *= 2) {
       const uint64_t set = __ballot(b & bit);
       same &= b & bit ? set : ~set;
     }
     if (in) {
       const int first = __builtin_ctzll(same);
-      uint32_t at = 0;
-      if (lane == first) at = atomicAdd(&mine[b], uint32_t(__builtin_popcountll(same)));
-      at = __shfl(at, first) + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
+      uint32_t to = 0;
+      if (lane == first) to = atomicAdd(&mine[b], uint32_t(__builtin_popcountll(same)));
+      to = __shfl(to, first) + __builtin_popcountll(same & ((uint64_t(1) << lane) - 1));
       const bool kept = b < p.E;
-      p.row[i] = kept ? int32_t(at) : ~int32_t(at);
-      p.choice[at] = kept ? i : ~i;
+      p.row[i] = kept ? int32_t(to) : ~int32_t(to);
+      p.choice[to] = kept ? i : ~i;
     }
   }
 }
 
-int64_t sort_groups(int64_t n) {
-  if (n <= kOneGroup) return 1;
-  const int64_t g = (n + 2047) / 2048;
-  return g < 128 ? g : 128;
+// How choices are dealt to workgroups.  One up to 4096 (us, captured, E = 128 to
+// 256: 4096 choices 7.0 by one workgroup, 7.9 by two launches; 8192 9.7 and
+// 8.2), then 2048 each, 4096 from 2^16 on (32768: 10.5 and 11.3; 131072: 12.9
+// and 12.2; 2^20: 43 and 27).  The counts of the workgroups before are added up
+// by every workgroup, or from 8192 of them on by a launch of their own (4112
+// counts: 10.5 and 10.4; 8256: 12.9 and 12.4; 2064: 8.6 and 9.5).
+struct SortShape {
+  int64_t groups, per_group;
+  bool scanned;
+};
+SortShape sort_shape(int64_t n, int64_t E) {
+  const int64_t nw = sort_waves(int(E)), unit = nw * 64;
+  if (n <= kOneGroup && (nw == 16 || n <= nw * 512)) return {1, (n + unit - 1) / unit * unit, false};
+  const int64_t each = nw < 16 ? nw * 512 : n < 1 << 16 ? 2048 : 4096;
+  int64_t groups = (n + each - 1) / each;
+  groups = groups > 512 ? 512 : groups < 1 ? 1 : groups;
+  const int64_t per = ((n + groups - 1) / groups + unit - 1) / unit * unit;
+  return {groups, per, groups * (E + 1) > kScannedCounts};
 }
 
 // ---- rows ----
@@ -366,8 +447,8 @@ int64_t tss_sort_by_expert_workspace_size(int64_t tokens, int64_t top, int64_t E
   const int32_t st = check_tokens(tokens, top, 8);
   if (st != TSS_OK) return st;
   if (E < 1 || E > kMaxGroups) return TSS_E_ARG;
-  const int64_t g = sort_groups(tokens * top);
-  return g > 1 ? g * (E + 1) * 4 : 0;
+  const int64_t g = sort_shape(tokens * top, E).groups;
+  return g > 1 ? (g + 1) * (E + 1) * 4 : 0;
 }
 
 int32_t tss_sort_by_expert(int64_t tokens, int64_t top, int64_t E, const void *expert, int32_t expert_bits,
@@ -381,16 +462,21 @@ int32_t tss_sort_by_expert(int64_t tokens, int64_t top, int64_t E, const void *e
   for (const void *q : {(const void *)sizes, (const void *)row, (const void *)choice, (const void *)workspace})
     if (reinterpret_cast<uintptr_t>(q) & 3u) return TSS_E_ALIGN;
   if (reinterpret_cast<uintptr_t>(expert) & (expert_bits / 8 - 1)) return TSS_E_ALIGN;
-  const int64_t groups = sort_groups(n);
-  const int64_t per_group = ((n + groups - 1) / groups + 63) / 64 * 64;
-  const SortArgs a{expert, int(n), int(E), int(per_group), sizes, row, choice, static_cast<uint32_t *>(workspace)};
-  hipStream_t s = static_cast<hipStream_t>(stream);
+  const SortShape f = sort_shape(n, E);
   const int nw = sort_waves(int(E));
+  const SortArgs a{expert, int(n), int(E), int(f.per_group), nw, f.scanned, sizes, row, choice, static_cast<uint32_t *>(workspace)};
+  hipStream_t s = static_cast<hipStream_t>(stream);
   auto go = [&](auto i) {
     using I = decltype(i);
-    if (groups > 1)
-      hipLaunchKernelGGL(sort_count_kernel<I>, dim3(uint32_t(groups)), dim3(kSortThreads), (E + 1) * 4, s, a);
-    hipLaunchKernelGGL(sort_place_kernel<I>, dim3(uint32_t(groups)), dim3(nw * 64), nw * (E + 1) * 4, s, a);
+    if (f.groups > 1)
+      hipLaunchKernelGGL(sort_count_kernel<I>, dim3(uint32_t(f.groups)), dim3(kSortThreads), (E + 1) * 4, s, a);
+    if (f.scanned)
+      hipLaunchKernelGGL(sort_scan_kernel, dim3(uint32_t((E + 256) / 256)), dim3(256), 0, s, int(f.groups), int(E + 1),
+                         a.counts);
+    if (f.groups > 1)
+      hipLaunchKernelGGL((sort_place_kernel<I, true>), dim3(uint32_t(f.groups)), dim3(kSortThreads), nw * (E + 1) * 4, s, a);
+    else
+      hipLaunchKernelGGL((sort_place_kernel<I, false>), dim3(1), dim3(kSortThreads), nw * (E + 1) * 4, s, a);
   };
   if (expert_bits == 32) go(int32_t{});
   else go(int64_t{});

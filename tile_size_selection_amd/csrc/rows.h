@@ -84,6 +84,22 @@ __device__ __forceinline__ void store8(T *p, const float (&f)[8]) {
   }
 }
 
+// The same past the caches, for outputs that they would not hold anyway.
+template <typename T>
+__device__ __forceinline__ void store8_streamed(T *p, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_nontemporal_store(f32x4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]}, reinterpret_cast<f32x4 *>(p) + i);
+  } else {
+    typedef T T8 __attribute__((ext_vector_type(8)));
+    T8 h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (T)f[i];
+    __builtin_nontemporal_store(h, reinterpret_cast<T8 *>(p));
+  }
+}
+
 // |a|, |b| to the larger, NaN if either is NaN.
 __device__ __forceinline__ float max_abs(float a, float b) {
   return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
@@ -150,10 +166,12 @@ __device__ __forceinline__ float max_lanes(float v) {
 // element (the bare product moves some of the values that lie on a rounding
 // border of the 8-bit type, as many of those of a 16-bit type do).  |v| <= amax keeps the
 // quotient below the halfway point past the largest value, so the conversion
-// needs no clamp.
+// needs no clamp.  Integers have few values, and halves between them are
+// common quotients (x = amax / 2 is 63.5), so theirs is the quotient by amax /
+// 127 itself, not by its rounding to fp32: `low` is what the rounding left out.
 template <typename Q>
 struct BlockScale {
-  float scale, inv, back;
+  float scale, inv, back, low;
   explicit __device__ __forceinline__ BlockScale(float amax) {
     scale = __builtin_elementwise_maximum(amax, kSmallestAmax) / kLargest<Q>;
     const float r = __builtin_amdgcn_rcpf(scale);
@@ -161,9 +179,11 @@ struct BlockScale {
     const bool inf = scale == __builtin_inff();
     inv = inf ? 0.0f : __builtin_fmaf(__builtin_fmaf(-scale, r, 1.0f), r, r);
     back = inf ? 0.0f : -scale;
+    low = inf ? 0.0f : __builtin_fmaf(-kLargest<Q>, scale, __builtin_elementwise_maximum(amax, kSmallestAmax)) / -kLargest<Q>;
   }
   __device__ __forceinline__ float quotient(float v) const {
     const float t = v * inv;
+    if constexpr (__is_same(Q, I8)) return __builtin_fmaf(__builtin_fmaf(t, low, __builtin_fmaf(t, back, v)), inv, t);
     return __builtin_fmaf(__builtin_fmaf(t, back, v), inv, t);
   }
 };

@@ -9,7 +9,6 @@ rows x 128 columns, column-block-major: scale[column block][row or row block];
 those of 8-bit integers one for each row: scale[row]."""
 from __future__ import annotations
 
-import ctypes
 import functools
 from typing import NamedTuple, Optional, Sequence, Tuple
 
@@ -37,9 +36,17 @@ def _choice(value: str, what: str, allowed) -> str:
     return value
 
 
+def _fits(t, dtype, *shape) -> bool:
+    """Whether t is contiguous, of this element type and shape; the first call
+    puts the compiled function in its place (it takes a third of the time)."""
+    global _fits
+    _fits = C.bind().fits
+    return _fits(t, dtype, *shape)
+
+
 def _given(t, what: str, shape, dtype):
     """t, checked: contiguous, of this shape and element type."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if not _fits(t, dtype, *shape):
         raise ValueError(f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
                          f"{tuple(t.shape)}" + ("" if t.is_contiguous() else ", not contiguous"))
     return t
@@ -96,6 +103,14 @@ def _call(where: str, fn, tensors, *args):
             st = fn(*args, _raw_stream(index))
     if st != C.TSS_OK:
         C.check(st, where)
+
+
+def _run(entry: str, *args):
+    """The entry point of this name on args and the current stream, through the
+    compiled binding: tensors are given as they are, all on one GPU."""
+    st = getattr(C.bind(), entry)(*args)
+    if st != C.TSS_OK:
+        C.check(st, entry)
 
 
 def _blocks(n: int) -> int:
@@ -220,9 +235,8 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, out_dtype
         mean, rstd = (None, None) if stats is True else stats
         mean = _out(mean, "mean", (rows,), torch.float32, x.device)
         rstd = _out(rstd, "rstd", (rows,), torch.float32, x.device)
-    _call("tss_layer_norm", C.lib().tss_layer_norm, (x, weight, bias, out, residual, scale, residual_out, mean, rstd),
-          rows, d, _DT[dt], x.data_ptr(), _ptr(residual), weight.data_ptr(), _ptr(bias), eps, _DT[od], out.data_ptr(),
-          _ptr(scale), _ptr(residual_out), _ptr(mean), _ptr(rstd))
+    _run("tss_layer_norm", rows, d, _DT[dt], x, residual, weight, bias, float(eps), _DT[od], out, scale, residual_out, mean,
+         rstd)
     return LayerNorm(out, scale, residual_out, mean, rstd)
 
 
@@ -252,11 +266,8 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=Non
     if need < 0:
         C.check(int(need), "tss_layer_norm_backward_workspace_size")
     workspace = _workspace(workspace, need, dy.device)
-    _call("tss_layer_norm_backward", C.lib().tss_layer_norm_backward,
-          (dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace),
-          rows, d, _DT[dt], dy.data_ptr(), h.data_ptr(), weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _ptr(dh),
-          dx.data_ptr(), dweight.data_ptr(), _ptr(dbias), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+    _run("tss_layer_norm_backward", rows, d, _DT[dt], dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace,
+         workspace.nbytes)
     return dx, dweight, dbias
 
 
@@ -298,8 +309,7 @@ def quantize_int8(x, gated: bool = False, out=None, scale=None) -> Tuple["torch.
         d //= 2
     out = _out(out, "out", (rows, d), torch.int8, x.device)
     scale = _out(scale, "scale", (rows,), torch.float32, x.device)
-    _call("tss_quantize_int8", C.lib().tss_quantize_int8, (x, out, scale),
-          rows, d, _DT[dt], x.data_ptr(), int(gated), out.data_ptr(), scale.data_ptr())
+    _run("tss_quantize_int8", rows, d, _DT[dt], x, int(gated), out, scale)
     return out, scale
 
 
@@ -374,9 +384,7 @@ def gemm_int8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
     need = gemm_int8_workspace_size(M, N, K)
     if need:
         workspace = _workspace(workspace, need, A.device)
-    _call("tss_gemm_int8", C.lib().tss_gemm_int8, (A, B, sa, sb, out, workspace),
-          M, N, K, A.data_ptr(), B.data_ptr(), sa.data_ptr(), sb.data_ptr(), out.data_ptr(), _DT[out_dtype],
-          _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    _run("tss_gemm_int8", M, N, K, A, B, sa, sb, out, _DT[out_dtype], workspace, 0 if workspace is None else workspace.nbytes)
     return out
 
 
@@ -463,45 +471,40 @@ def gemm_grouped_fp8(A, B, sa, sb, sizes, out_dtype: str = "bf16", out=None, fp3
     return out
 
 
-def _dense(t, what: str):
-    """t, checked: its elements lie in memory without gaps, in any order of
-    its dimensions."""
-    if not t.is_contiguous():
-        step = 1
-        for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n > 1):
-            if stride != step:
-                raise ValueError(f"{what} must lie in memory without gaps, not with strides {t.stride()}")
-            step *= size
-    return t
+_CLIPPED = {_TORCH[n]: _DT[n] for n in ("f16", "bf16", "f32")} if torch is not None else {}
 
 
-def _clip(grads, max_norm: float, out, norm, workspace, where: str):
-    grads = list(grads)
-    types = [_DT[_name(t, "a gradient", ("f16", "bf16", "f32"))] for t in grads]
-    for t in grads:
-        _dense(t, "a gradient")
-    if out is not None:
+def _refuse_list(grads, out):
+    """Says what is wrong with lists of which one tensor cannot be taken."""
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+    for t, o in zip(grads, grads if out is None else out):
+        _name(t, "a gradient", ("f16", "bf16", "f32"))
+        if o.shape != t.shape or o.dtype != t.dtype or o.stride() != t.stride():
+            raise ValueError(f"an output must have its gradient's shape, type and strides, {t.dtype} {tuple(t.shape)} "
+                             f"{t.stride()}, not {o.dtype} {tuple(o.shape)} {o.stride()}")
+    raise ValueError("gradients must lie in memory without gaps")
+
+
+def _clip(grads, max_norm: float, out, norm, workspace):
+    if out is not None and out is not grads:
         out = list(out)
-        if len(out) != len(grads):
-            raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-        for t, o in zip(grads, out):
-            if o is not t and (o.shape != t.shape or o.dtype != t.dtype or o.stride() != t.stride()):
-                raise ValueError(f"an output must have its gradient's shape, type and strides, {t.dtype} "
-                                 f"{tuple(t.shape)} {t.stride()}, not {o.dtype} {tuple(o.shape)} {o.stride()}")
     if not grads and norm is None:
         raise ValueError("without tensors norm must be given")
     device = grads[0].device if grads else norm.device
+    table = C.bind().table(grads, out, _CLIPPED)
+    if table is None:
+        _refuse_list(grads, out)
+    at, sizes, types, to, index = table
     norm = _out(norm, "norm", (), torch.float32, device)
+    if grads and norm.get_device() != index:
+        raise ValueError("every tensor must be on the same GPU")
     n = len(grads)
-    sizes = (C.i64 * n)(*[t.numel() for t in grads])
     need = C.lib().tss_clip_grad_norm_workspace_size(n, sizes)
     if need < 0:
-        C.check(int(need), where)
+        C.check(int(need), "tss_clip_grad_norm_workspace_size")
     workspace = _workspace(workspace, need, device)
-    pointers = lambda ts: (ctypes.c_void_p * n)(*[t.data_ptr() for t in ts])  # noqa: E731
-    _call(where, C.lib().tss_clip_grad_norm, (norm, workspace, *grads, *(out or ())),
-          n, pointers(grads), sizes, (C.i32 * n)(*types), max_norm, None if out is None else pointers(out),
-          norm.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _run("tss_clip_grad_norm", n, at, sizes, types, float(max_norm), to, norm, workspace, workspace.nbytes)
     return norm
 
 
@@ -522,7 +525,7 @@ def grad_norm(grads: Sequence["torch.Tensor"], norm=None, workspace=None):
     """The norm over all elements of the tensors (f16, bf16, f32, mixed), a
     float32 scalar on the GPU: squares are added in 64 bits, in a fixed order.
     norm: the scalar to write into, else allocated."""
-    return _clip(grads, 0.0, None, norm, workspace, "tss_clip_grad_norm")
+    return _clip(grads, 0.0, None, norm, workspace)
 
 
 @_list_streamed
@@ -533,4 +536,4 @@ def clip_grad_norm(grads: Sequence["torch.Tensor"], max_norm: float, out=None, n
     norm; nothing is read back to the host.  A NaN norm makes every element
     NaN, an infinite one multiplies by 0.  Tensors must lie in memory without
     gaps, and none may be given twice or overlap another that is written."""
-    return _clip(grads, max_norm, grads if out is None else out, norm, workspace, "tss_clip_grad_norm")
+    return _clip(grads, max_norm, grads if out is None else out, norm, workspace)

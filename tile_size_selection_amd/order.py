@@ -12,7 +12,7 @@ from typing import NamedTuple, Optional, Tuple
 
 from . import _capi as C
 from .api import _workspace, torch
-from .ops import _DT, _TORCH, _call, _choice, _given, _name, _out, _ptr, _streamed
+from .ops import _DT, _TORCH, _choice, _given, _name, _out, _run, _streamed
 
 _FLOATS = ("f16", "bf16", "f32")
 
@@ -57,10 +57,8 @@ def sort_by_expert(expert, experts: int, sizes=None, row=None, choice=None, work
     choice = _out(choice, "choice", (tokens * top,), torch.int32, expert.device)
     if need:
         workspace = _workspace(workspace, need, expert.device)
-    _call("tss_sort_by_expert", C.lib().tss_sort_by_expert, (expert, sizes, row, choice, workspace),
-          tokens, top, experts, expert.data_ptr(), 64 if expert.dtype == torch.int64 else 32, sizes.data_ptr(),
-          row.data_ptr(), choice.data_ptr(), _ptr(workspace),
-          0 if workspace is None else workspace.numel() * workspace.element_size())
+    _run("tss_sort_by_expert", tokens, top, experts, expert, 64 if expert.dtype == torch.int64 else 32, sizes, row, choice,
+         workspace, 0 if workspace is None else workspace.nbytes)
     return ExpertOrder(sizes, row, choice)
 
 
@@ -86,9 +84,7 @@ def gather_rows(x, order: ExpertOrder, scale=None, out=None, scale_out=None):
         scale_out = _out(scale_out, "scale_out", (*scale.shape[:-1], tokens * top), torch.float32, x.device)
     elif scale_out is not None:
         raise ValueError("scale_out needs scale")
-    _call("tss_gather_rows", C.lib().tss_gather_rows, (x, order.row, order.choice, out, scale, scale_out),
-          tokens, top, d, _DT[dt], x.data_ptr(), order.row.data_ptr(), order.choice.data_ptr(), out.data_ptr(),
-          _ptr(scale), blocks, _ptr(scale_out))
+    _run("tss_gather_rows", tokens, top, d, _DT[dt], x, order.row, order.choice, out, scale, blocks, scale_out)
     return out if scale is None else (out, scale_out)
 
 
@@ -103,8 +99,7 @@ def _combine(rows, order: ExpertOrder, weight, out_dtype: Optional[str], out):
         _given(weight, "weight", (tokens, top), torch.float32)
     od = _choice(out_dtype or dt, "out_dtype", _FLOATS if dt == "f32" else (dt, "f32"))
     out = _out(out, "out", (tokens, d), _TORCH[od], rows.device)
-    _call("tss_combine_rows", C.lib().tss_combine_rows, (rows, order.row, order.choice, weight, out),
-          tokens, top, d, _DT[dt], rows.data_ptr(), order.row.data_ptr(), _ptr(weight), _DT[od], out.data_ptr())
+    _run("tss_combine_rows", tokens, top, d, _DT[dt], rows, order.row, weight, _DT[od], out)
     return out
 
 
@@ -143,8 +138,5 @@ def combine_rows_backward(dy, rows, order: ExpertOrder, weight, drows=None,
     _given(weight, "weight", (tokens, top), torch.float32)
     drows = _out(drows, "drows", (tokens * top, d), dy.dtype, dy.device)
     dweight = _out(dweight, "dweight", (tokens, top), torch.float32, dy.device)
-    _call("tss_combine_rows_backward", C.lib().tss_combine_rows_backward,
-          (dy, rows, order.row, order.choice, weight, drows, dweight),
-          tokens, top, d, _DT[dt], dy.data_ptr(), _DT[rt], rows.data_ptr(), order.row.data_ptr(), weight.data_ptr(),
-          drows.data_ptr(), dweight.data_ptr())
+    _run("tss_combine_rows_backward", tokens, top, d, _DT[dt], dy, _DT[rt], rows, order.row, weight, drows, dweight)
     return drows, dweight
