@@ -13,7 +13,7 @@ import torch
 
 import tile_size_selection_amd as tss
 import ops_util as U
-from test_ops_plans import PRODUCTS
+from test_int8_plans import WAYS
 
 pytestmark = pytest.mark.gpu
 
@@ -42,7 +42,7 @@ def check(a, b, sa, sb, out, got=None):
 
 
 # the sizes that reach every way of running an 8-bit product, and odd ones of every kind
-SIZES = sorted(set(PRODUCTS) | {
+SIZES = sorted(set(WAYS) | {
     (1, 1, 16), (1, 8192, 8192), (3, 17, 48), (16, 256, 512), (17, 256, 512), (33, 1000, 2064), (64, 4104, 1040),
     (129, 130, 128), (1000, 1001, 1024), (255, 4097, 656), (2049, 1100, 4096), (4097, 515, 2048)})
 

@@ -101,9 +101,10 @@ __device__ __forceinline__ double piece_squares(const T *g, int64_t from, int64_
   return s;
 }
 
-template <typename T>
-__device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, int64_t end, bool wide, bool stream,
-                                            float factor) {
+// STREAMED: the output passes the caches by (a template argument: stores of
+// both kinds behind a test are made one of the plain kind).
+template <bool STREAMED, typename T>
+__device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, int64_t end, bool wide, float factor) {
   if (wide) {
     const int64_t whole = from + (end - from) / 8 * 8;
     int64_t i = from + threadIdx.x * 8;
@@ -117,7 +118,7 @@ __device__ __forceinline__ void piece_scale(const T *g, T *out, int64_t from, in
         widen8(r[u], f);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[k] *= factor;
-        if (stream) store8_streamed(out + i + u * kClipThreads * 8, f);
+        if constexpr (STREAMED) store8_streamed(out + i + u * kClipThreads * 8, f);
         else store8(out + i + u * kClipThreads * 8, f);
       }
     }
@@ -176,8 +177,9 @@ __global__ __launch_bounds__(kClipThreads) void clip_norm_kernel(const double *p
   if (threadIdx.x == 0) *norm = float(sqrt(s));
 }
 
+template <bool STREAMED>
 __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t, const double *partial, uint32_t sums,
-                                                                  float max_norm, float *norm, bool stream) {
+                                                                  float max_norm, float *norm) {
   __shared__ double red[kClipThreads / 64];
   const double n = sqrt(total_squares(partial, sums, red));
   if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(n);
@@ -187,8 +189,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable t, c
   with_range(t, gridDim.x - 1 - blockIdx.x, gridDim.x, [&](auto v, int k, int64_t from, int64_t end) {
     using T = decltype(v);
     if (factor == 1.0f && t.out[k] == t.in[k]) return;
-    piece_scale(static_cast<const T *>(t.in[k]), static_cast<T *>(t.out[k]), from, end,
-                aligned16(t.in[k]) && aligned16(t.out[k]), stream, factor);
+    piece_scale<STREAMED>(static_cast<const T *>(t.in[k]), static_cast<T *>(t.out[k]), from, end,
+                aligned16(t.in[k]) && aligned16(t.out[k]), factor);
   });
 }
 
@@ -294,8 +296,10 @@ int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const in
     hipLaunchKernelGGL(clip_norm_kernel, dim3(1), dim3(kClipThreads), 0, s, partial, uint32_t(sums), norm);
   } else {
     tables([&](const ClipTable &t, uint32_t groups) {
-      hipLaunchKernelGGL(clip_scale_kernel, dim3(groups), dim3(kClipThreads), 0, s, t, partial, uint32_t(sums), max_norm,
-                         norm, bytes >= kStreamed);
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(groups), dim3(kClipThreads), 0, s, t, partial, uint32_t(sums), max_norm, norm);
+      };
+      bytes >= kStreamed ? go(clip_scale_kernel<true>) : go(clip_scale_kernel<false>);
     });
   }
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;

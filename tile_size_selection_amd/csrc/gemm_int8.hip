@@ -113,16 +113,16 @@ hipError_t launch_lds(Kernel kernel, std::atomic<uint64_t> &attr_set, const Int8
   return hipGetLastError();
 }
 
-template <typename G, int KG>
+template <typename G>
 hipError_t launch_tile(const Int8Args &a, int64_t blocks, hipStream_t s) {
   static std::atomic<uint64_t> attr_set{0};
-  return launch_lds(gemm_int8_tile_kernel<G, KG>, attr_set, a, blocks, KG * G::THREADS, KG * G::LDS_BYTES, s);
+  return launch_lds(gemm_int8_tile_kernel<G>, attr_set, a, blocks, G::THREADS, G::LDS_BYTES, s);
 }
 
 hipError_t launch_rounds(const Int8Args &a, int64_t tiles, hipStream_t s) {
   static std::atomic<uint64_t> attr_set{0};
   const int64_t whole = tiles / kCUs * kCUs, rest = tiles - whole;
-  if (rest == 0 || tile_pieces(int(rest), false) == 1) return launch_tile<Tile256, 1>(a, tiles, s);
+  if (rest == 0 || tile_pieces(int(rest), false) == 1) return launch_tile<Tile256>(a, tiles, s);
   return launch_lds(gemm_int8_rounds_kernel<Tile256, Piece256, Tile128>, attr_set, a,
                     whole + rest * tile_pieces(int(rest), false), Tile256::THREADS, kRoundsLds, s);
 }
@@ -241,9 +241,9 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   } else if (pl.bm == 256) {
     err = launch_rounds(a, blocks, s);
   } else if (pl.bm == 128) {
-    err = launch_tile<Tile128, 1>(a, blocks, s);
+    err = launch_tile<Tile128>(a, blocks, s);
   } else {
-    err = pl.sets == 2 ? launch_tile<Tile64, 2>(a, blocks, s) : launch_tile<Tile64, 1>(a, blocks, s);
+    err = launch_tile<Tile64>(a, blocks, s);
   }
   if (err == hipSuccess && split) err = launch_join(a, C, out_dtype, s);
   return err == hipSuccess ? TSS_OK : TSS_E_HIP;

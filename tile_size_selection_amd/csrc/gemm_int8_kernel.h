@@ -90,23 +90,12 @@ __device__ __forceinline__ Int8Tile int8_tile_at(const Int8Args &p, int id) {
 //   2. rows TM/2 .., column by column; as a column ends, its B fragment is
 //      replaced by the next step's, and after the last column the A fragments
 //      are; the slot is refilled meanwhile.
-//
-// KG > 1: as many sets of G::NW waves share the tile, each taking a range of K
-// with a ring of its own; their sums are added at the end.  It fills a CU where
-// there are too few tiles for two workgroups each.
-template <typename G, int KG>
-__device__ __forceinline__ void int8_tile_product(const Int8Args &p, const Int8Tile &t, char *smem0) {
-  const int lane = threadIdx.x & 63, wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int set = KG > 1 ? wave_all / G::NW : 0, wave = KG > 1 ? wave_all % G::NW : wave_all;
+template <typename G>
+__device__ __forceinline__ void int8_tile_product(const Int8Args &p, const Int8Tile &t, char *smem) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wr = wave / G::WN, wc = wave % G::WN;
-  char *smem = smem0 + set * G::LDS_BYTES;
   const int row0 = t.row0, n0 = t.n0, rows = min(G::BM, p.M - row0), cols = min(G::BN, p.N - n0);
-  int kbeg = t.split * p.k_split, K = max(0, min(p.k_split, p.K - kbeg));
-  const int steps = (K + KG * 128 - 1) / (KG * 128);  // of every set; past a set's end they add zeros
-  if constexpr (KG > 1) {
-    kbeg += set * steps * 128;
-    K = max(0, min(K - set * steps * 128, steps * 128));
-  }
+  const int kbeg = t.split * p.k_split, K = max(0, min(p.k_split, p.K - kbeg)), steps = (K + 127) / 128;
 
   const i32x4 rsA = buffer_rsrc(p.A + int64_t(row0) * p.K + kbeg, K ? uint32_t(rows - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
   const i32x4 rsB = buffer_rsrc(p.B + int64_t(n0) * p.K + kbeg, K ? uint32_t(cols - 1) * uint32_t(p.K) + uint32_t(K) : 0u);
@@ -190,35 +179,6 @@ __device__ __forceinline__ void int8_tile_product(const Int8Args &p, const Int8T
     slot = next;
   }
   wait_vmcnt_lgkm0<0>();  // copies past the end still land in the LDS that the epilogue reuses
-  if constexpr (KG > 1) {
-    typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
-    lds_i32x4 *sums = (lds_i32x4 *)smem0;  // [set - 1][MFMA tile][wave][lane]
-    static_assert((KG - 1) * TM * TN * G::NW * 1024 <= KG * G::LDS_BYTES, "the sets' sums fit");
-    block_barrier();
-    if (set > 0) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) sums[(((set - 1) * TM * TN + i * TN + j) * G::NW + wave) * 64 + lane] = acc[i][j];
-      wait_vmcnt_lgkm0<0>();
-    }
-    block_barrier();
-    if (set > 0) {
-      block_barrier();  // the one that the store begins with
-      return;
-    }
-    for (int g = 0; g < KG - 1; ++g)
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-          const i32x4 v = sums[((g * TM * TN + i * TN + j) * G::NW + wave) * 64 + lane];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] += v[e];
-        }
-    wait_vmcnt_lgkm0<0>();
-  }
-
   f32x4 out[TM][TN];
   const bool sums = p.out_dtype == kInt8Sums;
   float sb[TN][4];
@@ -252,10 +212,10 @@ __device__ __forceinline__ void int8_tile_product(const Int8Args &p, const Int8T
   else store(float{});  // fp32, and 32-bit sums as they are
 }
 
-template <typename G, int KG>
-__global__ __launch_bounds__(G::THREADS *KG) void gemm_int8_tile_kernel(Int8Args p) {
+template <typename G>
+__global__ __launch_bounds__(G::THREADS) void gemm_int8_tile_kernel(Int8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
-  int8_tile_product<G, KG>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(blockIdx.x, gridDim.x)), smem);
+  int8_tile_product<G>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(blockIdx.x, gridDim.x)), smem);
 }
 
 // Large products: one workgroup fills a CU, and the last round's tiles are cut
@@ -268,7 +228,7 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_rounds_kernel(Int8Args p
   const int bid = blockIdx.x, n = p.tiles_m * p.tiles_n;
   const int whole = n / kCUs * kCUs, rest = n - whole, pieces = tile_pieces(rest, false);
   if (bid < whole) {
-    int8_tile_product<G, 1>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(bid, whole)), smem);
+    int8_tile_product<G>(p, int8_tile_at<G::BM, G::BN>(p, xcd_run(bid, whole)), smem);
     return;
   }
   const int piece = xcd_run(bid - whole, rest * pieces), part = piece % pieces;
@@ -276,8 +236,8 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_rounds_kernel(Int8Args p
   t.row0 += (pieces == 2 ? part : part / 2) * Half::BM;
   if (pieces == 4) t.n0 += part % 2 * Quarter::BN;
   if (t.row0 >= p.M || t.n0 >= p.N) return;
-  if (pieces == 2) int8_tile_product<Half, 1>(p, t, smem);
-  else int8_tile_product<Quarter, 1>(p, t, smem);
+  if (pieces == 2) int8_tile_product<Half>(p, t, smem);
+  else int8_tile_product<Quarter>(p, t, smem);
 }
 
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it

@@ -46,15 +46,21 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
   const T *x = static_cast<const T *>(p.x), *residual = static_cast<const T *>(p.residual);
   const T *weight = static_cast<const T *>(p.weight), *bias = static_cast<const T *>(p.bias);
   auto col_of = [&](int c) __attribute__((always_inline)) { return (c * lanes + t) * 8; };
-  // sums over the row; `slot`: each use its own
-  auto row_sum = [&](float v, int slot) __attribute__((always_inline)) {
+  // two sums over the row; each use its own slots, `slot` and the next
+  auto row_sums = [&](float &u, float &v, int slot) __attribute__((always_inline)) {
+    u = sum_lanes<L>(u);
     v = sum_lanes<L>(v);
-    if (L < 64 || wpr == 1) return v;
-    if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
+    if (L < 64 || wpr == 1) return;
+    if ((threadIdx.x & 63) == 0) {
+      red[slot][wave] = u;
+      red[slot + 1][wave] = v;
+    }
     __syncthreads();
-    float s = 0;
-    for (int i = 0; i < wpr; ++i) s += red[slot][i];
-    return s;
+    u = v = 0;
+    for (int i = 0; i < wpr; ++i) {
+      u += red[slot][i];
+      v += red[slot + 1][i];
+    }
   };
 
   Raw8<T> xr[CH], rr[CH], wr[CH], br[CH];
@@ -64,8 +70,10 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
     const bool in = col < d;
     xr[c] = in ? load8(x + base + col) : zero8<T>();
     rr[c] = in && residual ? load8(residual + base + col) : zero8<T>();
-    wr[c] = in ? load8(weight + col) : zero8<T>();
-    br[c] = in && bias ? load8(bias + col) : zero8<T>();
+    if constexpr (CH < 4) {
+      wr[c] = in ? load8(weight + col) : zero8<T>();
+      br[c] = in && bias ? load8(bias + col) : zero8<T>();
+    }
   }
   float h[CH][8], sum = 0;
 #pragma unroll
@@ -82,7 +90,9 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
     for (int i = 0; i < 8; ++i) sum += h[c][i];
   }
   const float inv_d = 1.0f / float(d);
-  const float mean0 = row_sum(sum, 0) * inv_d;
+  float none = 0;
+  row_sums(sum, none, 0);
+  const float mean0 = sum * inv_d;
   float rest = 0, sq = 0;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
@@ -94,8 +104,9 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
       sq += h[c][i] * h[c][i];
     }
   }
-  const float off = row_sum(rest, 1) * inv_d;  // the mean of h - mean0: what mean0 lacks
-  const float var = fmaxf(row_sum(sq, 2) * inv_d - off * off, 0.0f);
+  row_sums(rest, sq, 2);
+  const float off = rest * inv_d;  // the mean of h - mean0: what mean0 lacks
+  const float var = fmaxf(sq * inv_d - off * off, 0.0f);
   // a NaN in the row has to come through the max above
   const float r = var == var && off == off ? 1.0f / __builtin_sqrtf(var + p.eps) : off;
   if (t == 0) {
@@ -106,6 +117,10 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     float w[8], b[8];
+    if constexpr (CH == 4) {  // there are not enough registers to hold them from the start
+      wr[c] = col_of(c) < d ? load8(weight + col_of(c)) : zero8<T>();
+      br[c] = col_of(c) < d && bias ? load8(bias + col_of(c)) : zero8<T>();
+    }
     widen8(wr[c], w);
     widen8(br[c], b);
 #pragma unroll
@@ -119,9 +134,9 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
   if constexpr (INT8) {
     amax = max_lanes<L>(amax);
     if (L == 64 && wpr > 1) {
-      if ((threadIdx.x & 63) == 0) red[3][wave] = amax;
+      if ((threadIdx.x & 63) == 0) red[0][wave] = amax;  // read before the second sums' barrier
       __syncthreads();
-      for (int i = 0; i < wpr; ++i) amax = __builtin_elementwise_maximum(amax, red[3][i]);
+      for (int i = 0; i < wpr; ++i) amax = __builtin_elementwise_maximum(amax, red[0][i]);
     }
     const BlockScale<I8> s(amax);
     if (t == 0) p.scale[row] = s.scale;
@@ -134,7 +149,11 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
 
 template <typename T, bool INT8>
 int32_t launch_norm(const NormArgs &a, hipStream_t s) {
-  const Team f = team_of(a.d, a.rows < 1024 ? 1 : 4);
+  // Two chunks a thread where they keep a row in one wave, without barriers
+  // (60000 x 520, bf16: 30.8 us, with two waves 48), else one (16384 x 4096,
+  // bf16 with residual: 114 us, two chunks 121, four 126).  Few rows: one, a
+  // row's latency is all that counts.
+  const Team f = team_of(a.d, a.rows >= 1024 && a.d > 512 && a.d <= 1024 ? 2 : 1);
   const int block = f.waves == 1 ? 256 : f.waves * 64, rpb = f.waves == 1 ? 256 / f.lanes : 1;
   const int64_t blocks = (int64_t(a.rows) + rpb - 1) / rpb;
   if (blocks * block > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
@@ -168,7 +187,9 @@ constexpr int kNarrowThreads = 256;
 // registers over its rows, a workgroup joins its teams' and writes them to its
 // own slice of the workspace (added up in a fixed order afterwards: no
 // atomics, the same bits on every run).  D rows' loads are in flight while a
-// row is reduced and written.
+// row is reduced and written; D == 0 (wide rows, whose registers are full with dw and db):
+// none are, and the row is read again, from the caches, for its output (8000 x 8200, fp16: 139 us, with
+// one row ahead, which spills, 190).
 template <typename T, int CH, int D, int L>
 __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_norm_backward_kernel(BackArgs p) {
   constexpr bool kNarrow = L < 64;
@@ -181,15 +202,23 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
   T *dx = static_cast<T *>(p.dx);
   auto col_of = [&](int c) __attribute__((always_inline)) { return (c * lanes + t) * 8; };
-  float w[CH][8], dw[CH][8], db[CH][8];
+  Raw8<T> weight[CH];
+  float dw[CH][8], db[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
-    widen8(col_of(c) < d ? load8(static_cast<const T *>(p.weight) + col_of(c)) : zero8<T>(), w[c]);
+    weight[c] = col_of(c) < d ? load8(static_cast<const T *>(p.weight) + col_of(c)) : zero8<T>();
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[c][i] = db[c][i] = 0;
   }
-  Raw8<T> a[D][CH], b[D][CH], e[D][CH];
-  float mean[D], rstd[D];
+  constexpr int S = D ? D : 1;
+  Raw8<T> a[S][CH], b[S][CH], e[S][CH];
+  // keeps the compiler from holding several chunks' values in fp32 over the loop
+  auto opaque = [](Raw8<T> &v) __attribute__((always_inline)) {
+    if constexpr (CH > 1)
+#pragma unroll
+      for (int i = 0; i < int(sizeof(T) / 2); ++i) asm("" : "+v"(v.v[i]));
+  };
+  float mean[S], rstd[S];
   auto load_row = [&](int s, int64_t row) __attribute__((always_inline)) {
     const int64_t base = row * d;
 #pragma unroll
@@ -207,33 +236,47 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   for (int s = 0; s < D; ++s) load_row(s, int64_t(first) + int64_t(s) * stride);
   const float inv_d = 1.0f / float(d);
   int slot = 0;
-  for (int64_t row0 = first; row0 < rows; row0 += int64_t(D) * stride) {
+  for (int64_t row0 = first; row0 < rows; row0 += int64_t(S) * stride) {
 #pragma unroll
-    for (int s = 0; s < D; ++s) {
+    for (int s = 0; s < S; ++s) {
       const int64_t row = row0 + int64_t(s) * stride;
       if (row >= rows) break;
-      const float m = mean[s], r = rstd[s];
       Raw8<T> ca[CH], cb[CH], ce[CH];
+      if constexpr (D > 0) {
 #pragma unroll
-      for (int c = 0; c < CH; ++c) {
-        ca[c] = a[s][c];
-        cb[c] = b[s][c];
-        ce[c] = e[s][c];
+        for (int c = 0; c < CH; ++c) {
+          ca[c] = a[s][c];
+          cb[c] = b[s][c];
+          ce[c] = e[s][c];
+        }
+      } else {
+        mean[0] = p.mean[row];
+        rstd[0] = p.rstd[row];
       }
-      load_row(s, row + int64_t(D) * stride);
+      const float m = mean[s], r = rstd[s];
+      if constexpr (D > 0) load_row(s, row + int64_t(D) * stride);
       float sg = 0, sx = 0;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        float g[8], x[8];
-        widen8(ca[c], g);
-        widen8(cb[c], x);
+        float g[8], x[8], w[8];
+        if constexpr (D > 0) {
+          widen8(ca[c], g);
+          widen8(cb[c], x);
+        } else {
+          if constexpr (CH > 2) asm volatile("" ::: "memory");  // one chunk's registers at a time
+          const bool in = col_of(c) < d;
+          widen8(in ? load8(dy + row * d + col_of(c)) : zero8<T>(), g);
+          widen8(in ? load8(hh + row * d + col_of(c)) : zero8<T>(), x);
+        }
+        opaque(weight[c]);
+        widen8(weight[c], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {  // columns past the row: g = w = 0
           const float gx = (x[i] - m) * r * g[i];
           dw[c][i] += gx;
           db[c][i] += g[i];
-          sg += g[i] * w[c][i];
-          sx += gx * w[c][i];
+          sg += g[i] * w[i];
+          sx += gx * w[i];
         }
       }
       sg = sum_lanes<L>(sg);
@@ -256,14 +299,26 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
       sx *= inv_d;
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
-        if (col_of(c) >= d) continue;
-        float g[8], x[8], o[8];
-        widen8(ca[c], g);
-        widen8(cb[c], x);
-        widen8(ce[c], o);
+        const int col = col_of(c);
+        if (col >= d) continue;
+        float g[8], x[8], o[8], w[8];
+        if constexpr (D > 0) {
+          opaque(ca[c]);
+          opaque(cb[c]);
+          widen8(ca[c], g);
+          widen8(cb[c], x);
+          widen8(ce[c], o);
+        } else {
+          widen8(load8(dy + row * d + col), g);
+          widen8(load8(hh + row * d + col), x);
+          widen8(dh ? load8(dh + row * d + col) : zero8<T>(), o);
+        }
+        opaque(weight[c]);
+        widen8(weight[c], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[c][i] - sg - (x[i] - m) * r * sx);
-        store8(dx + row * d + col_of(c), o);
+        for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[i] - sg - (x[i] - m) * r * sx);
+        store8(dx + row * d + col, o);
+        if constexpr (CH > 2) asm volatile("" ::: "memory");
       }
     }
   }
@@ -304,15 +359,16 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   }
 }
 
-// Workgroups of the backward pass: 12 waves a CU and two workgroups at least,
-// but each adds 16 bytes a column (its shares of dw and db, written and read)
-// to the 8 a column that a row of 16-bit elements moves, so no more than one
-// for every 8 rows where that still gives every CU one.
+// Workgroups of the backward pass: 8 waves a CU (narrow rows: 16) and two
+// workgroups at least, but each adds 16 bytes a column (its shares of dw and
+// db, written and read) to the 8 a column that a row of 16-bit elements moves,
+// so no more than one for every 8 rows where that still gives every CU one.
+// 100000 x 512, bf16: 84 us, with 12 waves 90; 60000 x 1024, fp32: 187 and 203.
 int64_t backward_blocks(int64_t rows, int64_t d) {
   constexpr int64_t cus = 256;
   const Team f = team_of(d, 1);
   const int64_t teams = f.lanes < 64 ? kNarrowThreads / f.lanes : 1;
-  const int64_t per_cu = f.lanes < 64 ? 4 : 12 / f.waves, fill = cus * (per_cu > 2 ? per_cu : 2);
+  const int64_t per_cu = f.lanes < 64 ? 4 : 8 / f.waves, fill = cus * (per_cu > 2 ? per_cu : 2);
   const int64_t turns = (rows + teams - 1) / teams;  // a workgroup takes `teams` rows at a time
   const int64_t n = turns / 8 < cus ? cus : turns / 8 > fill ? fill : turns / 8;
   return turns < n ? turns : n;
@@ -321,14 +377,16 @@ int64_t backward_blocks(int64_t rows, int64_t d) {
 template <typename T>
 void launch_backward(const BackArgs &a, hipStream_t s) {
   const Team f = team_of(a.d, 1);
+  // One row ahead: two rows' registers leave room for fewer waves (300000 x 128,
+  // bf16: 63 us, two ahead 68; 16384 x 4096, fp32: 202 and 249; bf16 106 and 110).
   const dim3 grid(uint32_t(backward_blocks(a.rows, a.d))), block(f.lanes < 64 ? kNarrowThreads : f.waves * 64);
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
-  if (f.lanes == 8) go(layer_norm_backward_kernel<T, 1, 2, 8>);
-  else if (f.lanes == 16) go(layer_norm_backward_kernel<T, 1, 2, 16>);
-  else if (f.lanes == 32) go(layer_norm_backward_kernel<T, 1, 2, 32>);
-  else if (f.chunks == 1) go(layer_norm_backward_kernel<T, 1, 2, 64>);
-  else if (f.chunks == 2) go(layer_norm_backward_kernel<T, 2, 1, 64>);
-  else go(layer_norm_backward_kernel<T, 4, 1, 64>);
+  if (f.lanes == 8) go(layer_norm_backward_kernel<T, 1, 1, 8>);
+  else if (f.lanes == 16) go(layer_norm_backward_kernel<T, 1, 1, 16>);
+  else if (f.lanes == 32) go(layer_norm_backward_kernel<T, 1, 1, 32>);
+  else if (f.chunks == 1) go(layer_norm_backward_kernel<T, 1, 1, 64>);
+  else if (f.chunks == 2) go(layer_norm_backward_kernel<T, 2, 0, 64>);
+  else go(layer_norm_backward_kernel<T, 4, 0, 64>);
 }
 
 }  // namespace
