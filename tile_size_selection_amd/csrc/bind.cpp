@@ -128,6 +128,26 @@ struct Entry<F> {
   }
 };
 
+// A workspace's size: no tensor, no stream.
+template <auto F>
+struct Size;
+template <typename... A, int64_t (*F)(A...)>
+struct Size<F> {
+  template <size_t... I>
+  static int64_t run(const Slot *s, std::index_sequence<I...>) {
+    return F(as<A>(s[I])...);
+  }
+  static PyObject *call(PyObject *const *args, Py_ssize_t n) {
+    constexpr int kArgs = sizeof...(A);
+    if (n != kArgs) return PyErr_Format(PyExc_TypeError, "%d arguments, not %d", int(n), kArgs);
+    Slot s[kArgs];
+    int device = -1;
+    for (int i = 0; i < kArgs; ++i)
+      if (!take(args[i], s[i], device)) return nullptr;
+    return PyLong_FromLongLong(run(s, std::make_index_sequence<kArgs>()));
+  }
+};
+
 // fits(tensor, dtype, size, ...): contiguous, of this element type and shape.
 PyObject *fits(PyObject *const *args, Py_ssize_t n) {
   if (n < 2 || !THPVariable_Check(args[0]) || !THPDtype_Check(args[1]))
@@ -187,7 +207,12 @@ PyObject *method(PyObject *, PyObject *const *args, Py_ssize_t n) {
 
 #define TSS_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&f)), METH_FASTCALL, nullptr}
 #define TSS_ENTRY(name) TSS_METHOD(#name, method<Entry<name>::call>)
+#define TSS_SIZE(name) TSS_METHOD(#name, method<Size<name>::call>)
 PyMethodDef methods[] = {
+    TSS_SIZE(tss_layer_norm_backward_workspace_size),
+    TSS_SIZE(tss_gemm_int8_workspace_size),
+    TSS_SIZE(tss_clip_grad_norm_workspace_size),
+    TSS_SIZE(tss_sort_by_expert_workspace_size),
     TSS_METHOD("fits", method<fits>),
     TSS_METHOD("table", method<table>),
     TSS_ENTRY(tss_layer_norm),

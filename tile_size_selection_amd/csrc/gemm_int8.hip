@@ -127,10 +127,21 @@ hipError_t launch_rounds(const Int8Args &a, int64_t tiles, hipStream_t s) {
                     whole + rest * tile_pieces(int(rest), false), Tile256::THREADS, kRoundsLds, s);
 }
 
-// Waves of a workgroup of the kernel for few rows.
-int rows_waves(int64_t K) {
-  const int64_t nk = (K + 127) / 128, nw = (nk + kRowsUnroll - 1) / kRowsUnroll;
-  return int(nw > 16 ? 16 : nw < 1 ? 1 : nw);
+// The kernel for few rows: waves of a workgroup that takes `blocks` of K at a time in each.
+int rows_waves(int64_t K, int blocks) {
+  const int64_t nk = (K + 127) / 128, nw = (nk + blocks - 1) / blocks;
+  return int(nw > 16 ? 16 : nw);
+}
+
+hipError_t launch_rows(const Int8Args &a, hipStream_t s) {
+  auto go = [&](auto kernel, int groups, int blocks) {
+    const int nw = rows_waves(a.K, blocks), waves = nw > groups ? nw : groups;  // a wave joins each column group
+    const int64_t workgroups = int64_t(a.tiles_m) * ((int64_t(a.N) + 16 * groups - 1) / (16 * groups));
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(workgroups)), dim3(waves * 64), waves * groups * 1024, s, a);
+  };
+  if (int8_row_groups(a.M, a.N) == 2) go(gemm_int8_rows_kernel<2, 1>, 2, 1);
+  else go(gemm_int8_rows_kernel<1, 4>, 1, 4);
+  return hipGetLastError();
 }
 
 hipError_t launch_join(const Int8Args &a, void *C, int32_t out_dtype, hipStream_t s) {
@@ -229,15 +240,13 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   a.C = split ? workspace : C;
   a.out_dtype = split ? kInt8Sums : out_dtype;
   const int64_t tiles_m = (M + pl.bm - 1) / pl.bm, tiles_n = (N + pl.bn - 1) / pl.bn, blocks = tiles_m * tiles_n * a.splits;
-  const int threads = pl.bn == 16 ? rows_waves(K) * 64 : 512;
-  // the launch's thread count is 32 bits (tiles: 512 threads at most, and a round's pieces)
-  if ((blocks + 2 * kCUs) * threads > int64_t(UINT32_MAX)) return TSS_E_ARG;
+  // the launch's thread count is 32 bits (1024 threads at most, and a round's pieces)
+  if ((blocks + 2 * kCUs) * (pl.bn == 16 ? 1024 : 512) > int64_t(UINT32_MAX)) return TSS_E_ARG;
   a.tiles_m = int32_t(tiles_m);
   a.tiles_n = int32_t(tiles_n);
   hipError_t err;
   if (pl.bn == 16) {
-    hipLaunchKernelGGL(gemm_int8_rows_kernel, dim3(uint32_t(blocks)), dim3(threads), threads * 16, s, a);
-    err = hipGetLastError();
+    err = launch_rows(a, s);
   } else if (pl.bm == 256) {
     err = launch_rounds(a, blocks, s);
   } else if (pl.bm == 128) {

@@ -242,9 +242,12 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_rounds_kernel(Int8Args p
 
 // Few rows: B's bytes are the cost, and each is used by one wave only, so it
 // goes from memory straight into MFMA fragments.  A workgroup takes 16 rows
-// and 16 columns; its waves share K, block by block of 128, and their sums
-// are joined through LDS (whole numbers: any order).  A (read by every
-// workgroup) comes from L2.
+// and NC groups of 16 columns; its waves share K, block by block of 128, and
+// their sums are joined through LDS (whole numbers: any order).  A (read by
+// every workgroup) comes from L2; two column groups halve that.  U: blocks of K
+// whose loads a wave has in flight.  4 x 8192 x 8192, weights in no cache: 16.5
+// us, 4.1 TB/s of B (one group, U = 4: 18.8), 16 rows 19.2 (24.1); where two
+// groups leave CUs free, 16 x 4096 x 4096: 8.9 and with one 7.4.
 template <typename O>
 __device__ __forceinline__ void put_int8_row(const Int8Args &p, int row, int col, const float (&v)[4]) {
   O *to = static_cast<O *>(p.C) + int64_t(row) * p.N + col;
@@ -260,13 +263,14 @@ __device__ __forceinline__ void put_int8_row(const Int8Args &p, int row, int col
   }
 }
 
-static __global__ __launch_bounds__(1024) void gemm_int8_rows_kernel(Int8Args p) {
+template <int NC, int U>
+__global__ __launch_bounds__(1024) void gemm_int8_rows_kernel(Int8Args p) {
   extern __shared__ __attribute__((aligned(1024))) char smem[];
   const int lane = threadIdx.x & 63, nw = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int id = xcd_run(blockIdx.x, gridDim.x);
-  const int tm = id % p.tiles_m, row0 = tm * 16, n0 = id / p.tiles_m * 16;  // the rows of a column share its B
-  const int rows = min(16, p.M - row0), cols = min(16, p.N - n0), K = p.K, nk = (K + 127) / 128;
+  const int tm = id % p.tiles_m, row0 = tm * 16, n0 = id / p.tiles_m * 16 * NC;  // the rows of a column share its B
+  const int rows = min(16, p.M - row0), cols = min(16 * NC, p.N - n0), K = p.K, nk = (K + 127) / 128;
   auto rsrc = [](const void *base, uint32_t range) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, int(range), 0x00020000);
   };
@@ -274,35 +278,43 @@ static __global__ __launch_bounds__(1024) void gemm_int8_rows_kernel(Int8Args p)
   const auto rsB = rsrc(p.B + int64_t(n0) * K, uint32_t(cols) * uint32_t(K));
   const int fr = lane % 16, ch = lane / 16 * 16;
   const uint32_t a_off = fr < rows ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
-  const uint32_t b_off = fr < cols ? uint32_t(fr) * uint32_t(K) + uint32_t(ch) : kOOB;
+  uint32_t b_off[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) b_off[c] = c * 16 + fr < cols ? uint32_t(c * 16 + fr) * uint32_t(K) + uint32_t(ch) : kOOB;
   // a lane's 16 bytes at k (zeros from K on); `ch` is its place within 64
   auto load = [&](auto rs, uint32_t off, int k) __attribute__((always_inline)) -> i32x4 {
     const uint32_t o = k + ch < K && off != kOOB ? off + uint32_t(k) : kOOB;
     return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
   };
-  i32x4 acc = {0, 0, 0, 0};
-  for (int kb = wave; kb < nk; kb += nw * kRowsUnroll) {
-    Int8Fragment b[kRowsUnroll], a[kRowsUnroll];
+  i32x4 acc[NC];
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) {
+  for (int c = 0; c < NC; ++c) acc[c] = i32x4{0, 0, 0, 0};
+  for (int kb = wave; kb < nk; kb += nw * U) {
+    Int8Fragment b[U][NC], a[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       const int k = (kb + u * nw) * 128;
-      b[u] = {load(rsB, b_off, k), load(rsB, b_off, k + 64)};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) b[u][c] = {load(rsB, b_off[c], k), load(rsB, b_off[c], k + 64)};
       a[u] = {load(rsA, a_off, k), load(rsA, a_off, k + 64)};
     }
 #pragma unroll
-    for (int u = 0; u < kRowsUnroll; ++u) acc = mfma_int8(b[u], a[u], acc);
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) acc[c] = mfma_int8(b[u][c], a[u], acc[c]);
   }
-  i32x4 *red = reinterpret_cast<i32x4 *>(smem);
-  red[wave * 64 + lane] = acc;
+  i32x4 *red = reinterpret_cast<i32x4 *>(smem);  // [wave][column group][lane]
+#pragma unroll
+  for (int c = 0; c < NC; ++c) red[(wave * NC + c) * 64 + lane] = acc[c];
   __syncthreads();
-  if (wave != 0) return;
-  i32x4 s = red[lane];
+  if (wave >= NC) return;  // one wave joins one column group
+  i32x4 s = red[wave * 64 + lane];
   for (int w = 1; w < nw; ++w) {
-    const i32x4 v = red[w * 64 + lane];
+    const i32x4 v = red[(w * NC + wave) * 64 + lane];
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] += v[e];
   }
-  const int row = row0 + fr, col = n0 + lane / 16 * 4;
+  const int row = row0 + fr, col = n0 + wave * 16 + lane / 16 * 4;
   if (row >= p.M || col >= p.N) return;
   const float sa = p.sa[row];
   float v[4];

@@ -60,21 +60,32 @@ inline void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
   *n = int32_t((kb + per - 1) / per);
 }
 
-// A product of 8-bit integers: as an 8-bit floating-point one, but for its
-// ranges of K.  A step of a 64 x 128 tile takes 0.32 us; ranges cost a second
-// launch and 4 bytes of partial sums an element each, in us about 1.2 + s (0.3 +
-// M N / 430000).  128 x 4096 x 4096: 16.2, 13.6 and 15.1 us in 1, 2 and 4
-// ranges; 1024 x 1024 x 4096: 16.4, 17.8 and 20.4; 256 x 512 x 8192: 25.7, 18.2,
-// 14.4 and in 8 ranges 13.9.
+// Products of 8-bit integers.  Groups of 16 columns of a workgroup of the
+// kernel for few rows: two where that leaves no CU free (its measurements are
+// at the kernel).
+inline int int8_row_groups(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 31) / 32) >= 192 ? 2 : 1; }
+
+// By the time that each way takes, in ns.  The kernel for few rows: 3200, and
+// the longer of a workgroup's own reads and all of them, from L2 at 8.5 TB/s
+// (64 x 4096 x 4096: 14.8 us, 64 x 1024 x 8192 11.1, 64 x 8192 x 1024 9.0).
+// Tiles of 64 x 128: 5300 and 320 a step of K; ranges of K cost a second launch
+// and 4 bytes of partial sums an element each (128 x 4096 x 4096: 16.2, 13.6 and
+// 15.1 us in 1, 2 and 4 ranges; 1024 x 1024 x 4096: 16.4, 17.8 and 20.4; 256 x 512
+// x 8192: 25.7, 18.2, 14.4 and in 8 ranges 13.9).  Larger tiles as for 8-bit
+// floating point.
 inline ProductPlan plan_int8(int64_t M, int64_t N, int64_t K) {
-  ProductPlan p = plan_product(M, N, K, false);
-  p.sets = 1;
-  if (p.bm != 64) return p;
-  const int64_t kb = (K + 127) / 128, b = (M + 63) / 64 * ((N + 127) / 128);
-  auto ns = [&](int64_t s) { return 320 * ((kb + s - 1) / s) + (s > 1 ? 1200 + s * (300 + M * N / 430) : 0); };
-  p.splits = 1;
+  if (M <= 16) return {16, 16, 1};
+  auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
+  const int64_t b128 = blocks(128, 128);
+  if (b128 >= 160) return b128 <= kCUs ? ProductPlan{128, 128, 1} : ProductPlan{256, 256, 1};
+  const int64_t kb = (K + 127) / 128, b = blocks(64, 128);
+  auto tiles = [&](int64_t s) { return 5300 + 320 * ((kb + s - 1) / s) + (s > 1 ? 1200 + s * (300 + M * N / 430) : 0); };
+  ProductPlan p{64, 128, 1};
   for (int s = 2; s <= 8 && b * s <= kCUs; ++s)
-    if (ns(s) < ns(p.splits)) p.splits = s;
+    if (tiles(s) < tiles(p.splits)) p.splits = s;
+  const int64_t columns = 16 * int8_row_groups(M, N);
+  const int64_t own = 830 * K / 1024, all = blocks(16, columns) * (16 + columns) * K / 8500;
+  if (3200 + (own > all ? own : all) < tiles(p.splits)) return {16, 16, 1};
   return p;
 }
 

@@ -105,12 +105,30 @@ def _call(where: str, fn, tensors, *args):
         C.check(st, where)
 
 
-def _run(entry: str, *args):
+_ENTRIES = {}  # the compiled binding's functions that were called, by name
+
+
+def _entry(name: str):
+    f = _ENTRIES.get(name)
+    if f is None:
+        f = _ENTRIES[name] = getattr(C.bind(), name)
+    return f
+
+
+def _run(name: str, *args):
     """The entry point of this name on args and the current stream, through the
     compiled binding: tensors are given as they are, all on one GPU."""
-    st = getattr(C.bind(), entry)(*args)
+    st = _entry(name)(*args)
     if st != C.TSS_OK:
-        C.check(st, entry)
+        C.check(st, name)
+
+
+def _size(name: str, *args) -> int:
+    """What the entry point of this name, a workspace's size, gives."""
+    n = _entry(name)(*args)
+    if n < 0:
+        C.check(n, name)
+    return n
 
 
 def _blocks(n: int) -> int:
@@ -262,9 +280,7 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=Non
     dx = _out(dx, "dx", (rows, d), dy.dtype, dy.device)
     dweight = _out(dweight, "dweight", (d,), torch.float32, dy.device)
     dbias = None if dbias is False else _out(dbias, "dbias", (d,), torch.float32, dy.device)
-    need = C.lib().tss_layer_norm_backward_workspace_size(rows, d)
-    if need < 0:
-        C.check(int(need), "tss_layer_norm_backward_workspace_size")
+    need = _size("tss_layer_norm_backward_workspace_size", rows, d)
     workspace = _workspace(workspace, need, dy.device)
     _run("tss_layer_norm_backward", rows, d, _DT[dt], dy, h, weight, mean, rstd, dh, dx, dweight, dbias, workspace,
          workspace.nbytes)
@@ -357,10 +373,7 @@ def gemm_fp8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None, fp
 
 
 def gemm_int8_workspace_size(M: int, N: int, K: int) -> int:
-    n = C.lib().tss_gemm_int8_workspace_size(M, N, K)
-    if n < 0:
-        C.check(int(n), "tss_gemm_int8_workspace_size")
-    return int(n)
+    return _size("tss_gemm_int8_workspace_size", M, N, K)
 
 
 @_streamed
@@ -500,10 +513,7 @@ def _clip(grads, max_norm: float, out, norm, workspace):
     if grads and norm.get_device() != index:
         raise ValueError("every tensor must be on the same GPU")
     n = len(grads)
-    need = C.lib().tss_clip_grad_norm_workspace_size(n, sizes)
-    if need < 0:
-        C.check(int(need), "tss_clip_grad_norm_workspace_size")
-    workspace = _workspace(workspace, need, device)
+    workspace = _workspace(workspace, _size("tss_clip_grad_norm_workspace_size", n, sizes), device)
     _run("tss_clip_grad_norm", n, at, sizes, types, float(max_norm), to, norm, workspace, workspace.nbytes)
     return norm
 

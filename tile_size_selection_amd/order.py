@@ -10,9 +10,8 @@ from __future__ import annotations
 
 from typing import NamedTuple, Optional, Tuple
 
-from . import _capi as C
 from .api import _workspace, torch
-from .ops import _DT, _TORCH, _choice, _given, _name, _out, _run, _streamed
+from .ops import _DT, _TORCH, _choice, _given, _name, _out, _run, _size, _streamed
 
 _FLOATS = ("f16", "bf16", "f32")
 
@@ -29,13 +28,15 @@ class ExpertOrder(NamedTuple):
 
 def _order(order, tokens: Optional[int] = None) -> Tuple[int, int]:
     """(tokens, top) of an ExpertOrder, checked."""
-    if order.row.dim() != 2 or order.row.shape[1] < 1:
+    shape = order.row.shape
+    if len(shape) != 2 or shape[1] < 1:
         raise ValueError("order.row must be (tokens, top)")
-    _given(order.row, "order.row", tuple(order.row.shape), torch.int32)
-    if tokens is not None and order.row.shape[0] != tokens:
-        raise ValueError(f"the order is of {order.row.shape[0]} tokens, not of {tokens}")
-    _given(order.choice, "order.choice", (order.row.numel(),), torch.int32)
-    return tuple(order.row.shape)
+    n, top = shape
+    if tokens is not None and n != tokens:
+        raise ValueError(f"the order is of {n} tokens, not of {tokens}")
+    _given(order.row, "order.row", shape, torch.int32)
+    _given(order.choice, "order.choice", (n * top,), torch.int32)
+    return n, top
 
 
 @_streamed
@@ -49,9 +50,7 @@ def sort_by_expert(expert, experts: int, sizes=None, row=None, choice=None, work
         raise ValueError("expert must be (tokens, top) int32 or int64")
     tokens, top = expert.shape
     _given(expert, "expert", (tokens, top), expert.dtype)
-    need = C.lib().tss_sort_by_expert_workspace_size(tokens, top, experts)
-    if need < 0:
-        C.check(int(need), "tss_sort_by_expert")
+    need = _size("tss_sort_by_expert_workspace_size", tokens, top, experts)
     sizes = _out(sizes, "sizes", (experts,), torch.int32, expert.device)
     row = _out(row, "row", (tokens, top), torch.int32, expert.device)
     choice = _out(choice, "choice", (tokens * top,), torch.int32, expert.device)
