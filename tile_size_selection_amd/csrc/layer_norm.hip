@@ -32,134 +32,158 @@ struct NormArgs {
 
 // A row is held by L neighbouring lanes, or (L == 64) by wpr waves, one row
 // per workgroup where wpr > 1; lane t of it holds columns (c * lanes + t) * 8
-// .. + 7 for c < CH.
+// .. + 7 for c < CH.  Rows are taken a launch's teams apart: weight and bias
+// stay in registers, and the next row's loads are in flight while a row is
+// reduced and written.
 template <typename T, bool INT8, int CH, int L>
 __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
-  __shared__ float red[4][kMaxThreads / 64];
+  __shared__ float red[2][4][kMaxThreads / 64];
   const int wave = threadIdx.x >> 6, wpr = L == 64 ? p.wpr : 1;
   const int lanes = L * wpr;
   const int t = L < 64 ? threadIdx.x % L : wpr == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int row = xcd_run(blockIdx.x, gridDim.x) * (blockDim.x / lanes) + threadIdx.x / lanes;
-  if (row >= p.rows) return;  // wpr > 1: one row, the whole workgroup
+  const int teams = blockDim.x / lanes;
+  const int64_t stride = int64_t(gridDim.x) * teams;
   const int d = p.d;
-  const int64_t base = int64_t(row) * d;
   const T *x = static_cast<const T *>(p.x), *residual = static_cast<const T *>(p.residual);
   const T *weight = static_cast<const T *>(p.weight), *bias = static_cast<const T *>(p.bias);
   auto col_of = [&](int c) __attribute__((always_inline)) { return (c * lanes + t) * 8; };
-  // two sums over the row; each use its own slots, `slot` and the next
+  int set = 0;
+  // two sums over the row; each use its own slots, `slot` and the next, and each row the other set of
+  // them: a wave writes the next row's while others may still read this row's
   auto row_sums = [&](float &u, float &v, int slot) __attribute__((always_inline)) {
     u = sum_lanes<L>(u);
     v = sum_lanes<L>(v);
     if (L < 64 || wpr == 1) return;
     if ((threadIdx.x & 63) == 0) {
-      red[slot][wave] = u;
-      red[slot + 1][wave] = v;
+      red[set][slot][wave] = u;
+      red[set][slot + 1][wave] = v;
     }
     __syncthreads();
     u = v = 0;
     for (int i = 0; i < wpr; ++i) {
-      u += red[slot][i];
-      v += red[slot + 1][i];
+      u += red[set][slot][i];
+      v += red[set][slot + 1][i];
     }
   };
 
   Raw8<T> xr[CH], rr[CH], wr[CH], br[CH];
+  auto load_row = [&](int64_t row) __attribute__((always_inline)) {
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int col = col_of(c);
-    const bool in = col < d;
-    xr[c] = in ? load8(x + base + col) : zero8<T>();
-    rr[c] = in && residual ? load8(residual + base + col) : zero8<T>();
-    if constexpr (CH < 4) {
-      wr[c] = in ? load8(weight + col) : zero8<T>();
-      br[c] = in && bias ? load8(bias + col) : zero8<T>();
+    for (int c = 0; c < CH; ++c) {
+      const int col = col_of(c);
+      const bool in = col < d && row < p.rows;
+      xr[c] = in ? load8(x + row * d + col) : zero8<T>();
+      rr[c] = in && residual ? load8(residual + row * d + col) : zero8<T>();
     }
-  }
-  float h[CH][8], sum = 0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    widen8(xr[c], h[c]);
-    if (residual) {
-      float r[8];
-      widen8(rr[c], r);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) h[c][i] += r[i];
-    }
-    if (p.h && col_of(c) < d) store8(static_cast<T *>(p.h) + base + col_of(c), h[c]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum += h[c][i];
-  }
-  const float inv_d = 1.0f / float(d);
-  float none = 0;
-  row_sums(sum, none, 0);
-  const float mean0 = sum * inv_d;
-  float rest = 0, sq = 0;
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
+  };
+  // The widest rows: there are not enough registers to hold weight and bias, nor the next row.
+  constexpr bool kHeld = CH < 4;
+  int64_t row = int64_t(blockIdx.x) * teams + threadIdx.x / lanes;
+  if constexpr (kHeld) load_row(row);
+  auto load_weight = [&](int c) __attribute__((always_inline)) {
     const bool in = col_of(c) < d;
+    wr[c] = in ? load8(weight + col_of(c)) : zero8<T>();
+    br[c] = in && bias ? load8(bias + col_of(c)) : zero8<T>();
+  };
+  if constexpr (kHeld)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      h[c][i] = in ? h[c][i] - mean0 : 0.0f;
-      rest += h[c][i];
-      sq += h[c][i] * h[c][i];
-    }
-  }
-  row_sums(rest, sq, 2);
-  const float off = rest * inv_d;  // the mean of h - mean0: what mean0 lacks
-  const float var = fmaxf(sq * inv_d - off * off, 0.0f);
-  // a NaN in the row has to come through the max above
-  const float r = var == var && off == off ? 1.0f / __builtin_sqrtf(var + p.eps) : off;
-  if (t == 0) {
-    if (p.mean) p.mean[row] = mean0 + off;
-    if (p.rstd) p.rstd[row] = r;
-  }
-  float amax = 0;
+    for (int c = 0; c < CH; ++c) load_weight(c);
+  const float inv_d = 1.0f / float(d);
+  for (; row < p.rows; row += stride, set ^= 1) {
+    const int64_t base = row * d;
+    float h[CH][8], sum = 0, none = 0;
+    if constexpr (!kHeld) load_row(row);
 #pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    float w[8], b[8];
-    if constexpr (CH == 4) {  // there are not enough registers to hold them from the start
-      wr[c] = col_of(c) < d ? load8(weight + col_of(c)) : zero8<T>();
-      br[c] = col_of(c) < d && bias ? load8(bias + col_of(c)) : zero8<T>();
-    }
-    widen8(wr[c], w);
-    widen8(br[c], b);
+    for (int c = 0; c < CH; ++c) {
+      widen8(xr[c], h[c]);
+      if (residual) {
+        float r[8];
+        widen8(rr[c], r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      h[c][i] = (h[c][i] - off) * r * w[i] + b[i];
-      if constexpr (INT8) amax = max_abs(amax, h[c][i]);  // columns past the row: w = b = 0
+        for (int i = 0; i < 8; ++i) h[c][i] += r[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += h[c][i];
     }
-    if constexpr (!INT8)
-      if (col_of(c) < d) store8(static_cast<T *>(p.y) + base + col_of(c), h[c]);
-  }
-  if constexpr (INT8) {
-    amax = max_lanes<L>(amax);
-    if (L == 64 && wpr > 1) {
-      if ((threadIdx.x & 63) == 0) red[0][wave] = amax;  // read before the second sums' barrier
-      __syncthreads();
-      for (int i = 0; i < wpr; ++i) amax = __builtin_elementwise_maximum(amax, red[0][i]);
-    }
-    const BlockScale<I8> s(amax);
-    if (t == 0) p.scale[row] = s.scale;
+    if constexpr (kHeld) load_row(row + stride);
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      if (col_of(c) < d)
-        *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(p.y) + base + col_of(c)) = pack8(h[c], s);
+      if (p.h && col_of(c) < d) store8(static_cast<T *>(p.h) + base + col_of(c), h[c]);
+    row_sums(sum, none, 0);
+    const float mean0 = sum * inv_d;
+    float rest = 0, sq = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      const bool in = col_of(c) < d;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[c][i] = in ? h[c][i] - mean0 : 0.0f;
+        rest += h[c][i];
+        sq += h[c][i] * h[c][i];
+      }
+    }
+    row_sums(rest, sq, 2);
+    const float off = rest * inv_d;  // the mean of h - mean0: what mean0 lacks
+    const float var = fmaxf(sq * inv_d - off * off, 0.0f);
+    // a NaN in the row has to come through the max above
+    const float r = var == var && off == off ? 1.0f / __builtin_sqrtf(var + p.eps) : off;
+    if (t == 0) {
+      if (p.mean) p.mean[row] = mean0 + off;
+      if (p.rstd) p.rstd[row] = r;
+    }
+    float amax = 0;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float w[8], b[8];
+      if constexpr (!kHeld) load_weight(c);
+      widen8(wr[c], w);
+      widen8(br[c], b);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        h[c][i] = (h[c][i] - off) * r * w[i] + b[i];
+        if constexpr (INT8) amax = max_abs(amax, h[c][i]);  // columns past the row: w = b = 0
+      }
+      if constexpr (!INT8)
+        if (col_of(c) < d) store8(static_cast<T *>(p.y) + base + col_of(c), h[c]);
+    }
+    if constexpr (INT8) {
+      amax = max_lanes<L>(amax);
+      if (L == 64 && wpr > 1) {
+        if ((threadIdx.x & 63) == 0) red[set][0][wave] = amax;  // read before the second sums' barrier
+        __syncthreads();
+        for (int i = 0; i < wpr; ++i) amax = __builtin_elementwise_maximum(amax, red[set][0][i]);
+      }
+      const BlockScale<I8> s(amax);
+      if (t == 0) p.scale[row] = s.scale;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        if (col_of(c) < d)
+          *reinterpret_cast<u32x2 *>(static_cast<uint8_t *>(p.y) + base + col_of(c)) = pack8(h[c], s);
+    }
   }
 }
 
 template <typename T, bool INT8>
 int32_t launch_norm(const NormArgs &a, hipStream_t s) {
-  // Two chunks a thread where they keep a row in one wave, without barriers
-  // (60000 x 520, bf16: 30.8 us, with two waves 48), else one (16384 x 4096,
-  // bf16 with residual: 114 us, two chunks 121, four 126).  Few rows: one, a
-  // row's latency is all that counts.
-  const Team f = team_of(a.d, a.rows >= 1024 && a.d > 512 && a.d <= 1024 ? 2 : 1);
+  // Few rows: one chunk a thread, a row's latency is all that counts.  Else two.
+  const Team f = team_of(a.d, a.rows < 1024 || a.d <= 512 ? 1 : 2);
   const int block = f.waves == 1 ? 256 : f.waves * 64, rpb = f.waves == 1 ? 256 / f.lanes : 1;
-  const int64_t blocks = (int64_t(a.rows) + rpb - 1) / rpb;
+  int64_t blocks = (int64_t(a.rows) + rpb - 1) / rpb;
+  // Rows of two chunks a thread: as many workgroups as the CUs hold at once, four waves a SIMD of which a
+  // workgroup may put one more on the first, and each takes rows in turn (16384 x 4096, bf16: 50.7 us, one
+  // row a workgroup 62; 60000 x 520 31 and 44; where some of them wait, 5 waves three times a CU, 7031 x
+  // 5120: 43, twice 34).  One chunk: 200000 x 256, bf16 with residual, takes 72 us with a row a team, 76 in turn.
+  if (f.chunks > 1) {
+    const int waves = block / 64, per_cu = waves < 4 ? 16 / waves : 4 / ((waves + 3) / 4);
+    const int64_t most = 256 * (per_cu < 1 ? 1 : per_cu);
+    blocks = blocks < most ? blocks : most;
+  }
   if (blocks * block > int64_t(UINT32_MAX)) return TSS_E_ARG;  // the launch's thread count is 32 bits
   NormArgs p = a;
   p.wpr = f.waves;
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(block), 0, s, p); };
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(blocks)), dim3(block), 0, s, p);
+  };
   if (f.lanes == 8) go(layer_norm_kernel<T, INT8, 1, 8>);
   else if (f.lanes == 16) go(layer_norm_kernel<T, INT8, 1, 16>);
   else if (f.lanes == 32) go(layer_norm_kernel<T, INT8, 1, 32>);

@@ -71,14 +71,19 @@ inline int int8_row_groups(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 
 // Tiles of 64 x 128: 5300 and 320 a step of K; ranges of K cost a second launch
 // and 4 bytes of partial sums an element each (128 x 4096 x 4096: 16.2, 13.6 and
 // 15.1 us in 1, 2 and 4 ranges; 1024 x 1024 x 4096: 16.4, 17.8 and 20.4; 256 x 512
-// x 8192: 25.7, 18.2, 14.4 and in 8 ranges 13.9).  Larger tiles as for 8-bit
-// floating point.
+// x 8192: 25.7, 18.2, 14.4 and in 8 ranges 13.9).  More of them than CUs: one
+// round of 128 x 128 (634 x 3778 x 5088: 30.2 us, in 300 of 64 x 128 39.7), else
+// 256 x 256 (5139 x 2722 x 7440: 115, 164 and 200 us; 836 x 5581 x 240: 13.6, 16.4
+// and 15.5).
 inline ProductPlan plan_int8(int64_t M, int64_t N, int64_t K) {
   if (M <= 16) return {16, 16, 1};
   auto blocks = [&](int64_t bm, int64_t bn) { return (M + bm - 1) / bm * ((N + bn - 1) / bn); };
-  const int64_t b128 = blocks(128, 128);
-  if (b128 >= 160) return b128 <= kCUs ? ProductPlan{128, 128, 1} : ProductPlan{256, 256, 1};
-  const int64_t kb = (K + 127) / 128, b = blocks(64, 128);
+  const int64_t kb = (K + 127) / 128, b = blocks(64, 128), b128 = blocks(128, 128), b256 = blocks(256, 256);
+  if (b > kCUs) {
+    // two rounds of 128 x 128 where 256 x 256 would be one that is not cut (135 of these: 43.4 us, 493 of those 37.5)
+    const bool two = b128 <= 2 * kCUs && b256 > kCUs / 2 && b256 < kCUs;
+    return b128 <= kCUs || two ? ProductPlan{128, 128, 1} : ProductPlan{256, 256, 1};
+  }
   auto tiles = [&](int64_t s) { return 5300 + 320 * ((kb + s - 1) / s) + (s > 1 ? 1200 + s * (300 + M * N / 430) : 0); };
   ProductPlan p{64, 128, 1};
   for (int s = 2; s <= 8 && b * s <= kCUs; ++s)
