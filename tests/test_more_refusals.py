@@ -25,7 +25,7 @@ NORM = dict(rows=4, d=64, dtype=BF16, x=P, residual=P, weight=P, bias=P, eps=1e-
 
 
 @pytest.mark.parametrize("change,status", [
-    (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(rows=1 << 31), ARG), (dict(rows=(1 << 31) - 1, d=4096), ARG),
+    (dict(rows=-1), ARG), (dict(d=0), ARG), (dict(rows=1 << 31), ARG), (dict(rows=(1 << 31) - 1, d=512), ARG),
     (dict(d=12), ALIGN), (dict(d=32776), UNSUP), (dict(dtype=9), DTYPE), (dict(dtype=I8), DTYPE),
     (dict(out_dtype=F16), DTYPE), (dict(out_dtype=E4M3), DTYPE), (dict(out_dtype=I8), ARG), (dict(x=None), ARG),
     (dict(weight=None), ARG), (dict(y=None), ARG), (dict(eps=-1.0), ARG), (dict(eps=float("nan")), ARG),
@@ -160,8 +160,8 @@ Q = P + (1 << 16)
     (dict(at=[P], sizes=[8], types=[E4M3]), DTYPE), (dict(at=[None], sizes=[8], types=[F32]), ARG),
     (dict(at=[P], sizes=[8], types=[F32], out=[None]), ARG), (dict(at=[P + 2], sizes=[8], types=[F32]), ALIGN),
     (dict(at=[P + 1], sizes=[8], types=[BF16]), ALIGN), (dict(at=[P], sizes=[8], types=[F32], norm=None), ARG),
-    (dict(at=[P], sizes=[8], types=[F32], norm=P + 2), ALIGN), (dict(at=[P], sizes=[8], types=[F32], ws=None), ARG),
-    (dict(at=[P], sizes=[8], types=[F32], ws=P + 4), ALIGN), (dict(at=[P], sizes=[8], types=[F32], ws_bytes=7), ARG),
+    (dict(at=[P], sizes=[8], types=[F32], norm=P + 2), ALIGN), (dict(at=[P], sizes=[1 << 17], types=[F32], ws=None), ARG),
+    (dict(at=[P], sizes=[8], types=[F32], ws=P + 4), ALIGN), (dict(at=[P], sizes=[1 << 17], types=[F32], ws_bytes=511), ARG),
     (dict(at=[P], sizes=[8], types=[F32], out=[P], max_norm=-1.0), ARG),
     (dict(at=[P], sizes=[8], types=[F32], out=[P], max_norm=float("nan")), ARG),
     # written twice, in place and not; an output that overlaps an input; one that begins inside another
@@ -177,7 +177,10 @@ def test_clip_refuses(call, status):
 
 def test_clip_workspace():
     size = lambda *n: C.lib().tss_clip_grad_norm_workspace_size(len(n), (C.i64 * len(n))(*n))  # noqa: E731
-    assert size() == 0 and size(0) == 0 and size(1) == 8 and size(1, 0, 1) == 16 and size(-1) == ARG
+    assert size() == 0 and size(0) == 0 and size(-1) == ARG
+    # up to 20 units of 2048 elements one workgroup needs none; else 8 bytes a workgroup, 2048 of them at most a table
+    assert size(1) == 0 and size(2048 * 20) == 0 and size(2048 * 20 + 1) == 21 * 8 and size(2048 * 12, 1, 0, 2048 * 8) == 21 * 8
+    assert size(*[1] * 128) == 128 * 8 and size(*[1] * 129) == 129 * 8 and size(1 << 26) == 2048 * 8
 
 
 def z(*shape, t=torch.bfloat16):

@@ -513,8 +513,11 @@ def _clip(grads, max_norm: float, out, norm, workspace):
     if grads and norm.get_device() != index:
         raise ValueError("every tensor must be on the same GPU")
     n = len(grads)
-    workspace = _workspace(workspace, _size("tss_clip_grad_norm_workspace_size", n, sizes), device)
-    _run("tss_clip_grad_norm", n, at, sizes, types, float(max_norm), to, norm, workspace, workspace.nbytes)
+    need = _size("tss_clip_grad_norm_workspace_size", n, sizes)
+    if need:
+        workspace = _workspace(workspace, need, device)
+    _run("tss_clip_grad_norm", n, at, sizes, types, float(max_norm), to, norm, workspace,
+         0 if workspace is None else workspace.nbytes)
     return norm
 
 
