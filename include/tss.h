@@ -641,14 +641,13 @@ int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, 
 /*
  * h = x + residual; y = (h - mean(h)) / sqrt(mean((h - mean(h))^2) + eps) *
  * weight + bias, row by row.  residual and bias may be NULL.  y: out_dtype
- * dtype, or TSS_I8 with scale[rows] (NULL otherwise): scale = max(largest |y|
- * of the row, 1e-30) / 127, the value y / scale rounded to nearest even; of a
- * row with a NaN or an infinity scale is not finite.  residual_out (may be
- * NULL): h rounded to dtype; it may be residual or x itself.  y may be x when
- * out_dtype is dtype.  mean, rstd (may be NULL): rows fp32, the mean and
- * 1 / sqrt(...).  weight, bias: d elements of dtype.  d <= 32768; rows * d
- * below about 2^35 and rows < 2^31 (a launch's threads).  x, residual, weight,
- * bias, y and residual_out 16-byte aligned.  rows == 0: nothing to do.
+ * dtype, or TSS_I8 with scale[rows] (NULL otherwise) as tss_quantize_int8
+ * makes them of y.  residual_out (may be NULL): h rounded to dtype; it may be
+ * residual or x itself.  y may be x when out_dtype is dtype.  mean, rstd (may
+ * be NULL): rows fp32, the mean and 1 / sqrt(...).  weight, bias: d elements of
+ * dtype.  d <= 32768; rows < 2^31, and where d <= 512 the rows times 8, 16, 32
+ * or 64 lanes of 8 columns (the fewest that hold one) below 2^32.  x, residual,
+ * weight, bias, y and residual_out 16-byte aligned.  rows == 0: nothing to do.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_UNSUPPORTED (d),
  * TSS_E_HIP.
  */
@@ -675,10 +674,13 @@ int64_t tss_layer_norm_backward_workspace_size(int64_t rows, int64_t d);
 /*
  * q (rows x d, 8-bit integers -127 .. 127) and scale[rows] from x, or with
  * gated from silu(gate) * up in fp32 where x has rows of 2 d elements, gate
- * then up: scale = max(largest |value| of the row, 1e-30) / 127, q = value /
- * scale rounded to nearest even, as fp32 division rounds.  A row with a NaN or
- * an infinity has that as its scale; its finite values are 0.  d <= 32768 (of q);
- * x and q 16-byte aligned, scale 4-byte.  rows == 0: nothing to do.
+ * then up: scale = max(largest |value| of the row, 1e-30) / 127 in fp32, q = the
+ * value times 127 / that magnitude, rounded to nearest even (the exact quotient's
+ * rounding for 16-bit values, within 2^-17 of a border k + 1/2 either one for
+ * fp32).  A row with a NaN or an infinity has that as its scale; all its values
+ * are 0.  d <= 32768 (of q); rows times the lanes that hold one (8 columns each)
+ * below about 2^32; x and q 16-byte aligned, scale 4-byte.  rows == 0: nothing
+ * to do.
  * Errors: as tss_layer_norm.
  */
 int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, void *q, float *scale,
@@ -697,7 +699,8 @@ int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x,
  * A norm that is NaN makes every output NaN; an infinite one multiplies by 0.
  * max_norm >= 0 (not read when out is NULL).  At most 2^40 elements in all.
  * workspace: device memory of at least tss_clip_grad_norm_workspace_size(n,
- * sizes) bytes, 8-byte aligned, scratch.  n == 0: the norm is 0.
+ * sizes) bytes, 8-byte aligned, scratch (may be NULL when that is 0).  n == 0:
+ * the norm is 0.
  * Errors: TSS_E_ARG (also overlapping outputs), TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
 int32_t tss_clip_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,

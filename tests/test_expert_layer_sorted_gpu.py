@@ -118,3 +118,9 @@ def test_a_step_in_a_graph():
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+def test_the_command_runs(monkeypatch, capsys):
+    monkeypatch.setattr("sys.argv", ["expert_layer", "--tokens", "64", "--width", "256", "--hidden", "128", "--experts", "4"])
+    X.main()
+    assert "shared expert" in capsys.readouterr().out

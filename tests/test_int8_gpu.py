@@ -153,6 +153,7 @@ def test_quantisation_on_rounding_borders():
 def test_rows_that_are_not_finite_stay_by_themselves():
     x = U.normal(U.gen(8), 6, 1032).float()
     x[1, 5], x[2, 6], x[3, 1031] = float("nan"), float("inf"), -float("inf")
+    x[1, 9] = torch.tensor(0x7fc12345, dtype=torch.int32).view(torch.float32)  # a NaN with a payload
     q, s = tss.quantize_int8(x.to(CUDA))
     assert s[1].isnan() and s[2].isinf() and s[3].isinf() and s[[0, 4, 5]].isfinite().all()
     assert (q[1:4] == 0).all()

@@ -132,11 +132,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
   __syncthreads();
   // the bins are kept for the second time, if the workgroup's fit
   const bool held = !MANY || p.per_group <= kHeld;
-  uint16_t *kept_bins = held_bins - group * p.per_group;
+  const int group_from = group * p.per_group;
 #pragma unroll 4
   for (int i = from + lane; i < end; i += 64) {
     const int b = bin_of<I>(p, i);
-    if (held) kept_bins[i] = uint16_t(b);
+    if (held) held_bins[i - group_from] = uint16_t(b);
     atomicAdd(&mine[b], 1u);
   }
   if (shared) {
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortArgs p) {
   for (int i0 = from; i0 < end; i0 += 64) {
     const int i = i0 + lane;
     const bool in = i < end;
-    const int b = !in ? bins : held ? kept_bins[i] : bin_of<I>(p, i);
+    const int b = !in ? bins : held ? held_bins[i - group_from] : bin_of<I>(p, i);
     uint64_t same = __ballot(in);  // the lanes with this lane's bin
 #pragma unroll 1
     for (int bit = 1; bit < bins; bit *= 2) {

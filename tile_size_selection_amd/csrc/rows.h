@@ -175,8 +175,8 @@ struct BlockScale {
   explicit __device__ __forceinline__ BlockScale(float amax) {
     scale = __builtin_elementwise_maximum(amax, kSmallestAmax) / kLargest<Q>;
     const float r = __builtin_amdgcn_rcpf(scale);
-    // an infinite scale: finite values are 0, infinite ones NaN
-    const bool inf = scale == __builtin_inff();
+    // an infinite scale: finite values are 0, infinite ones NaN; integers, which have no NaN: also of a NaN scale
+    const bool inf = __is_same(Q, I8) ? !(scale < __builtin_inff()) : scale == __builtin_inff();
     inv = inf ? 0.0f : __builtin_fmaf(__builtin_fmaf(-scale, r, 1.0f), r, r);
     back = inf ? 0.0f : -scale;
     low = inf ? 0.0f : __builtin_fmaf(-kLargest<Q>, scale, __builtin_elementwise_maximum(amax, kSmallestAmax)) / -kLargest<Q>;
@@ -196,10 +196,13 @@ __device__ __forceinline__ u32x2 round8(const float (&f)[8]) {
   for (int i = 0; i < 2; ++i) {
     int w = 0;
     if constexpr (__is_same(Q, I8)) {
-      // 1.5 * 2^23 added: the sum's last byte is the rounded quotient in two's complement; 0 of infinities and NaN
+      // 1.5 * 2^23 added: the sum's last byte is the rounded quotient in two's complement; 0 of a NaN
       uint32_t b[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) b[j] = __builtin_bit_cast(uint32_t, f[4 * i + j] + 0x1.8p23f);
+      for (int j = 0; j < 4; ++j) {
+        const float q = f[4 * i + j];
+        b[j] = __builtin_bit_cast(uint32_t, (q == q ? q : 0.0f) + 0x1.8p23f);
+      }
       const uint32_t lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(b[3], b[2], 0x04000c0cu);
       w = int(lo | hi);
     } else if constexpr (__is_same(Q, E4M3)) {

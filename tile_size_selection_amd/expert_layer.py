@@ -283,11 +283,11 @@ def main():
 
     out8, _ = forward_fp8_sorted(x, residual, w8, expert, weight)
     got, _, kept = forward_sorted(x, residual, norm, w1, w2, expert, weight)
-    g = backward_sorted(dout, dh, norm, w1, w2, weight, kept)
+    grad = backward_sorted(dout, dh, norm, w1, w2, weight, kept)
     print(f"rows sorted, gathered and joined by the library: 8-bit forward {off(out8, out):.2e}, "
           f"{_timed(lambda: forward_fp8_sorted(x, residual, w8, expert, weight)):.0f} us; bf16 forward {off(got, out):.2e}, "
           f"{_timed(lambda: forward_sorted(x, residual, norm, w1, w2, expert, weight)):.0f} us; backward "
-          + ", ".join(f"{n} {off(b, w):.2e}" for n, b, w in zip(("dx", "dnorm", "dW1", "dW2"), (g.x, g.norm, g.w1, g.w2), grads))
+          + ", ".join(f"{n} {off(b, w):.2e}" for n, b, w in zip(("dx", "dnorm", "dW1", "dW2"), (grad.x, grad.norm, grad.w1, grad.w2), grads))
           + f", {_timed(lambda: backward_sorted(dout, dh, norm, w1, w2, weight, kept)):.0f} us; a step with clipping "
           f"{_timed(lambda: train_step(x, residual, norm, w1, w2, expert, weight, dout, dh, 1.0)):.0f} us")
     bias = (0.2 * normal(a.width)).to(bf16)
