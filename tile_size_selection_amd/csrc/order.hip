@@ -258,9 +258,10 @@ struct GatherArgs {
   float *scale_out;
   int tokens, top, pieces;  // pieces of a row
   int blocks_scale;         // column blocks of the scales
-  uint32_t row_groups;      // workgroups of the rows; those of the scales follow
+  uint32_t scale_groups;    // workgroups of the scales; those of the rows follow
 };
 
+constexpr int kScalesTogether = 16;  // 5186 x 6 x 6832 bytes, 54 blocks: 60 us, a thread for all blocks of a row 77
 constexpr int kPlacesTogether = 8;  // places read before the first is written (one by one: 129 us, 126 with 8 a token)
 
 // STREAMED: a template argument, because stores of both kinds behind a test are made one of the plain kind.
@@ -268,8 +269,8 @@ template <int BYTES, bool STREAMED>
 __global__ __launch_bounds__(kRowThreads) void gather_rows_kernel(GatherArgs p) {
   using P = typename Piece<BYTES>::type;
   const int n = p.tokens * p.top;
-  if (blockIdx.x < p.row_groups) {
-    const uint32_t id = blockIdx.x * kRowThreads + threadIdx.x;
+  if (blockIdx.x >= p.scale_groups) {
+    const uint32_t id = (blockIdx.x - p.scale_groups) * kRowThreads + threadIdx.x;
     const int t = int(id / uint32_t(p.pieces)), c = int(id - uint32_t(t) * uint32_t(p.pieces));
     if (t >= p.tokens) return;
     const P v = static_cast<const P *>(p.x)[int64_t(t) * p.pieces + c];
@@ -288,15 +289,20 @@ __global__ __launch_bounds__(kRowThreads) void gather_rows_kernel(GatherArgs p) 
       }
     }
   } else {
-    // the scales, row by row of the output: one thread a row, its column blocks one after the other
-    const int r = int((blockIdx.x - p.row_groups) * kRowThreads + threadIdx.x);
+    // the scales: a thread takes a row of the output and kScalesTogether of its column blocks
+    const uint32_t across = uint32_t(p.blocks_scale + kScalesTogether - 1) / kScalesTogether;
+    const int r = int(blockIdx.x / across * kRowThreads + threadIdx.x), b0 = int(blockIdx.x % across) * kScalesTogether;
     if (r >= n) return;
     const int i = p.choice[r];
     const bool in = i >= 0 && i < n;
     const int t = in ? i / p.top : 0;
-#pragma unroll 8
-    for (int b = 0; b < p.blocks_scale; ++b)
-      p.scale_out[int64_t(b) * n + r] = in ? p.scale[int64_t(b) * p.tokens + t] : 0.0f;
+    float v[kScalesTogether];
+#pragma unroll
+    for (int u = 0; u < kScalesTogether; ++u)
+      v[u] = in && b0 + u < p.blocks_scale ? p.scale[int64_t(b0 + u) * p.tokens + t] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < kScalesTogether; ++u)
+      if (b0 + u < p.blocks_scale) p.scale_out[int64_t(b0 + u) * n + r] = v[u];
   }
 }
 
@@ -513,10 +519,11 @@ int32_t tss_gather_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, c
   if (misaligned(x) || misaligned(rows)) return TSS_E_ALIGN;
   const bool wide = d * size % 16 == 0;
   const int64_t pieces = d * size / (wide ? 16 : 8), n = tokens * top;
-  const int64_t groups = (tokens * pieces + kRowThreads - 1) / kRowThreads;
-  const int64_t all = groups + (scale_blocks ? (n + kRowThreads - 1) / kRowThreads : 0);
-  if (tokens * pieces > kMaxThreadsOfLaunch - kRowThreads || all * kRowThreads > kMaxThreadsOfLaunch) return TSS_E_ARG;
-  const GatherArgs a{x, rows, row, choice, scale, scale_out, int(tokens), int(top), int(pieces), int(scale_blocks), uint32_t(groups)};
+  const int64_t scale_groups = (n + kRowThreads - 1) / kRowThreads * ((scale_blocks + kScalesTogether - 1) / kScalesTogether);
+  const int64_t all = scale_groups + (tokens * pieces + kRowThreads - 1) / kRowThreads;
+  if (all > (kMaxThreadsOfLaunch - kRowThreads) / kRowThreads) return TSS_E_ARG;
+  const GatherArgs a{x, rows, row, choice, scale, scale_out, int(tokens), int(top), int(pieces), int(scale_blocks),
+                     uint32_t(scale_groups)};
   hipStream_t s = static_cast<hipStream_t>(stream);
   const bool streamed = n * d * size >= kStreamed;
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(uint32_t(all)), dim3(kRowThreads), 0, s, a); };
