@@ -98,6 +98,33 @@ def test_norm_to_8_bit_integers(shape, dtype):
     assert (got.y.abs().amax(1) == 127).all()
 
 
+# rows of several turns of a launch: one wave a row, two, five, nine, and four chunks a thread
+TURNS = [(9000, 520), (9001, 1032), (5003, 4104), (4001, 8200), (1103, 16392), (40000, 128)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", TURNS)
+def test_rows_taken_in_turn(shape, dtype):
+    g = torch.Generator(device=CUDA)
+    g.manual_seed(21)
+    x, r = ((torch.randn(*shape, generator=g, device=CUDA) + 0.5).to(U.TYPES[dtype]) for _ in range(2))
+    w, b = (dev(t) for t in params(shape[1], dtype))
+    half, low = U.half_step(dtype)
+    for residual in (None, r):
+        y, h, mean, rstd = definition(x, residual, w, b)
+        known = inner(y, h, rstd, w, b)
+        got = tss.layer_norm(x, w, b, residual, eps=EPS, stats=True)
+        assert ((got.y.double() - y).abs() <= known + (y.abs() + known) * half + low).all()
+        assert ((got.rstd.double() - rstd).abs() <= rstd * REL * 2).all()
+        if residual is not None:
+            assert ((got.h.double() - h).abs() <= h.abs() * (half + 2.0 ** -23) + low).all()
+        q = tss.layer_norm(x, w, b, residual, eps=EPS, out_dtype="i8")
+        s = q.scale.double()[:, None]
+        assert ((q.y.double() * s - y).abs() <= s * 0.5 * (1 + 2.0 ** -15) + known + y.abs() * 2.0 ** -23).all()
+        over = x.clone()
+        assert torch.equal(tss.layer_norm(over, w, b, residual, eps=EPS, out=over).y, got.y)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_a_mean_far_from_zero_costs_no_digits(dtype):
     """Rows of mean 1000 and spread 1 (fp32: 2^-10): what is left is what the elements themselves hold."""

@@ -239,3 +239,44 @@ def test_a_captured_run_follows_its_inputs():
         torch.cuda.synchronize()
         for a, b in zip(held, want):
             assert torch.equal(a, b)
+
+
+def test_two_streams_at_once_and_given_workspaces():
+    """Sorts on two streams overlap, each with its own workspace; a short one is refused."""
+    experts = [choices(20000, 8, 128, 40 + i) for i in range(2)]
+    dev = [e.to(CUDA) for e in experts]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [torch.empty(1 << 20, dtype=torch.uint8, device=CUDA) for _ in range(2)]
+    orders = []
+    for turn in range(3):
+        for i in range(2):
+            streams[i].wait_stream(torch.cuda.current_stream())
+            orders.append((i, tss.sort_by_expert(dev[i], 128, workspace=spaces[i] if turn else None, stream=streams[i])))
+    torch.cuda.synchronize()
+    want = [defined(e, 128) for e in experts]
+    for i, o in orders:
+        assert o.sizes.tolist() == want[i][0] and torch.equal(o.row.cpu(), want[i][1]) and torch.equal(o.choice.cpu(), want[i][2])
+    with pytest.raises(ValueError):
+        tss.sort_by_expert(dev[0], 128, workspace=torch.empty(64, dtype=torch.uint8, device=CUDA))
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^32 bytes and 2^31 elements of rows: the last token's go where the first's do."""
+    tokens, top, d = 70001, 4, 8192
+    expert = choices(tokens, top, 16, 50)
+    order = tss.sort_by_expert(expert.to(CUDA), 16)
+    x = torch.zeros(tokens, d, dtype=torch.float16, device=CUDA)
+    tail = U.normal(U.gen(51), 50, d).to(torch.float16).to(CUDA)
+    x[-50:] = tail
+    rows = tss.gather_rows(x, order)
+    row = order.row[-50:].long()
+    kept = (row >= 0)[..., None]
+    assert torch.equal(rows[row.clamp(min=0)] * kept, (tail[:, None] * kept))
+    weight = torch.ones(tokens, top, device=CUDA)
+    y = tss.combine_rows(rows, order, weight)
+    n = kept.sum(1)
+    assert torch.equal(y[-50:], (tail.float() * n).half()) and (y[:-50] == 0).all()
+    drows, dweight = tss.combine_rows_backward(x, rows, order, weight)
+    assert torch.equal(drows, rows)
+    want = (tail.double().square().sum(1)[:, None] * kept[..., 0]).cpu()
+    assert ((dweight[-50:].double().cpu() - want).abs() <= want * 2.0 ** -18).all() and (dweight[:-50] == 0).all()

@@ -9,6 +9,8 @@
 // wherever tensors begin and end; the workgroups' sums are added in a fixed
 // order by every workgroup that scales (the same bits on every run, and one
 // launch fewer than with a pass of its own).
+// 226505854 elements in 60 tensors, fp32 and bf16: 352 us, 110 of it the norm's
+// pass (5.6 TB/s); the outputs pass the caches by (through them 379).
 // The tensors' addresses travel in the kernel's arguments, kTable at a time:
 // no copy from host memory, so a captured graph holds all that it needs.
 #include <algorithm>
