@@ -177,7 +177,8 @@ def test_outputs_over_inputs_and_beside_others():
 
 @pytest.mark.parametrize("with_dh", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("shape", SHAPES + [(9000, 128), (5000, 1024), (3000, 40)])
+@pytest.mark.parametrize("shape", SHAPES + [(9000, 128), (5000, 1024), (3000, 40), (1500, 200), (1024, 72), (1024, 4096), (1025, 4096), (600, 8192),
+                                            (40, 2056)])
 def test_backward(shape, dtype, with_dh):
     rows, d = shape
     h, dy = rows_of(shape, dtype, 8), rows_of(shape, dtype, 9, mean=0)
@@ -195,13 +196,20 @@ def test_backward(shape, dtype, with_dh):
     half, low = U.half_step(dtype)
     check(got[0], dx, dx.abs() * half + size * REL + low, "dx")
     # a column's sum: at most rows / 256 + 1 rows of a lane in turn, then fixed trees of 6 + 4 and 64 + 4 + 16 additions
+    # (few rows: rows / 128 + 1 in turn, 4 + 16 additions: fewer up to 9000 rows)
     adds = (rows / 256 + 1 + 10 + 84) * 2.0 ** -24 + 4 * 2.0 ** -24
     check(got[1], (dy.double() * xhat).sum(0), (dy.double() * xhat).abs().sum(0) * adds, "dweight")
     check(got[2], dy.double().sum(0), dy.double().abs().sum(0) * adds, "dbias")
     again = tss.layer_norm_backward(dev(dy), dev(h), dev(w), dev(mean), dev(rstd), dev(dh), dbias=False)
     assert again[2] is None and torch.equal(again[0], got[0]) and torch.equal(again[1], got[1])
     over = dev(dy)
-    assert torch.equal(tss.layer_norm_backward(over, dev(h), dev(w), dev(mean), dev(rstd), dev(dh), dx=over)[0], got[0])
+    over = tss.layer_norm_backward(over, dev(h), dev(w), dev(mean), dev(rstd), dev(dh), dx=over)
+    assert torch.equal(over[0], got[0])
+    check(over[1], (dy.double() * xhat).sum(0), (dy.double() * xhat).abs().sum(0) * adds, "dweight, dx over dy")
+    check(over[2], dy.double().sum(0), dy.double().abs().sum(0) * adds, "dbias, dx over dy")
+    if with_dh:
+        over = dev(dh)
+        assert torch.equal(tss.layer_norm_backward(dev(dy), dev(h), dev(w), dev(mean), dev(rstd), over, dx=over)[0], got[0])
 
 
 def test_gradients_are_differences():

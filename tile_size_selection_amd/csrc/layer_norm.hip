@@ -14,7 +14,7 @@
 // shows, is taken out again, so that a mean far from zero costs no digits.
 // 16384 x 4096, bf16: 50 us (5.3 TB/s; a large copy: 5.1), with residual 99 to 105,
 // backward 106, of which 4.5 add up dw and db; 300000 x 128, fp16: 29.5 us (5.2
-// TB/s); one row of 4096: 2.7 us.
+// TB/s); one row of 4096: 2.7 us, its backward 4.3.
 #include "row_launch.h"
 
 using namespace tss;
@@ -207,6 +207,14 @@ struct BackArgs {
   float *partial;  // [2][workgroups][d]: shares of dw and of db
 };
 
+// dh + r (g w - sg - (x - m) r sx), its fused steps written out, and none with a conversion to fp16 (the
+// empty statement): the kernels below give the same bits.
+__device__ __forceinline__ float dx_of(float g, float w, float x, float m, float r, float sg, float sx, float dh) {
+  float v = __builtin_fmaf(r, __builtin_fmaf(-((x - m) * r), sx, __builtin_fmaf(g, w, -sg)), dh);
+  asm("" : "+v"(v));
+  return v;
+}
+
 constexpr int kNarrowThreads = 256;
 
 // Teams of L lanes, or (L == 64) the whole workgroup, take a row each, a
@@ -302,8 +310,8 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
           const float gx = (x[i] - m) * r * g[i];
           dw[c][i] += gx;
           db[c][i] += g[i];
-          sg += g[i] * w[i];
-          sx += gx * w[i];
+          sg = __builtin_fmaf(g[i], w[i], sg);
+          sx = __builtin_fmaf(gx, w[i], sx);
         }
       }
       sg = sum_lanes<L>(sg);
@@ -343,7 +351,7 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
         opaque(weight[c]);
         widen8(weight[c], w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += r * (g[i] * w[i] - sg - (x[i] - m) * r * sx);
+        for (int i = 0; i < 8; ++i) o[i] = dx_of(g[i], w[i], x[i], m, r, sg, sx, o[i]);
         store8(dx + row * d + col, o);
         if constexpr (CH > 2) asm volatile("" ::: "memory");
       }
@@ -386,6 +394,111 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   }
 }
 
+// Few elements: one launch, whose first workgroups take a cache line of columns each over
+// all rows, for dw and db, and the others the rows, W waves each, for dx.  They share
+// nothing, so dy and h are read twice, the second time from the caches.
+constexpr int kFewThreads = 1024;
+constexpr int kTogether = 4;  // rows whose loads a thread has in flight
+template <typename T>
+constexpr int kFewLanes = 16 / sizeof(T);  // lanes of 8 columns that make 128 bytes
+
+template <typename T, int W>
+__global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(BackArgs p, int column_groups, float *dweight,
+                                                                              float *dbias) {
+  constexpr int kWaves = kFewThreads / 64, L = kFewLanes<T>, kColumns = L * 8;
+  const int wave = threadIdx.x >> 6, rows = p.rows, d = p.d;
+  const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
+  if (int(blockIdx.x) < column_groups) {
+    __shared__ float join[2][kWaves][kColumns];
+    const int l = threadIdx.x % L, col = (blockIdx.x * L + l) * 8;
+    float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0}, db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int row0 = threadIdx.x / L; row0 < rows; row0 += kTogether * (kFewThreads / L)) {
+      Raw8<T> a[kTogether], b[kTogether];
+      float m[kTogether], r[kTogether];
+#pragma unroll
+      for (int u = 0; u < kTogether; ++u) {
+        const int row = row0 + u * (kFewThreads / L);
+        const bool in = row < rows && col < d;
+        a[u] = in ? load8(dy + int64_t(row) * d + col) : zero8<T>();
+        b[u] = in ? load8(hh + int64_t(row) * d + col) : zero8<T>();
+        m[u] = in ? p.mean[row] : 0.0f;
+        r[u] = in ? p.rstd[row] : 0.0f;
+      }
+#pragma unroll
+      for (int u = 0; u < kTogether; ++u) {
+        float g[8], x[8];
+        widen8(a[u], g);
+        widen8(b[u], x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          dw[i] += (x[i] - m[u]) * r[u] * g[i];
+          db[i] += g[i];
+        }
+      }
+    }
+    // the lanes of a wave that hold the same columns, then the waves in order
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int k = L; k < 64; k *= 2) {
+        dw[i] += __shfl_xor(dw[i], k);
+        db[i] += __shfl_xor(db[i], k);
+      }
+      if ((threadIdx.x & 63) < L) {
+        join[0][wave][l * 8 + i] = dw[i];
+        join[1][wave][l * 8 + i] = db[i];
+      }
+    }
+    __syncthreads();
+    const int c = threadIdx.x % kColumns, of = threadIdx.x / kColumns, at = blockIdx.x * kColumns + c;
+    float *out = of == 0 ? dweight : dbias;
+    if (of > 1 || !out || at >= d) return;
+    float v = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) v += join[of][i][c];
+    out[at] = v;
+    return;
+  }
+  __shared__ float red[2][kWaves];
+  const int row = (int(blockIdx.x) - column_groups) * (kWaves / W) + wave / W, col = threadIdx.x % (W * 64) * 8;
+  const bool in = row < rows && col < d;
+  const int64_t at = int64_t(row) * d + col;
+  float g[8], x[8], o[8], w[8];
+  widen8(in ? load8(dy + at) : zero8<T>(), g);
+  widen8(in ? load8(hh + at) : zero8<T>(), x);
+  widen8(in && dh ? load8(dh + at) : zero8<T>(), o);
+  widen8(in ? load8(static_cast<const T *>(p.weight) + col) : zero8<T>(), w);
+  const float m = row < rows ? p.mean[row] : 0.0f, r = row < rows ? p.rstd[row] : 0.0f, inv_d = 1.0f / float(d);
+  float sg = 0, sx = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // columns past the row: g = w = 0
+    const float gx = (x[i] - m) * r * g[i];
+    sg = __builtin_fmaf(g[i], w[i], sg);
+    sx = __builtin_fmaf(gx, w[i], sx);
+  }
+  sg = sum_lanes<64>(sg);
+  sx = sum_lanes<64>(sx);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      red[0][wave] = sg;
+      red[1][wave] = sx;
+    }
+    __syncthreads();
+    sg = sx = 0;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      sg += red[0][wave / W * W + i];
+      sx += red[1][wave / W * W + i];
+    }
+  }
+  sg *= inv_d;
+  sx *= inv_d;
+  if (!in) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = dx_of(g[i], w[i], x[i], m, r, sg, sx, o[i]);
+  store8(static_cast<T *>(p.dx) + at, o);
+}
+
 // Workgroups of the backward pass: 8 waves a CU (narrow rows: 16) and two
 // workgroups at least, but each adds 16 bytes a column (its shares of dw and
 // db, written and read) to the 8 a column that a row of 16-bit elements moves,
@@ -399,6 +512,26 @@ int64_t backward_blocks(int64_t rows, int64_t d) {
   const int64_t turns = (rows + teams - 1) / teams;  // a workgroup takes `teams` rows at a time
   const int64_t n = turns / 8 < cus ? cus : turns / 8 > fill ? fill : turns / 8;
   return turns < n ? turns : n;
+}
+
+// The columns' workgroups take 4.5 us and 1.5 more for 500 rows; rows of more bytes in all keep the CUs busy in
+// two launches too (us, one launch and two; bf16 256 x 4096: 5.0 and 10.7; 1000 x 1024 6.4 and 10.3, 8192 17.9
+// and 21.0; 2000 x 128 8.6 and 8.1; fp32 1000 x 4096: 17.9 and 18.5, 8192 34 and 30).
+bool few(int64_t rows, int64_t d, int64_t size) {
+  return rows <= 1024 && d <= kFewThreads * 8 && rows * d * size <= int64_t(1) << 24;
+}
+
+template <typename T>
+void launch_few(const BackArgs &a, float *dweight, float *dbias, hipStream_t s) {
+  const int columns = (a.d / 8 + kFewLanes<T> - 1) / kFewLanes<T>;
+  auto go = [&](auto kernel, int waves) {
+    const int per = kFewThreads / 64 / waves;
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(columns + (a.rows + per - 1) / per)), dim3(kFewThreads), 0, s, a, columns,
+                       dweight, dbias);
+  };
+  if (a.d <= 512) go(layer_norm_backward_few_kernel<T, 1>, 1);
+  else if (a.d <= 2048) go(layer_norm_backward_few_kernel<T, 4>, 4);
+  else go(layer_norm_backward_few_kernel<T, 16>, 16);
 }
 
 template <typename T>
@@ -469,6 +602,12 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
     return TSS_E_ALIGN;
   float *partial = static_cast<float *>(workspace);
   const BackArgs a{int(rows), int(d), dy, h, weight, mean, rstd, dh, dx, partial};
+  if (few(rows, d, dtype == TSS_F32 ? 4 : 2) && dx != dy && dx != h) {  // over dy or h: what one workgroup writes another may still have to read
+    if (dtype == TSS_F16) launch_few<_Float16>(a, dweight, dbias, s);
+    else if (dtype == TSS_BF16) launch_few<__bf16>(a, dweight, dbias, s);
+    else launch_few<float>(a, dweight, dbias, s);
+    return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
+  }
   if (dtype == TSS_F16) launch_backward<_Float16>(a, s);
   else if (dtype == TSS_BF16) launch_backward<__bf16>(a, s);
   else launch_backward<float>(a, s);
