@@ -21,6 +21,12 @@ using namespace tss;
 
 namespace {
 
+// The sum of n <= 16 slots, to every lane: a lane reads one (in turn, each read would wait for the one before).
+__device__ __forceinline__ float sum_slots(const float *slots, int n) {
+  const int i = threadIdx.x & 15;
+  return sum_lanes<16>(i < n ? slots[i] : 0.0f);
+}
+
 // ---- forward ----
 
 struct NormArgs {
@@ -62,11 +68,8 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
       red[set][slot + 1][wave] = v;
     }
     __syncthreads();
-    u = v = 0;
-    for (int i = 0; i < wpr; ++i) {
-      u += red[set][slot][i];
-      v += red[set][slot + 1][i];
-    }
+    u = sum_slots(red[set][slot], wpr);
+    v = sum_slots(red[set][slot + 1], wpr);
   };
 
   Raw8<T> xr[CH], rr[CH], wr[CH], br[CH];
@@ -199,7 +202,7 @@ int32_t launch_norm(const NormArgs &a, hipStream_t s) {
 // ---- backward ----
 
 struct BackArgs {
-  int rows, d;
+  int rows, d, wpr;  // waves of a row
   const void *dy, *h, *weight;
   const float *mean, *rstd;
   const void *dh;
@@ -216,8 +219,9 @@ __device__ __forceinline__ float dx_of(float g, float w, float x, float m, float
 }
 
 constexpr int kNarrowThreads = 256;
+constexpr int kTeamWaves = 8;  // of a workgroup of several teams
 
-// Teams of L lanes, or (L == 64) the whole workgroup, take a row each, a
+// Teams of L lanes, or (L == 64) of wpr waves, take a row each, a
 // launch's teams apart; a lane keeps its columns' shares of dw and db in
 // registers over its rows, a workgroup joins its teams' and writes them to its
 // own slice of the workspace (added up in a fixed order afterwards: no
@@ -230,9 +234,9 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   constexpr bool kNarrow = L < 64;
   __shared__ float red[2][2][kMaxThreads / 64];
   const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
-  const int lanes = kNarrow ? L : int(blockDim.x), t = threadIdx.x % lanes;
-  const int teams = kNarrow ? kNarrowThreads / L : 1;
-  const int stride = gridDim.x * teams, first = blockIdx.x * teams + threadIdx.x / lanes;
+  const int wpr = kNarrow ? 1 : p.wpr, lanes = kNarrow ? L : wpr * 64, t = threadIdx.x % lanes;
+  const int teams = kNarrow ? kNarrowThreads / L : CH > 1 ? 1 : nw / wpr, team = threadIdx.x / lanes;
+  const int stride = gridDim.x * teams;
   const int rows = p.rows, d = p.d;
   const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
   T *dx = static_cast<T *>(p.dx);
@@ -268,14 +272,14 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
     rstd[s] = row < rows ? p.rstd[row] : 0.0f;
   };
 #pragma unroll
-  for (int s = 0; s < D; ++s) load_row(s, int64_t(first) + int64_t(s) * stride);
+  for (int s = 0; s < D; ++s) load_row(s, int64_t(blockIdx.x) * teams + team + int64_t(s) * stride);
   const float inv_d = 1.0f / float(d);
   int slot = 0;
-  for (int64_t row0 = first; row0 < rows; row0 += int64_t(S) * stride) {
+  for (int64_t row0 = int64_t(blockIdx.x) * teams; row0 < rows; row0 += int64_t(S) * stride) {
 #pragma unroll
     for (int s = 0; s < S; ++s) {
-      const int64_t row = row0 + int64_t(s) * stride;
-      if (row >= rows) break;
+      const int64_t row = row0 + team + int64_t(s) * stride;
+      if ((kNarrow ? row : row - team) >= rows) break;  // teams that meet at the barrier go on together
       Raw8<T> ca[CH], cb[CH], ce[CH];
       if constexpr (D > 0) {
 #pragma unroll
@@ -316,18 +320,15 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
       }
       sg = sum_lanes<L>(sg);
       sx = sum_lanes<L>(sx);
-      if (!kNarrow && nw > 1) {
+      if (!kNarrow && wpr > 1) {
         // two sets of slots: a wave writes the next row's while others may still read this row's
         if ((threadIdx.x & 63) == 0) {
           red[slot][0][wave] = sg;
           red[slot][1][wave] = sx;
         }
         __syncthreads();
-        sg = sx = 0;
-        for (int i = 0; i < nw; ++i) {
-          sg += red[slot][0][i];
-          sx += red[slot][1][i];
-        }
+        sg = sum_slots(&red[slot][0][team * wpr], wpr);
+        sx = sum_slots(&red[slot][1][team * wpr], wpr);
         slot ^= 1;
       }
       sg *= inv_d;
@@ -335,7 +336,7 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = col_of(c);
-        if (col >= d) continue;
+        if (col >= d || row >= rows) continue;
         float g[8], x[8], o[8], w[8];
         if constexpr (D > 0) {
           opaque(ca[c]);
@@ -383,6 +384,19 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
       }
       pw[c] = vw;
       pb[c] = vb;
+    }
+  } else if (CH == 1 && teams > 1) {
+    extern __shared__ float join_teams[];  // [team][8 columns of each lane]
+#pragma unroll
+    for (int of = 0; of < 2; ++of) {
+      store8(join_teams + threadIdx.x * 8, of ? db[0] : dw[0]);
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += blockDim.x) {
+        float v = 0;
+        for (int i = 0; i < teams; ++i) v += join_teams[i * lanes * 8 + c];
+        (of ? pb : pw)[c] = v;
+      }
+      __syncthreads();
     }
   } else {
 #pragma unroll
@@ -484,12 +498,8 @@ __global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(Ba
       red[1][wave] = sx;
     }
     __syncthreads();
-    sg = sx = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      sg += red[0][wave / W * W + i];
-      sx += red[1][wave / W * W + i];
-    }
+    sg = sum_slots(&red[0][wave / W * W], W);
+    sx = sum_slots(&red[1][wave / W * W], W);
   }
   sg *= inv_d;
   sx *= inv_d;
@@ -499,17 +509,24 @@ __global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(Ba
   store8(static_cast<T *>(p.dx) + at, o);
 }
 
-// Workgroups of the backward pass: 8 waves a CU (narrow rows: 16) and two
-// workgroups at least, but each adds 16 bytes a column (its shares of dw and
-// db, written and read) to the 8 a column that a row of 16-bit elements moves,
-// so no more than one for every 8 rows where that still gives every CU one.
-// 100000 x 512, bf16: 84 us, with 12 waves 90; 60000 x 1024, fp32: 187 and 203.
-int64_t backward_blocks(int64_t rows, int64_t d) {
+// Rows that a workgroup takes at a time.
+int64_t backward_teams(const Team &f) {
+  return f.lanes < 64 ? kNarrowThreads / f.lanes : f.waves < kTeamWaves ? kTeamWaves / f.waves : 1;
+}
+
+// Workgroups of the backward pass: two a CU (narrow rows: four; fp32 rows in
+// teams: one, whose loads are twice the bytes), but each adds 16 bytes a column
+// (its shares of dw and db, written and read) to the 8 a column that a row of
+// 16-bit elements moves, so no more than one for every 8 turns where that still
+// gives every CU one.  100000 x 512, bf16: 83 us, 60000 x 1024 100, by one
+// workgroup a CU 80 and 104, by four 84 and 106, and by more of one row each,
+// without teams, 87 and 107; 200000 x 264 86 (128 without); fp32 100000 x 512
+// 152, by two workgroups 164.
+int64_t backward_blocks(int64_t rows, int64_t d, int64_t size) {
   constexpr int64_t cus = 256;
   const Team f = team_of(d, 1);
-  const int64_t teams = f.lanes < 64 ? kNarrowThreads / f.lanes : 1;
-  const int64_t per_cu = f.lanes < 64 ? 4 : 8 / f.waves, fill = cus * (per_cu > 2 ? per_cu : 2);
-  const int64_t turns = (rows + teams - 1) / teams;  // a workgroup takes `teams` rows at a time
+  const int64_t teams = backward_teams(f), fill = cus * (f.lanes < 64 ? 4 : teams > 1 && size == 4 ? 1 : 2);
+  const int64_t turns = (rows + teams - 1) / teams;
   const int64_t n = turns / 8 < cus ? cus : turns / 8 > fill ? fill : turns / 8;
   return turns < n ? turns : n;
 }
@@ -539,8 +556,9 @@ void launch_backward(const BackArgs &a, hipStream_t s) {
   const Team f = team_of(a.d, 1);
   // One row ahead: two rows' registers leave room for fewer waves (300000 x 128,
   // bf16: 63 us, two ahead 68; 16384 x 4096, fp32: 202 and 249; bf16 106 and 110).
-  const dim3 grid(uint32_t(backward_blocks(a.rows, a.d))), block(f.lanes < 64 ? kNarrowThreads : f.waves * 64);
-  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a); };
+  const dim3 grid(uint32_t(backward_blocks(a.rows, a.d, sizeof(T)))), block(f.lanes < 64 ? kNarrowThreads : backward_teams(f) * f.waves * 64);
+  const int lds = f.lanes == 64 && backward_teams(f) > 1 ? int(block.x) * 32 : 0;  // to join the teams' sums
+  auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, s, a); };
   if (f.lanes == 8) go(layer_norm_backward_kernel<T, 1, 1, 8>);
   else if (f.lanes == 16) go(layer_norm_backward_kernel<T, 1, 1, 16>);
   else if (f.lanes == 32) go(layer_norm_backward_kernel<T, 1, 1, 32>);
@@ -580,7 +598,7 @@ int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, co
 
 int64_t tss_layer_norm_backward_workspace_size(int64_t rows, int64_t d) {
   const int32_t st = check_rows(rows, d, TSS_F32, INT32_MAX);
-  return st != TSS_OK ? st : backward_blocks(rows, d) * d * 8;
+  return st != TSS_OK ? st : backward_blocks(rows, d, 2) * d * 8;  // fp32 takes no more
 }
 
 int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
@@ -601,7 +619,7 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
       misaligned(workspace))
     return TSS_E_ALIGN;
   float *partial = static_cast<float *>(workspace);
-  const BackArgs a{int(rows), int(d), dy, h, weight, mean, rstd, dh, dx, partial};
+  const BackArgs a{int(rows), int(d), team_of(d, 1).waves, dy, h, weight, mean, rstd, dh, dx, partial};
   if (few(rows, d, dtype == TSS_F32 ? 4 : 2) && dx != dy && dx != h) {  // over dy or h: what one workgroup writes another may still have to read
     if (dtype == TSS_F16) launch_few<_Float16>(a, dweight, dbias, s);
     else if (dtype == TSS_BF16) launch_few<__bf16>(a, dweight, dbias, s);
@@ -611,7 +629,7 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
   if (dtype == TSS_F16) launch_backward<_Float16>(a, s);
   else if (dtype == TSS_BF16) launch_backward<__bf16>(a, s);
   else launch_backward<float>(a, s);
-  launch_column_sums(backward_blocks(rows, d), d, partial, dweight, dbias, s);
+  launch_column_sums(backward_blocks(rows, d, dtype == TSS_F32 ? 4 : 2), d, partial, dweight, dbias, s);
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 
