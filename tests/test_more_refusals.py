@@ -145,7 +145,10 @@ def test_combine_backward_refuses(change, status):
     assert C.lib().tss_combine_rows_backward(*_with(COMBINE_BACK, **change)) == status
 
 
-def clip(at, sizes, types, out=None, max_norm=1.0, norm=P, ws=P, ws_bytes=1 << 20):
+NORM = P + (1 << 24)
+
+
+def clip(at, sizes, types, out=None, max_norm=1.0, norm=NORM, ws=P, ws_bytes=1 << 20):
     n = len(at)
     pointers = lambda v: None if v is None else (ctypes.c_void_p * n)(*v)  # noqa: E731
     return C.lib().tss_clip_grad_norm(n, pointers(at), (C.i64 * n)(*sizes), (C.i32 * n)(*types), max_norm, pointers(out),
@@ -170,7 +173,10 @@ Q = P + (1 << 16)
     (dict(at=[P, Q], sizes=[8, 8], types=[F32] * 2, out=[Q, P]), ARG),
     (dict(at=[P], sizes=[8], types=[F32], out=[P + 4]), ARG), (dict(at=[P + 4], sizes=[8], types=[F32], out=[P]), ARG),
     (dict(at=[P, P + 16], sizes=[8, 8], types=[F32] * 2, out=[P, P + 16]), ARG),
-    (dict(at=[P, Q], sizes=[8, 8], types=[F32] * 2, out=[P + 64, P + 92]), ARG)])
+    (dict(at=[P, Q], sizes=[8, 8], types=[F32] * 2, out=[P + 64, P + 92]), ARG),
+    # the norm's place inside a tensor that is scaled, an output, an input
+    (dict(at=[P], sizes=[8], types=[F32], out=[P], norm=P + 28), ARG), (dict(at=[P], sizes=[8], types=[F32], out=[Q], norm=Q), ARG),
+    (dict(at=[P], sizes=[8], types=[F32], out=[Q], norm=P + 4), ARG)])
 def test_clip_refuses(call, status):
     assert clip(**call) == status
 

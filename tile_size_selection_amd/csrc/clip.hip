@@ -272,14 +272,16 @@ int32_t count_sums(int64_t n, const int64_t *sizes, Sums *out) {
 }
 
 // An output may be its own input; apart from that no output overlaps another
-// output or an input.
-bool overlapping(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int32_t *types) {
+// output or an input, nor does the norm's place.
+bool overlapping(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int32_t *types,
+                 const float *norm) {
   struct Span {
     uintptr_t begin, end;
     bool written;
   };
   std::vector<Span> spans;
-  spans.reserve(size_t(2 * n));
+  spans.reserve(size_t(2 * n + 1));
+  spans.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm + 1), true});
   for (int64_t i = 0; i < n; ++i) {
     if (sizes[i] == 0) continue;
     const uintptr_t bytes = uintptr_t(sizes[i]) * bytes_of(types[i]);
@@ -314,7 +316,7 @@ int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const in
   if (reinterpret_cast<uintptr_t>(norm) % 4 || reinterpret_cast<uintptr_t>(workspace) % 8) return TSS_E_ALIGN;
   const int64_t sums = c.sums;
   if (sums && !c.one() && (!workspace || workspace_bytes < sums * 8)) return TSS_E_ARG;
-  if (out && overlapping(n, grads, out, sizes, dtypes)) return TSS_E_ARG;
+  if (out && overlapping(n, grads, out, sizes, dtypes, norm)) return TSS_E_ARG;
   double *partial = static_cast<double *>(workspace);
   // launch(table, its workgroups) for each table
   auto tables = [&](auto launch) {
