@@ -145,10 +145,10 @@ def test_combine_backward_refuses(change, status):
     assert C.lib().tss_combine_rows_backward(*_with(COMBINE_BACK, **change)) == status
 
 
-NORM = P + (1 << 24)
+CLIP_NORM = P + (1 << 24)
 
 
-def clip(at, sizes, types, out=None, max_norm=1.0, norm=NORM, ws=P, ws_bytes=1 << 20):
+def clip(at, sizes, types, out=None, max_norm=1.0, norm=CLIP_NORM, ws=P, ws_bytes=1 << 20):
     n = len(at)
     pointers = lambda v: None if v is None else (ctypes.c_void_p * n)(*v)  # noqa: E731
     return C.lib().tss_clip_grad_norm(n, pointers(at), (C.i64 * n)(*sizes), (C.i32 * n)(*types), max_norm, pointers(out),
