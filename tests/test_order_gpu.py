@@ -100,6 +100,15 @@ def test_gather(tokens, top, d, dtype):
     assert torch.equal(tss.gather_rows(x.to(CUDA), order).view(torch.int8).cpu(), want)
 
 
+@pytest.mark.parametrize("tokens,top,d", [(9000, 8, 4096), (9001, 8, 4104), (70000, 4, 1024), (40000, 7, 1032)])
+def test_gather_of_many_bytes(tokens, top, d):
+    order = tss.sort_by_expert(choices(tokens, top, 30, 12).to(CUDA), 30)
+    x = torch.randint(-128, 128, (tokens, d), generator=U.gen(13), dtype=torch.int8).to(CUDA)
+    rows = tss.gather_rows(x, order)
+    kept = order.choice >= 0
+    assert torch.equal(rows, x[order.choice.clamp(min=0).long() // top] * kept[:, None])
+
+
 def of_choices(rows, row):
     return torch.where((row >= 0)[..., None], rows.double()[row.clamp(min=0).long()], 0)
 

@@ -241,8 +241,10 @@ SortShape sort_shape(int64_t n, int64_t E) {
 constexpr int kRowThreads = 256;
 
 // Bytes of gathered rows from which on they pass the caches by (131072 x 4096
-// bytes: 118.5 us, through them 125.7); fewer are read from there by the
-// product that follows.
+// bytes: 102 us, through them 113; x 4160 109 and 122); fewer are read from there
+// by the product that follows.  Rows that share 64 bytes with their neighbours
+// go through the caches, which join the parts (x 4112 143 us, past them 155;
+// 64000 x 8200 144 and 168).
 constexpr int64_t kStreamed = int64_t(1) << 28;
 
 // What 16 (or 8) bytes of a row are to the copies below.
@@ -530,10 +532,10 @@ int32_t tss_gather_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, c
   const GatherArgs a{x, rows, row, choice, scale, scale_out, int(tokens), int(top), int(pieces), int(scale_blocks),
                      uint32_t(scale_groups)};
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool streamed = n * d * size >= kStreamed;
+  const bool streamed = n * d * size >= kStreamed && d * size % 64 == 0;
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(uint32_t(all)), dim3(kRowThreads), 0, s, a); };
   if (wide) streamed ? go(gather_rows_kernel<16, true>) : go(gather_rows_kernel<16, false>);
-  else streamed ? go(gather_rows_kernel<8, true>) : go(gather_rows_kernel<8, false>);
+  else go(gather_rows_kernel<8, false>);
   return launched();
 }
 
