@@ -39,7 +39,8 @@ def check(got, ts, max_norm, norm):
 SIZES = {
     "one": [1], "small": [5, 1, 300, 4096, 17], "empty ones": [0, 7, 0, 0, 4097, 0], "one workgroup": [2048 * 3 + 1, 5, 2048 * 12, 700, 2047], "a unit more": [2048 * 20, 1], "ragged": [4095, 4096, 4097, 8193, 123457],
     "pieces": [5000003, 1, 2 ** 20], "many": [37 + i for i in range(400)], "a table": [64] * 128, "over a table": [64] * 129,
-    "large": [70000001, 33]}
+    "large": [70000001, 33],
+    "a small table": [3000] * 5 + [0, 0] + [3001] * 11 + [0], "over it": [3000] * 17}
 
 
 @pytest.mark.parametrize("ratio", [0.25, 4.0])
