@@ -177,7 +177,8 @@ def test_outputs_over_inputs_and_beside_others():
 
 @pytest.mark.parametrize("with_dh", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("shape", SHAPES + [(9000, 128), (5000, 1024), (3000, 40), (1500, 200), (1024, 72), (1024, 4096), (1025, 4096), (600, 8192), (1300, 520), (2051, 1544), (5000, 264),
+@pytest.mark.parametrize("shape", SHAPES + [(9000, 128), (5000, 1024), (3000, 40), (1500, 200), (1024, 72), (1024, 4096), (1025, 4096), (600, 8192), (1300, 520), (2051, 1544), (5000, 264), (187, 11056), (30, 16384), (64, 2056), (65, 504),
+                                            (66, 16376),
                                             (40, 2056)])
 def test_backward(shape, dtype, with_dh):
     rows, d = shape

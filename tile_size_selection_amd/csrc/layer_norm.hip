@@ -14,7 +14,7 @@
 // shows, is taken out again, so that a mean far from zero costs no digits.
 // 16384 x 4096, bf16: 50 us (5.3 TB/s; a large copy: 5.1), with residual 99 to 105,
 // backward 106, of which 4.5 add up dw and db; 300000 x 128, fp16: 29.5 us (5.2
-// TB/s); one row of 4096: 2.7 us, its backward 4.3.
+// TB/s); one row of 4096: 2.7 us, its backward 3.5.
 #include "row_launch.h"
 
 using namespace tss;
@@ -408,30 +408,28 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   }
 }
 
-// Few elements: one launch, whose first workgroups take a cache line of columns each over
-// all rows, for dw and db, and the others the rows, W waves each, for dx.  They share
+// Few elements: one launch, whose first workgroups take 8 L columns each over all rows, for
+// dw and db, and the others the rows, W waves each (CH > 1: a workgroup each), for dx.  They share
 // nothing, so dy and h are read twice, the second time from the caches.
 constexpr int kFewThreads = 1024;
-constexpr int kTogether = 4;  // rows whose loads a thread has in flight
 template <typename T>
-constexpr int kFewLanes = 16 / sizeof(T);  // lanes of 8 columns that make 128 bytes
-
-template <typename T, int W>
+constexpr int kRowsTogether = 8 / sizeof(T);  // rows whose loads a thread has in flight
+template <typename T, int W, int CH, int L>
 __global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(BackArgs p, int column_groups, float *dweight,
                                                                               float *dbias) {
-  constexpr int kWaves = kFewThreads / 64, L = kFewLanes<T>, kColumns = L * 8;
-  const int wave = threadIdx.x >> 6, rows = p.rows, d = p.d;
+  constexpr int kWaves = kFewThreads / 64, kTogether = kRowsTogether<T>;
+  const int wave = threadIdx.x >> 6, nw = CH > 1 ? blockDim.x >> 6 : kWaves, rows = p.rows, d = p.d;
   const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
   if (int(blockIdx.x) < column_groups) {
-    __shared__ float join[2][kWaves][kColumns];
+    __shared__ float join[2][kWaves][L * 8];
     const int l = threadIdx.x % L, col = (blockIdx.x * L + l) * 8;
     float dw[8] = {0, 0, 0, 0, 0, 0, 0, 0}, db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    for (int row0 = threadIdx.x / L; row0 < rows; row0 += kTogether * (kFewThreads / L)) {
+    for (int row0 = threadIdx.x / L; row0 < rows; row0 += kTogether * (nw * 64 / L)) {
       Raw8<T> a[kTogether], b[kTogether];
       float m[kTogether], r[kTogether];
 #pragma unroll
       for (int u = 0; u < kTogether; ++u) {
-        const int row = row0 + u * (kFewThreads / L);
+        const int row = row0 + u * (nw * 64 / L);
         const bool in = row < rows && col < d;
         a[u] = in ? load8(dy + int64_t(row) * d + col) : zero8<T>();
         b[u] = in ? load8(hh + int64_t(row) * d + col) : zero8<T>();
@@ -464,31 +462,44 @@ __global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(Ba
       }
     }
     __syncthreads();
-    const int c = threadIdx.x % kColumns, of = threadIdx.x / kColumns, at = blockIdx.x * kColumns + c;
+    constexpr int columns = L * 8;
+    const int c = threadIdx.x % columns, of = threadIdx.x / columns, at = blockIdx.x * columns + c;
     float *out = of == 0 ? dweight : dbias;
     if (of > 1 || !out || at >= d) return;
     float v = 0;
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i) v += join[of][i][c];
+    for (int i = 0; i < nw; ++i) v += join[of][i][c];
     out[at] = v;
     return;
   }
   __shared__ float red[2][kWaves];
-  const int row = (int(blockIdx.x) - column_groups) * (kWaves / W) + wave / W, col = threadIdx.x % (W * 64) * 8;
-  const bool in = row < rows && col < d;
-  const int64_t at = int64_t(row) * d + col;
-  float g[8], x[8], o[8], w[8];
-  widen8(in ? load8(dy + at) : zero8<T>(), g);
-  widen8(in ? load8(hh + at) : zero8<T>(), x);
-  widen8(in && dh ? load8(dh + at) : zero8<T>(), o);
-  widen8(in ? load8(static_cast<const T *>(p.weight) + col) : zero8<T>(), w);
+  const int wpr = CH > 1 ? nw : W, team = wave / wpr, t = threadIdx.x - team * wpr * 64;
+  const int row = (int(blockIdx.x) - column_groups) * (nw / wpr) + team;
+  auto col_of = [&](int c) __attribute__((always_inline)) { return (c * wpr * 64 + t) * 8; };
+  const int64_t base = int64_t(row) * d;
+  Raw8<T> a[CH], b[CH], e[CH], weight[CH];
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int col = col_of(c);
+    const bool in = row < rows && col < d;
+    a[c] = in ? load8(dy + base + col) : zero8<T>();
+    b[c] = in ? load8(hh + base + col) : zero8<T>();
+    e[c] = in && dh ? load8(dh + base + col) : zero8<T>();
+    weight[c] = in ? load8(static_cast<const T *>(p.weight) + col) : zero8<T>();
+  }
   const float m = row < rows ? p.mean[row] : 0.0f, r = row < rows ? p.rstd[row] : 0.0f, inv_d = 1.0f / float(d);
   float sg = 0, sx = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {  // columns past the row: g = w = 0
-    const float gx = (x[i] - m) * r * g[i];
-    sg = __builtin_fmaf(g[i], w[i], sg);
-    sx = __builtin_fmaf(gx, w[i], sx);
+  for (int c = 0; c < CH; ++c) {
+    float g[8], x[8], w[8];
+    widen8(a[c], g);
+    widen8(b[c], x);
+    widen8(weight[c], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {  // columns past the row: g = w = 0
+      const float gx = (x[i] - m) * r * g[i];
+      sg = __builtin_fmaf(g[i], w[i], sg);
+      sx = __builtin_fmaf(gx, w[i], sx);
+    }
   }
   sg = sum_lanes<64>(sg);
   sx = sum_lanes<64>(sx);
@@ -498,15 +509,23 @@ __global__ __launch_bounds__(kFewThreads) void layer_norm_backward_few_kernel(Ba
       red[1][wave] = sx;
     }
     __syncthreads();
-    sg = sum_slots(&red[0][wave / W * W], W);
-    sx = sum_slots(&red[1][wave / W * W], W);
+    sg = sum_slots(&red[0][team * wpr], wpr);
+    sx = sum_slots(&red[1][team * wpr], wpr);
   }
   sg *= inv_d;
   sx *= inv_d;
-  if (!in) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = dx_of(g[i], w[i], x[i], m, r, sg, sx, o[i]);
-  store8(static_cast<T *>(p.dx) + at, o);
+  for (int c = 0; c < CH; ++c) {
+    if (row >= rows || col_of(c) >= d) continue;
+    float g[8], x[8], o[8], w[8];
+    widen8(a[c], g);
+    widen8(b[c], x);
+    widen8(e[c], o);
+    widen8(weight[c], w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = dx_of(g[i], w[i], x[i], m, r, sg, sx, o[i]);
+    store8(static_cast<T *>(p.dx) + base + col_of(c), o);
+  }
 }
 
 // Rows that a workgroup takes at a time.
@@ -531,24 +550,34 @@ int64_t backward_blocks(int64_t rows, int64_t d, int64_t size) {
   return turns < n ? turns : n;
 }
 
-// The columns' workgroups take 4.5 us and 1.5 more for 500 rows; rows of more bytes in all keep the CUs busy in
-// two launches too (us, one launch and two; bf16 256 x 4096: 5.0 and 10.7; 1000 x 1024 6.4 and 10.3, 8192 17.9
-// and 21.0; 2000 x 128 8.6 and 8.1; fp32 1000 x 4096: 17.9 and 18.5, 8192 34 and 30).
+// The columns' workgroups take 4 us and 2 more for 1000 rows; rows of more bytes in all keep the CUs busy in
+// two launches too (us, one launch and two; bf16 256 x 4096: 5.3 and 10.9; 1000 x 1024 6.4 and 9.5, 8192 17.9
+// and 21.0; 2000 x 128 8.6 and 8.1; fp32 1000 x 4096: 17.9 and 18.5, 8192 34 and 30; 500 x 16384 42.0 and 41.5).
 bool few(int64_t rows, int64_t d, int64_t size) {
-  return rows <= 1024 && d <= kFewThreads * 8 && rows * d * size <= int64_t(1) << 24;
+  return rows <= 1024 && d <= kFewThreads * 16 && rows * d * size <= int64_t(1) << 24;
 }
 
-template <typename T>
+template <typename T, int L>
 void launch_few(const BackArgs &a, float *dweight, float *dbias, hipStream_t s) {
-  const int columns = (a.d / 8 + kFewLanes<T> - 1) / kFewLanes<T>;
-  auto go = [&](auto kernel, int waves) {
-    const int per = kFewThreads / 64 / waves;
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(columns + (a.rows + per - 1) / per)), dim3(kFewThreads), 0, s, a, columns,
+  const Team f = team_of(a.d, 1);
+  const int columns = (a.d / 8 + L - 1) / L;
+  auto go = [&](auto kernel, int rows, int threads) {  // rows of a workgroup
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(columns + (a.rows + rows - 1) / rows)), dim3(threads), 0, s, a, columns,
                        dweight, dbias);
   };
-  if (a.d <= 512) go(layer_norm_backward_few_kernel<T, 1>, 1);
-  else if (a.d <= 2048) go(layer_norm_backward_few_kernel<T, 4>, 4);
-  else go(layer_norm_backward_few_kernel<T, 16>, 16);
+  if (a.d <= 512) go(layer_norm_backward_few_kernel<T, 1, 1, L>, 16, kFewThreads);
+  else if (a.d <= 2048) go(layer_norm_backward_few_kernel<T, 4, 1, L>, 4, kFewThreads);
+  else if (f.chunks == 1) go(layer_norm_backward_few_kernel<T, 16, 1, L>, 1, kFewThreads);
+  else go(layer_norm_backward_few_kernel<T, 16, 2, L>, 1, f.waves * 64);
+}
+
+// Columns of a workgroup: 128 bytes, which makes the most of the CUs; up to 64
+// rows 256 columns, fewer workgroups (64 x 16384, bf16: 5.1 us, fp32 1 x 16384
+// 4.8 and by 32 columns 11.5).
+template <typename T>
+void launch_few(const BackArgs &a, float *dweight, float *dbias, hipStream_t s) {
+  if (a.rows <= 64) launch_few<T, 32>(a, dweight, dbias, s);
+  else launch_few<T, 16 / sizeof(T)>(a, dweight, dbias, s);
 }
 
 template <typename T>
