@@ -591,6 +591,9 @@ int32_t tss_lds_probe(int32_t pattern, int32_t stride_words, int32_t iters, int3
  * largest value of the type, stored column-block-major, scale[col / 128][row]
  * or scale[col / 128][row / 128] (the last block of a row or column may be
  * short).  A NaN in a block makes its scale and all its values NaN.
+ * Here and below, what a call writes (outputs, statistics, workspace) must not
+ * overlap anything else that it reads or writes, unless it says that an output
+ * may be an input: then both begin at the same address.
  */
 
 /*
@@ -713,6 +716,8 @@ int64_t tss_clip_grad_norm_workspace_size(int64_t n, const int64_t *sizes);
  * j.  There are tokens * top rows, sorted by expert (a token's choices of one
  * expert in their order, and the experts' rows in the tokens' order).  A
  * choice outside 0 .. E - 1 is dropped: it comes behind all routed rows.
+ * Memory that is written and overlaps other memory of the call is refused with
+ * TSS_E_ARG, apart from what each call allows.
  */
 
 /*
@@ -723,7 +728,8 @@ int64_t tss_clip_grad_norm_workspace_size(int64_t n, const int64_t *sizes);
  * expert: tokens x top integers of expert_bits (32 or 64) bits.  1 <= E <=
  * 4096, tokens * top <= 2^30.  workspace: device memory of at least
  * tss_sort_by_expert_workspace_size bytes, 4-byte aligned, scratch (may be
- * NULL when that is 0).  tokens == 0: sizes is zero-filled.
+ * NULL when that is 0).  row may be expert where that is 32 bits.  tokens == 0:
+ * sizes is zero-filled.
  * Errors: TSS_E_ARG, TSS_E_DTYPE (expert_bits), TSS_E_ALIGN, TSS_E_HIP.
  */
 int32_t tss_sort_by_expert(int64_t tokens, int64_t top, int64_t E, const void *expert, int32_t expert_bits,
@@ -761,7 +767,8 @@ int32_t tss_combine_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, 
  * Gradients of tss_combine_rows: drows[row[t][j]] = weight[t][j] dy[t] (dtype;
  * dropped choices' rows zero) and dweight[t][j] (fp32) = <dy[t],
  * rows[row[t][j]]> (dropped: zero).  dtype: of dy and drows; rows_dtype: dtype
- * or TSS_F32.  drows may be rows when the types are the same.  d <= 32768.
+ * or TSS_F32.  drows may be rows when the types are the same, dweight may be
+ * weight.  d <= 32768.
  * Errors: as tss_gather_rows, TSS_E_UNSUPPORTED (d).
  */
 int32_t tss_combine_rows_backward(int64_t tokens, int64_t top, int64_t d, int32_t dtype, const void *dy,

@@ -1,0 +1,68 @@
+"""Calls whose outputs or workspace overlap what else they read or write are
+refused before any device work (their workgroups run in no order: each such
+call would be a race), through the C ABI with addresses that are never touched."""
+import pytest
+
+from tile_size_selection_amd import _capi as C
+
+ARG, BF16, F32, I8 = C.TSS_E_ARG, C.TSS_BF16, C.TSS_F32, C.TSS_I8
+MIB = 1 << 20
+
+
+def at(i, off=0):
+    """Address `off` bytes into the i-th of many places a MiB long."""
+    return (i + 1) * MIB + off
+
+
+def refused(call, base, change):
+    assert set(change) <= set(base)
+    return call(*{**base, **change}.values()) == ARG
+
+
+SORT = dict(tokens=4, top=2, E=8, expert=at(0), bits=64, sizes=at(1), row=at(2), choice=at(3), ws=None, ws_bytes=0, stream=None)
+LONG = dict(SORT, tokens=20000, ws=at(4), ws_bytes=MIB)
+
+
+@pytest.mark.parametrize("base,change", [
+    (SORT, dict(row=at(0))), (SORT, dict(row=at(0, 4), bits=32)), (SORT, dict(choice=at(0), bits=32)), (SORT, dict(choice=at(0, 60))),
+    (SORT, dict(sizes=at(0, 28), bits=32)), (SORT, dict(row=at(3))), (SORT, dict(choice=at(2, 28))), (SORT, dict(sizes=at(2, 28))),
+    (SORT, dict(sizes=at(2, -28))), (SORT, dict(sizes=at(3))), (SORT, dict(row=at(0), choice=at(0), bits=32)),
+    (LONG, dict(ws=at(0, 8))), (LONG, dict(ws=at(1))), (LONG, dict(ws=at(2, 159996))), (LONG, dict(ws=at(3, -4)))])
+def test_sort(base, change):
+    assert refused(C.lib().tss_sort_by_expert, base, change)
+
+
+GATHER = dict(tokens=4, top=2, d=64, dtype=BF16, x=at(0), row=at(1), choice=at(2), rows=at(3), scale=at(4), blocks=3,
+              scale_out=at(5), stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(rows=at(0)), dict(rows=at(0, 496)), dict(rows=at(0, -1008)), dict(rows=at(0), top=1), dict(rows=at(1, 16)),
+    dict(rows=at(2, -1008)), dict(rows=at(4, 32)), dict(scale_out=at(4)), dict(scale_out=at(4), top=1), dict(scale_out=at(3, 1020)),
+    dict(scale_out=at(0)), dict(scale_out=at(1)), dict(scale_out=at(2, 28)),
+    dict(rows=at(0), top=1, choice=None, scale=None, blocks=0, scale_out=None)])
+def test_gather(change):
+    assert refused(C.lib().tss_gather_rows, GATHER, change)
+
+
+COMBINE = dict(tokens=4, top=2, d=64, dtype=BF16, rows=at(0), row=at(1), weight=at(2), out=BF16, y=at(3), stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(y=at(0)), dict(y=at(0), top=1), dict(y=at(0, 1008)), dict(y=at(0, -496)), dict(y=at(0, -1008), out=F32), dict(y=at(1)),
+    dict(y=at(2, 16)), dict(y=at(0), weight=None)])
+def test_combine(change):
+    assert refused(C.lib().tss_combine_rows, COMBINE, change)
+
+
+BACK = dict(tokens=4, top=2, d=64, dtype=BF16, dy=at(0), rows_dtype=BF16, rows=at(1), row=at(2), weight=at(3), drows=at(4),
+            dweight=at(5), stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(drows=at(0)), dict(drows=at(0), top=1), dict(drows=at(0, 496)), dict(drows=at(1, 16)), dict(drows=at(1, -16)),
+    dict(drows=at(1), rows_dtype=F32), dict(drows=at(2)), dict(drows=at(3, 16)), dict(drows=at(5, -1008)), dict(dweight=at(0)),
+    dict(dweight=at(1, 1020)), dict(dweight=at(2)), dict(dweight=at(3, 4)), dict(dweight=at(4, 1020)),
+    dict(drows=at(1), dweight=at(1))])
+def test_combine_backward(change):
+    assert refused(C.lib().tss_combine_rows_backward, BACK, change)

@@ -20,6 +20,7 @@
 // dependent steps; 8 choices: 3.6), 16384 x 8 x 4096 bytes with scales gathered
 // in 107 us (5.8 TB/s; a large copy: 5.1), 5001 x 6 x 5120 bf16 combined in 70
 // (4.9), the gradients of 8200 x 4 x 2048 fp16 in 57 (5.3).
+#include "ranges.h"
 #include "row_launch.h"
 
 using namespace tss;
@@ -492,6 +493,13 @@ int32_t tss_sort_by_expert(int64_t tokens, int64_t top, int64_t E, const void *e
   for (const void *q : {(const void *)sizes, (const void *)row, (const void *)choice, (const void *)workspace})
     if (reinterpret_cast<uintptr_t>(q) & 3u) return TSS_E_ALIGN;
   if (reinterpret_cast<uintptr_t>(expert) & (expert_bits / 8 - 1)) return TSS_E_ALIGN;
+  Ranges at;
+  const uint32_t choices = at.reads(expert, n * expert_bits / 8);
+  at.writes(sizes, E * 4);
+  at.writes(row, n * 4, expert_bits == 32 ? choices : 0);  // a choice's own place, written when its bin is known
+  at.writes(choice, n * 4);
+  at.writes(workspace, need);
+  if (at.clash()) return TSS_E_ARG;
   const SortShape f = sort_shape(n, E);
   const int nw = sort_waves(int(E));
   const SortArgs a{expert, int(n), int(E), int(f.per_group), nw, f.scanned, sizes, row, choice, static_cast<uint32_t *>(workspace)};
@@ -529,6 +537,16 @@ int32_t tss_gather_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, c
   const int64_t scale_groups = (n + kRowThreads - 1) / kRowThreads * ((scale_blocks + kScalesTogether - 1) / kScalesTogether);
   const int64_t all = scale_groups + (tokens * pieces + kRowThreads - 1) / kRowThreads;
   if (all > (kMaxThreadsOfLaunch - kRowThreads) / kRowThreads) return TSS_E_ARG;
+  Ranges at;
+  at.reads(x, tokens * d * size);
+  at.reads(row, n * 4);
+  at.writes(rows, n * d * size);
+  if (scale_blocks) {
+    at.reads(choice, n * 4);
+    at.reads(scale, scale_blocks * tokens * 4);
+    at.writes(scale_out, scale_blocks * n * 4);
+  }
+  if (at.clash()) return TSS_E_ARG;
   const GatherArgs a{x, rows, row, choice, scale, scale_out, int(tokens), int(top), int(pieces), int(scale_blocks),
                      uint32_t(scale_groups)};
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -549,6 +567,12 @@ int32_t tss_combine_rows(int64_t tokens, int64_t top, int64_t d, int32_t dtype, 
     if (misaligned(rows) || misaligned(y)) return TSS_E_ALIGN;
     const int64_t chunks = d / 8;
     if (tokens * chunks > kMaxThreadsOfLaunch - kRowThreads) return TSS_E_ARG;
+    Ranges at;
+    at.reads(rows, tokens * top * d * size_of(dtype));
+    at.reads(row, tokens * top * 4);
+    at.reads(weight, tokens * top * 4);
+    at.writes(y, tokens * d * size_of(out_dtype));
+    if (at.clash()) return TSS_E_ARG;
     const CombineArgs a{rows, row, weight, y, int(tokens), int(top), int(chunks)};
     hipLaunchKernelGGL((combine_rows_kernel<decltype(r), decltype(o)>),
                        dim3(uint32_t((tokens * chunks + kRowThreads - 1) / kRowThreads)), dim3(kRowThreads), 0,
@@ -578,6 +602,14 @@ int32_t tss_combine_rows_backward(int64_t tokens, int64_t top, int64_t d, int32_
       const int block = lanes < 64 ? kRowThreads : f.waves * 64, per = lanes < 64 ? kRowThreads / lanes : 1;
       const int64_t groups = (tokens + per - 1) / per;
       if (groups * block > kMaxThreadsOfLaunch) return TSS_E_ARG;
+      const int64_t n = tokens * top;
+      Ranges at;
+      at.reads(dy, tokens * d * sizeof(D));
+      at.reads(row, n * 4);
+      const uint32_t values = at.reads(rows, n * d * sizeof(R)), weights = at.reads(weight, n * 4);
+      at.writes(drows, n * d * sizeof(D), __is_same(D, R) ? values : 0);
+      at.writes(dweight, n * 4, weights);
+      if (at.clash()) return TSS_E_ARG;
       const CombineBackArgs a{dy, rows, row, weight, drows, dweight, int(tokens), int(top), int(d)};
       auto go = [&](auto kernel) {
         hipLaunchKernelGGL(kernel, dim3(uint32_t(groups)), dim3(block), 0, static_cast<hipStream_t>(stream), a);

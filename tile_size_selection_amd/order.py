@@ -5,7 +5,10 @@ ops.py; the work is libtss.so's (include/tss.h documents each entry point).
 A router gives each of `tokens` tokens `top` choices of an expert.  Their rows,
 tokens * top in all, are sorted by expert, a token's in the order of its
 choices.  A choice outside 0 .. experts - 1 is dropped: its place is behind the
-routed rows, and is written as its complement (~place, a negative number)."""
+routed rows, and is written as its complement (~place, a negative number).
+
+An output given to a call may overlap none of its other tensors, apart from
+what the call allows: such calls are refused."""
 from __future__ import annotations
 
 from typing import NamedTuple, Optional, Tuple
@@ -43,7 +46,7 @@ def _order(order, tokens: Optional[int] = None) -> Tuple[int, int]:
 def sort_by_expert(expert, experts: int, sizes=None, row=None, choice=None, workspace=None) -> ExpertOrder:
     """ExpertOrder of expert (tokens, top), int32 or int64: the stable order of
     the choices by expert.  experts: 1 to 4096.  sizes, row, choice: outputs to
-    write into, else allocated; workspace: a device tensor of at least
+    write into, else allocated (row may be an int32 expert itself); workspace: a device tensor of at least
     tss_sort_by_expert_workspace_size bytes (allocated here when one is needed
     and not given)."""
     if expert.dim() != 2 or expert.shape[1] < 1 or expert.dtype not in (torch.int32, torch.int64):
@@ -125,7 +128,7 @@ def combine_rows_backward(dy, rows, order: ExpertOrder, weight, drows=None,
     """(drows, dweight) of combine_rows: drows[row[t][j]] = weight[t][j] *
     dy[t] in dy's type (zero behind the routed rows), dweight[t][j] = <dy[t],
     rows[row[t][j]]> in float32 (zero where dropped).  rows: dy's type or f32;
-    drows may be rows when the types are the same."""
+    drows may be rows when the types are the same, dweight may be weight."""
     dt = _name(dy, "dy", _FLOATS)
     rt = _name(rows, "rows", (dt, "f32"))
     if dy.dim() != 2:
