@@ -646,8 +646,9 @@ int32_t tss_quantize_fp8(int64_t rows, int64_t d, int32_t dtype, const void *x, 
  * weight + bias, row by row.  residual and bias may be NULL.  y: out_dtype
  * dtype, or TSS_I8 with scale[rows] (NULL otherwise) as tss_quantize_int8
  * makes them of y.  residual_out (may be NULL): h rounded to dtype; it may be
- * residual or x itself.  y may be x when out_dtype is dtype.  mean, rstd (may
- * be NULL): rows fp32, the mean and 1 / sqrt(...).  weight, bias: d elements of
+ * residual or x itself.  y may be x or residual when out_dtype is dtype (but
+ * not where residual_out is).  mean, rstd (may be NULL): rows fp32, the mean and
+ * 1 / sqrt(...).  Other overlaps are refused.  weight, bias: d elements of
  * dtype.  d <= 32768; rows < 2^31, and where d <= 512 the rows times 8, 16, 32
  * or 64 lanes of 8 columns (the fewest that hold one) below 2^32.  x, residual,
  * weight, bias, y and residual_out 16-byte aligned.  rows == 0: nothing to do.
@@ -664,7 +665,7 @@ int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, co
  * (the gradient of x and of residual; dh, which may be NULL, is what arrives
  * through residual_out), dweight[d] (fp32) = sum over rows of dy xhat and
  * dbias[d] (fp32; may be NULL) = sum over rows of dy, added in a fixed order.
- * dx may be dy or dh.  workspace: device memory of at least
+ * dx may be dy, h or dh; other overlaps are refused.  workspace: device memory of at least
  * tss_layer_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned,
  * scratch.  rows == 0: dweight and dbias are zero-filled.
  * Errors: as tss_layer_norm; TSS_E_ARG for a missing or small workspace.

@@ -66,3 +66,32 @@ BACK = dict(tokens=4, top=2, d=64, dtype=BF16, dy=at(0), rows_dtype=BF16, rows=a
     dict(drows=at(1), dweight=at(1))])
 def test_combine_backward(change):
     assert refused(C.lib().tss_combine_rows_backward, BACK, change)
+
+
+NORM = dict(rows=4, d=64, dtype=BF16, x=at(0), residual=at(1), weight=at(2), bias=at(3), eps=1e-5, out_dtype=BF16, y=at(4),
+            scale=None, h=at(5), mean=at(6), rstd=at(7), stream=None)
+NORM_I8 = dict(NORM, out_dtype=I8, scale=at(8))
+
+
+@pytest.mark.parametrize("base,change", [
+    (NORM, dict(y=at(0, 128))), (NORM, dict(y=at(0, -128))), (NORM, dict(y=at(1, 496))), (NORM, dict(y=at(2))), (NORM, dict(y=at(3, 112))),
+    (NORM, dict(y=at(5))), (NORM, dict(y=at(5, 16))), (NORM, dict(y=at(0), h=at(0))), (NORM, dict(h=at(1, 128))), (NORM, dict(h=at(2))),
+    (NORM, dict(mean=at(7))), (NORM, dict(mean=at(0))), (NORM, dict(rstd=at(6, 12))), (NORM, dict(rstd=at(4, 508))), (NORM, dict(mean=at(3))),
+    (NORM_I8, dict(y=at(0))), (NORM_I8, dict(y=at(1))), (NORM_I8, dict(y=at(1, 496))), (NORM_I8, dict(scale=at(4, 252))),
+    (NORM_I8, dict(scale=at(6))), (NORM_I8, dict(scale=at(0))), (NORM_I8, dict(y=at(5)))])
+def test_layer_norm(base, change):
+    assert refused(C.lib().tss_layer_norm, base, change)
+
+
+# 4 rows: one launch; 2000: two, which read dy and h once
+NORM_BACK = dict(rows=4, d=64, dtype=BF16, dy=at(0), h=at(1), weight=at(2), mean=at(3), rstd=at(4), dh=at(5), dx=at(6), dweight=at(7),
+                 dbias=at(8), ws=at(9), ws_bytes=MIB, stream=None)
+
+
+@pytest.mark.parametrize("rows", [4, 2000])
+@pytest.mark.parametrize("change", [
+    dict(dx=at(0, 128)), dict(dx=at(0, -128)), dict(dx=at(1, 128)), dict(dx=at(5, -16)), dict(dx=at(2)), dict(dx=at(3)), dict(dx=at(4, 0)),
+    dict(dx=at(7)), dict(dx=at(9)), dict(dweight=at(0)), dict(dweight=at(1, 64)), dict(dweight=at(8)), dict(dbias=at(2)), dict(dbias=at(6)),
+    dict(dbias=at(3)), dict(ws=at(0)), dict(ws=at(1, 16)), dict(ws=at(5)), dict(ws=at(6)), dict(ws=at(8)), dict(ws=at(7, -16))])
+def test_layer_norm_backward(change, rows):
+    assert refused(C.lib().tss_layer_norm_backward, dict(NORM_BACK, rows=rows), change)

@@ -60,3 +60,29 @@ def test_overlaps_are_refused():
         with pytest.raises(tss.TssError):
             call()
     assert (x == 1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(300, 64), (37, 520), (1300, 2056), (20, 8200), (5, 32768), (2000, 264)])
+def test_norms_over_their_inputs(rows, d, dtype):
+    g = U.gen(6)
+    x, r, dy = (U.normal(g, rows, d).to(U.TYPES[dtype]).to(CUDA) for _ in range(3))
+    w, b = ((1 + 0.2 * U.normal(g, d)).to(U.TYPES[dtype]).to(CUDA) for _ in range(2))
+    want = tss.layer_norm(x, w, b, r, stats=True)
+    over = r.clone()
+    assert torch.equal(tss.layer_norm(x, w, b, over, out=over).y, want.y)
+    a, c = x.clone(), r.clone()
+    got = tss.layer_norm(a, w, b, c, out=c, residual_out=a)  # crosswise
+    assert torch.equal(c, want.y) and torch.equal(a, want.h)
+    same = tss.layer_norm(x, w, b, x)
+    twice = x.clone()
+    got = tss.layer_norm(twice, w, b, twice, residual_out=twice)
+    assert torch.equal(got.y, same.y) and torch.equal(twice, same.h)
+    grads = tss.layer_norm_backward(dy, want.h, w, want.mean, want.rstd, r)
+    h = want.h.clone()
+    got = tss.layer_norm_backward(dy, h, w, want.mean, want.rstd, r, dx=h)
+    assert torch.equal(h, grads[0])
+    # few rows are added in another order then: each sum is off by at most rows + 3 roundings of its terms' magnitudes
+    xhat = (want.h.double() - want.mean.double()[:, None]) * want.rstd.double()[:, None]
+    for p, q, terms in ((got[1], grads[1], dy.double() * xhat), (got[2], grads[2], dy.double())):
+        assert ((p.double() - q.double()).abs() <= 2 * (rows + 3) * 2.0 ** -24 * terms.abs().sum(0)).all()

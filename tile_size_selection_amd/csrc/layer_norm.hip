@@ -15,6 +15,7 @@
 // 16384 x 4096, bf16: 50 us (5.3 TB/s; a large copy: 5.1), with residual 99 to 105,
 // backward 106, of which 4.5 add up dw and db; 300000 x 128, fp16: 29.5 us (5.2
 // TB/s); one row of 4096: 2.7 us, its backward 3.5.
+#include "ranges.h"
 #include "row_launch.h"
 
 using namespace tss;
@@ -612,6 +613,21 @@ int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, co
   if (misaligned(x) || misaligned(residual) || misaligned(weight) || misaligned(bias) || misaligned(y) ||
       misaligned(residual_out))
     return TSS_E_ALIGN;
+  const int64_t size = dtype == TSS_F32 ? 4 : 2, bytes = rows * d * size;
+  Ranges at;
+  const uint32_t inputs = at.reads(x, bytes) | at.reads(residual, bytes);
+  at.reads(weight, d * size);
+  at.reads(bias, d * size);
+  if (out_dtype == TSS_I8) {
+    at.writes(y, rows * d);
+    at.writes(scale, rows * 4);
+  } else {
+    at.writes(y, bytes, inputs);
+  }
+  at.writes(residual_out, bytes, inputs);
+  at.writes(mean, rows * 4);
+  at.writes(rstd, rows * 4);
+  if (at.clash()) return TSS_E_ARG;
   const NormArgs a{int(rows), int(d), 1, x, residual, weight, bias, eps, y, scale, residual_out, mean, rstd};
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto go = [&](auto t) {
@@ -647,9 +663,20 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
   if (misaligned(dy) || misaligned(h) || misaligned(weight) || misaligned(dh) || misaligned(dx) ||
       misaligned(workspace))
     return TSS_E_ALIGN;
+  const int64_t size = dtype == TSS_F32 ? 4 : 2, bytes = rows * d * size;
+  Ranges at;
+  const uint32_t inputs = at.reads(dy, bytes) | at.reads(h, bytes) | at.reads(dh, bytes);
+  at.reads(weight, d * size);
+  at.reads(mean, rows * 4);
+  at.reads(rstd, rows * 4);
+  at.writes(dx, bytes, inputs);
+  at.writes(dweight, d * 4);
+  at.writes(dbias, d * 4);
+  at.writes(workspace, tss_layer_norm_backward_workspace_size(rows, d));
+  if (at.clash()) return TSS_E_ARG;
   float *partial = static_cast<float *>(workspace);
   const BackArgs a{int(rows), int(d), team_of(d, 1).waves, dy, h, weight, mean, rstd, dh, dx, partial};
-  if (few(rows, d, dtype == TSS_F32 ? 4 : 2) && dx != dy && dx != h) {  // over dy or h: what one workgroup writes another may still have to read
+  if (few(rows, d, size) && dx != dy && dx != h) {  // over dy or h: what one workgroup writes another may still have to read
     if (dtype == TSS_F16) launch_few<_Float16>(a, dweight, dbias, s);
     else if (dtype == TSS_BF16) launch_few<__bf16>(a, dweight, dbias, s);
     else launch_few<float>(a, dweight, dbias, s);
@@ -658,7 +685,7 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
   if (dtype == TSS_F16) launch_backward<_Float16>(a, s);
   else if (dtype == TSS_BF16) launch_backward<__bf16>(a, s);
   else launch_backward<float>(a, s);
-  launch_column_sums(backward_blocks(rows, d, dtype == TSS_F32 ? 4 : 2), d, partial, dweight, dbias, s);
+  launch_column_sums(backward_blocks(rows, d, size), d, partial, dweight, dbias, s);
   return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
 }
 

@@ -228,7 +228,8 @@ def layer_norm(x, weight, bias=None, residual=None, eps: float = 1e-5, out_dtype
     gives).  h comes back rounded to x's type (residual_out may be residual
     itself).  stats: True, or a pair of float32 tensors of `rows`, to get the
     mean and rstd that the backward pass takes.  out, scale, residual_out:
-    outputs to write into, else allocated."""
+    outputs to write into, else allocated; out may be x or residual (unless it
+    is 'i8', or residual_out is that one), other overlaps are refused."""
     dt = _name(x, "x", ("f16", "bf16", "f32"))
     if x.dim() != 2:
         raise ValueError("x must be (rows, d)")
@@ -265,7 +266,8 @@ def layer_norm_backward(dy, h, weight, mean, rstd, dh=None, dx=None, dweight=Non
     (g - mean(g) - xhat mean(g xhat)), the gradient of both x and residual (dh:
     the gradient that arrives through h; it may be None), dweight = sum over
     rows of dy xhat and dbias = sum over rows of dy in float32, the same bits on
-    every run.  dbias False: not computed, None comes back.  dx may be dy or dh."""
+    every run.  dbias False: not computed, None comes back.  dx may be dy, h or
+    dh; other overlaps are refused."""
     dt = _name(dy, "dy", ("f16", "bf16", "f32"))
     if dy.dim() != 2:
         raise ValueError("dy must be (rows, d)")
