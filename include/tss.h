@@ -684,7 +684,7 @@ int64_t tss_layer_norm_backward_workspace_size(int64_t rows, int64_t d);
  * fp32).  A row with a NaN or an infinity has that as its scale; all its values
  * are 0.  d <= 32768 (of q); rows times the lanes that hold one (8 columns each)
  * below about 2^32; x and q 16-byte aligned, scale 4-byte.  rows == 0: nothing
- * to do.
+ * to do.  Overlaps are refused (TSS_E_ARG).
  * Errors: as tss_layer_norm.
  */
 int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x, int32_t gated, void *q, float *scale,
@@ -814,6 +814,7 @@ int64_t tss_gemm_fp8_workspace_size(int64_t M, int64_t N, int64_t K);
  * that is 0), 16-byte aligned, scratch.
  * K a multiple of 16 below 2^17, any M and N; A, B, C 16-byte aligned, sa and
  * sb 4-byte; A and B below 2 GiB each; fewer than 2^23 tiles of 64 x 128 of C.
+ * C and workspace that overlap an operand or each other are refused.
  * M == 0 or N == 0: nothing to do.  K == 0: C is zero-filled.
  * Errors: TSS_E_ARG, TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */

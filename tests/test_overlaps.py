@@ -95,3 +95,26 @@ NORM_BACK = dict(rows=4, d=64, dtype=BF16, dy=at(0), h=at(1), weight=at(2), mean
     dict(dbias=at(3)), dict(ws=at(0)), dict(ws=at(1, 16)), dict(ws=at(5)), dict(ws=at(6)), dict(ws=at(8)), dict(ws=at(7, -16))])
 def test_layer_norm_backward(change, rows):
     assert refused(C.lib().tss_layer_norm_backward, dict(NORM_BACK, rows=rows), change)
+
+
+QUANT = dict(rows=4, d=64, dtype=BF16, x=at(0), gated=0, q=at(1), scale=at(2), stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=at(0)), dict(q=at(0), dtype=F32), dict(q=at(0, 496)), dict(q=at(0, -240)), dict(q=at(0, 512), gated=1), dict(q=at(2, -240)),
+    dict(scale=at(0)), dict(scale=at(1, 252)), dict(scale=at(0, 1020), gated=1), dict(scale=at(0, 1020), dtype=F32)])
+def test_quantize_int8(change):
+    assert refused(C.lib().tss_quantize_int8, QUANT, change)
+
+
+GEMM = dict(M=4, N=64, K=128, A=at(0), B=at(1), sa=at(2), sb=at(3), C=at(4), out=BF16, ws=None, ws_bytes=0, stream=None)
+SPLIT = dict(GEMM, M=256, N=512, K=8192, B=at(8), sa=at(16), sb=at(17), C=at(18), ws=at(24), ws_bytes=1 << 24)
+
+
+@pytest.mark.parametrize("base,change", [
+    (GEMM, dict(C=at(0))), (GEMM, dict(C=at(0, -496))), (GEMM, dict(C=at(0, 496))), (GEMM, dict(C=at(1, 8176))), (GEMM, dict(C=at(2))),
+    (GEMM, dict(C=at(3, 240))), (GEMM, dict(C=at(2, -1008), out=F32)),
+    (SPLIT, dict(C=at(8))), (SPLIT, dict(ws=at(0))), (SPLIT, dict(ws=at(8, 16))), (SPLIT, dict(ws=at(16))), (SPLIT, dict(ws=at(17))),
+    (SPLIT, dict(ws=at(18))), (SPLIT, dict(ws=at(18, -16))), (SPLIT, dict(C=at(24, 16)))])
+def test_gemm_int8(base, change):
+    assert refused(C.lib().tss_gemm_int8, base, change)

@@ -11,6 +11,7 @@
 
 #include "gemm_int8_kernel.h"
 #include "plans.h"
+#include "ranges.h"
 #include "row_launch.h"
 
 using namespace tss;
@@ -188,6 +189,11 @@ int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x,
   if (rows == 0) return TSS_OK;
   if (!x || !q || !scale) return TSS_E_ARG;
   if (misaligned(x) || misaligned(q) || off_by(scale, 4)) return TSS_E_ALIGN;
+  Ranges at;
+  at.reads(x, rows * d * (dtype == TSS_F32 ? 4 : 2) * (gated ? 2 : 1));
+  at.writes(q, rows * d);
+  at.writes(scale, rows * 4);
+  if (at.clash()) return TSS_E_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto go = [&](auto t) {
     using T = decltype(t);
@@ -244,6 +250,14 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   const int64_t tiles_m = (M + pl.bm - 1) / pl.bm, tiles_n = (N + pl.bn - 1) / pl.bn, blocks = tiles_m * tiles_n * a.splits;
   // the launch's thread count is 32 bits (1024 threads at most, and a round's pieces)
   if ((blocks + 2 * kCUs) * (pl.bn == 16 ? 1024 : 512) > int64_t(UINT32_MAX)) return TSS_E_ARG;
+  Ranges at;
+  at.reads(A, M * K);
+  at.reads(B, N * K);
+  at.reads(sa, M * 4);
+  at.reads(sb, N * 4);
+  at.writes(C, M * N * (out_dtype == TSS_F32 ? 4 : 2));
+  if (split) at.writes(workspace, a.splits * slice_elements(M, N) * 4);
+  if (at.clash()) return TSS_E_ARG;
   a.tiles_m = int32_t(tiles_m);
   a.tiles_n = int32_t(tiles_n);
   hipError_t err;

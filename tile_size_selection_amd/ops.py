@@ -317,7 +317,8 @@ def quantize_fp8(x, fp8: str = "e4m3", gated: bool = False, block_rows: int = 1,
 def quantize_int8(x, gated: bool = False, out=None, scale=None) -> Tuple["torch.Tensor", "torch.Tensor"]:
     """(q, scale) of x (rows, d), or with gated of silu(gate) * up where x is
     (rows, 2 d), gate then up: q int8 in -127 .. 127 and scale (rows,) float32,
-    the row's largest magnitude / 127.  d a multiple of 8 up to 32768."""
+    the row's largest magnitude / 127.  d a multiple of 8 up to 32768.  out and
+    scale over x or each other are refused."""
     dt = _name(x, "x", ("f16", "bf16", "f32"))
     if x.dim() != 2 or (gated and x.shape[1] % 2):
         raise ValueError("x must be (rows, d), or (rows, 2 d) with gated")
@@ -384,7 +385,8 @@ def gemm_int8(A, B, sa, sb, out_dtype: str = "bf16", out=None, workspace=None):
     token, and int8 B (N, K) with sb (N,), one for each channel; the sums over K
     are exact.  out_dtype 'bf16', 'f16' or 'f32'.  K a multiple of 16 below
     2^17.  workspace: a device tensor of at least gemm_int8_workspace_size bytes
-    (allocated here when one is needed and not given)."""
+    (allocated here when one is needed and not given).  out and workspace over
+    an operand or each other are refused."""
     _name(A, "A", ("i8",))
     _name(B, "B", ("i8",))
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
