@@ -698,14 +698,14 @@ int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x,
  * TSS_BF16 or TSS_F32) and out are host memory and read before the call
  * returns; what grads and out point to is device memory, each tensor without
  * gaps and aligned to its elements (to 16 bytes for the full rate), out[i] of
- * grads[i]'s type.  out[i] may be grads[i]; otherwise no output, nor *norm, may
- * overlap another output or an input.  Squares are added in 64 bits and a fixed order.
+ * grads[i]'s type.  out[i] may be grads[i]; otherwise no output, nor *norm or
+ * the workspace, may overlap another or an input.  Squares are added in 64 bits and a fixed order.
  * A norm that is NaN makes every output NaN; an infinite one multiplies by 0.
  * max_norm >= 0 (not read when out is NULL).  At most 2^40 elements in all.
  * workspace: device memory of at least tss_clip_grad_norm_workspace_size(n,
  * sizes) bytes, 8-byte aligned, scratch (may be NULL when that is 0).  n == 0:
  * the norm is 0.
- * Errors: TSS_E_ARG (also overlapping outputs), TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
+ * Errors: TSS_E_ARG (also for overlaps), TSS_E_DTYPE, TSS_E_ALIGN, TSS_E_HIP.
  */
 int32_t tss_clip_grad_norm(int64_t n, const void *const *grads, const int64_t *sizes, const int32_t *dtypes,
                            float max_norm, void *const *out, float *norm, void *workspace, int64_t workspace_bytes,

@@ -1,6 +1,8 @@
 """Calls whose outputs or workspace overlap what else they read or write are
 refused before any device work (their workgroups run in no order: each such
 call would be a race), through the C ABI with addresses that are never touched."""
+import ctypes
+
 import pytest
 
 from tile_size_selection_amd import _capi as C
@@ -118,3 +120,22 @@ SPLIT = dict(GEMM, M=256, N=512, K=8192, B=at(8), sa=at(16), sb=at(17), C=at(18)
     (SPLIT, dict(ws=at(18))), (SPLIT, dict(ws=at(18, -16))), (SPLIT, dict(C=at(24, 16)))])
 def test_gemm_int8(base, change):
     assert refused(C.lib().tss_gemm_int8, base, change)
+
+
+def clip(tensors, out=None, norm=at(30), ws=at(31)):
+    """tensors: (address, elements), fp32."""
+    n = len(tensors)
+    pointers = lambda v: None if v is None else (ctypes.c_void_p * n)(*v)  # noqa: E731
+    return C.lib().tss_clip_grad_norm(n, pointers([a for a, _ in tensors]), (C.i64 * n)(*[e for _, e in tensors]), (C.i32 * n)(*[F32] * n),
+                                      1.0, pointers(out), norm, ws, MIB, None)
+
+
+TWO = [(at(0), 200000), (at(1), 100000)]  # 147 sums, 1176 bytes of workspace
+
+
+@pytest.mark.parametrize("call", [
+    dict(norm=at(0, 4)), dict(norm=at(1, 399996)), dict(norm=at(31, 1172)), dict(ws=at(0)), dict(ws=at(1, 399992)), dict(ws=at(1, -1168)),
+    dict(ws=at(30)), dict(out=[at(0), at(1)], ws=at(1)), dict(out=[at(2), at(3)], ws=at(3, 8)), dict(out=[at(2), at(3)], ws=at(0)),
+    dict(out=[at(2), at(3)], ws=at(30, -1168)), dict(out=[at(2), at(3)], norm=at(31, 8))])
+def test_clipping(call):
+    assert clip(TWO, **call) == ARG

@@ -86,3 +86,25 @@ def test_norms_over_their_inputs(rows, d, dtype):
     xhat = (want.h.double() - want.mean.double()[:, None]) * want.rstd.double()[:, None]
     for p, q, terms in ((got[1], grads[1], dy.double() * xhat), (got[2], grads[2], dy.double())):
         assert ((p.double() - q.double()).abs() <= 2 * (rows + 3) * 2.0 ** -24 * terms.abs().sum(0)).all()
+
+
+def test_clipping_beside_others():
+    """The norm and the workspace right behind and before the tensors."""
+    values = U.normal(U.gen(7), 300000).float()
+    want = values.to(CUDA)
+    norm = tss.clip_grad_norm([want[:200000], want[200000:]], 1.0)
+    need = 8 * (98 + 49)
+    for first in (0, need // 4):
+        buf = torch.zeros(300000 + need // 4 + 4, device=CUDA)
+        ts = buf[first:first + 300000]
+        ts.copy_(values)
+        ws = buf[0:need // 4] if first else buf[300000:300000 + need // 4]
+        pair = [ts[:200000], ts[200000:]]
+        at = buf[300000 + need // 4]
+        assert torch.equal(tss.grad_norm(pair, norm=at, workspace=ws), norm)
+        tss.clip_grad_norm(pair, 1.0, norm=at, workspace=ws)
+        assert torch.equal(ts, want) and torch.equal(at, norm)
+        for call in (dict(norm=ts[5]), dict(norm=at, workspace=ts)):
+            with pytest.raises(tss.TssError):
+                tss.grad_norm(pair, **call)
+        assert torch.equal(ts, want)

@@ -277,6 +277,20 @@ int32_t count_sums(int64_t n, const int64_t *sizes, Sums *out) {
   return st;
 }
 
+// Whether `bytes` at p overlap a tensor that is read or written.
+bool touches(const void *p, int64_t bytes, int64_t n, const void *const *in, void *const *out, const int64_t *sizes,
+             const int32_t *types) {
+  const uintptr_t begin = reinterpret_cast<uintptr_t>(p), end = begin + uintptr_t(bytes);
+  for (int64_t i = 0; i < n; ++i) {
+    const uintptr_t length = uintptr_t(sizes[i]) * bytes_of(types[i]);
+    for (const void *q : {in[i], out ? static_cast<const void *>(out[i]) : in[i]}) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(q);
+      if (begin < end && length && begin < at + length && at < end) return true;
+    }
+  }
+  return false;
+}
+
 // An output may be its own input; apart from that no output overlaps another
 // output or an input, nor does the norm's place.
 bool overlapping(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int32_t *types,
@@ -368,7 +382,13 @@ int32_t clip(int64_t n, const void *const *grads, const int64_t *sizes, const in
   if (reinterpret_cast<uintptr_t>(norm) % 4 || reinterpret_cast<uintptr_t>(workspace) % 8) return TSS_E_ALIGN;
   const int64_t sums = c.sums;
   if (sums && !c.one() && (!workspace || workspace_bytes < sums * 8)) return TSS_E_ARG;
-  if (out && overlapping(n, grads, out, sizes, dtypes, norm)) return TSS_E_ARG;
+  if (out ? overlapping(n, grads, out, sizes, dtypes, norm) : touches(norm, sizeof(float), n, grads, out, sizes, dtypes))
+    return TSS_E_ARG;
+  if (sums && !c.one()) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(workspace), at = reinterpret_cast<uintptr_t>(norm);
+    if (at < begin + uintptr_t(sums) * 8 && begin < at + sizeof(float)) return TSS_E_ARG;
+    if (touches(workspace, sums * 8, n, grads, out, sizes, dtypes)) return TSS_E_ARG;
+  }
   double *partial = static_cast<double *>(workspace);
   auto go = [&](auto launch) { return launch(n, grads, sizes, dtypes, max_norm, out, norm, partial, c, bytes, s); };
   return tensors <= kSmallTable ? go(launch_clip<kSmallTable>) : go(launch_clip<kTable>);

@@ -541,7 +541,7 @@ def _list_streamed(f):
 def grad_norm(grads: Sequence["torch.Tensor"], norm=None, workspace=None):
     """The norm over all elements of the tensors (f16, bf16, f32, mixed), a
     float32 scalar on the GPU: squares are added in 64 bits, in a fixed order.
-    norm: the scalar to write into, else allocated."""
+    norm: the scalar to write into (in none of the tensors), else allocated."""
     return _clip(grads, 0.0, None, norm, workspace)
 
 
@@ -552,5 +552,6 @@ def clip_grad_norm(grads: Sequence["torch.Tensor"], max_norm: float, out=None, n
     min(1, max_norm / (norm + 1e-6)) in float32, rounded once.  Returns grad_norm's
     norm; nothing is read back to the host.  A NaN norm makes every element
     NaN, an infinite one multiplies by 0.  Tensors must lie in memory without
-    gaps, and none may be given twice or overlap another that is written."""
+    gaps, and none may be given twice or overlap another that is written, nor
+    may norm or workspace lie in one."""
     return _clip(grads, max_norm, grads if out is None else out, norm, workspace)
