@@ -130,20 +130,12 @@ hipError_t launch_rounds(const Int8Args &a, int64_t tiles, hipStream_t s) {
                     whole + rest * tile_pieces(int(rest), false), Tile256::THREADS, kRoundsLds, s);
 }
 
-// The kernel for few rows: waves of a workgroup that takes `blocks` of K at a time in each.
-int rows_waves(int64_t K, int blocks) {
-  const int64_t nk = (K + 127) / 128, nw = (nk + blocks - 1) / blocks;
-  return int(nw > 16 ? 16 : nw);
-}
-
-hipError_t launch_rows(const Int8Args &a, hipStream_t s) {
-  auto go = [&](auto kernel, int groups, int blocks) {
-    const int nw = rows_waves(a.K, blocks), waves = nw > groups ? nw : groups;  // a wave joins each column group
-    const int64_t workgroups = int64_t(a.tiles_m) * ((int64_t(a.N) + 16 * groups - 1) / (16 * groups));
-    hipLaunchKernelGGL(kernel, dim3(uint32_t(workgroups)), dim3(waves * 64), waves * groups * 1024, s, a);
+hipError_t launch_rows(const Int8Args &a, const Int8RowsLaunch &f, hipStream_t s) {
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(f.workgroups)), dim3(f.waves * 64), f.waves * f.groups * 1024, s, a);
   };
-  if (int8_row_groups(a.M, a.N) == 2) go(gemm_int8_rows_kernel<2, 1>, 2, 1);
-  else go(gemm_int8_rows_kernel<1, 4>, 1, 4);
+  if (f.groups == 2) go(gemm_int8_rows_kernel<2, 1>);
+  else go(gemm_int8_rows_kernel<1, 4>);
   return hipGetLastError();
 }
 
@@ -248,8 +240,10 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   a.C = split ? workspace : C;
   a.out_dtype = split ? kInt8Sums : out_dtype;
   const int64_t tiles_m = (M + pl.bm - 1) / pl.bm, tiles_n = (N + pl.bn - 1) / pl.bn, blocks = tiles_m * tiles_n * a.splits;
-  // the launch's thread count is 32 bits (1024 threads at most, and a round's pieces)
-  if ((blocks + 2 * kCUs) * (pl.bn == 16 ? 1024 : 512) > int64_t(UINT32_MAX)) return TSS_E_ARG;
+  const Int8RowsLaunch rows = int8_rows_launch(M, N, K);
+  // the launch's thread count is 32 bits (tiles: 512 threads at most, and a round's pieces)
+  const int64_t threads = pl.bn == 16 ? rows.workgroups * rows.waves * 64 : (blocks + 2 * kCUs) * 512;
+  if (threads > int64_t(UINT32_MAX)) return TSS_E_ARG;
   Ranges at;
   at.reads(A, M * K);
   at.reads(B, N * K);
@@ -262,7 +256,7 @@ int32_t tss_gemm_int8(int64_t M, int64_t N, int64_t K, const void *A, const void
   a.tiles_n = int32_t(tiles_n);
   hipError_t err;
   if (pl.bn == 16) {
-    err = launch_rows(a, s);
+    err = launch_rows(a, rows, s);
   } else if (pl.bm == 256) {
     err = launch_rounds(a, blocks, s);
   } else if (pl.bm == 128) {

@@ -65,6 +65,19 @@ inline void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
 // at the kernel).
 inline int int8_row_groups(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 31) / 32) >= 192 ? 2 : 1; }
 
+// The launch of the kernel for few rows: groups of 16 columns of a workgroup,
+// workgroups, and waves of each (as many as join a group each, at least).
+struct Int8RowsLaunch {
+  int groups;
+  int64_t workgroups;
+  int waves;
+};
+inline Int8RowsLaunch int8_rows_launch(int64_t M, int64_t N, int64_t K) {
+  const int groups = int8_row_groups(M, N), blocks = groups == 2 ? 1 : 4;  // blocks of 128 of K that a wave takes at a time
+  const int64_t nk = (K + 127) / 128, nw = (nk + blocks - 1) / blocks, most = nw > 16 ? 16 : nw;
+  return {groups, (M + 15) / 16 * ((N + 16 * groups - 1) / (16 * groups)), int(most > groups ? most : groups)};
+}
+
 // By the time that each way takes, in ns.  The kernel for few rows: 3200, and
 // the longer of a workgroup's own reads and all of them, from L2 at 8.5 TB/s
 // (64 x 4096 x 4096: 14.8 us, 64 x 1024 x 8192 11.1, 64 x 8192 x 1024 9.0).
