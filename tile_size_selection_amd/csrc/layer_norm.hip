@@ -28,6 +28,20 @@ __device__ __forceinline__ float sum_slots(const float *slots, int n) {
   return sum_lanes<16>(i < n ? slots[i] : 0.0f);
 }
 
+// The same for rows of CH chunks a thread.  The widest in turn: their registers
+// are full, and what the lanes' sums keep in some more is spilled (2000 x
+// 32768, bf16, the gradients: 356 us, by lanes and with several teams' indices 528).
+template <int CH>
+__device__ __forceinline__ float wave_sums(const float *slots, int n) {
+  if constexpr (CH <= 2) {
+    return sum_slots(slots, n);
+  } else {
+    float s = 0;
+    for (int i = 0; i < n; ++i) s += slots[i];
+    return s;
+  }
+}
+
 // ---- forward ----
 
 struct NormArgs {
@@ -69,8 +83,8 @@ __global__ __launch_bounds__(kMaxThreads) void layer_norm_kernel(NormArgs p) {
       red[set][slot + 1][wave] = v;
     }
     __syncthreads();
-    u = sum_slots(red[set][slot], wpr);
-    v = sum_slots(red[set][slot + 1], wpr);
+    u = wave_sums<CH>(red[set][slot], wpr);
+    v = wave_sums<CH>(red[set][slot + 1], wpr);
   };
 
   Raw8<T> xr[CH], rr[CH], wr[CH], br[CH];
@@ -235,8 +249,9 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
   constexpr bool kNarrow = L < 64;
   __shared__ float red[2][2][kMaxThreads / 64];
   const int wave = threadIdx.x >> 6, nw = blockDim.x >> 6;
-  const int wpr = kNarrow ? 1 : p.wpr, lanes = kNarrow ? L : wpr * 64, t = threadIdx.x % lanes;
-  const int teams = kNarrow ? kNarrowThreads / L : CH > 1 ? 1 : nw / wpr, team = threadIdx.x / lanes;
+  constexpr bool kOne = CH > 1;  // one team: known here, because the widest rows have no register to spare
+  const int wpr = kNarrow ? 1 : p.wpr, lanes = kNarrow ? L : wpr * 64, t = kOne ? threadIdx.x : threadIdx.x % lanes;
+  const int teams = kNarrow ? kNarrowThreads / L : kOne ? 1 : nw / wpr, team = kOne ? 0 : threadIdx.x / lanes;
   const int stride = gridDim.x * teams;
   const int rows = p.rows, d = p.d;
   const T *dy = static_cast<const T *>(p.dy), *hh = static_cast<const T *>(p.h), *dh = static_cast<const T *>(p.dh);
@@ -328,8 +343,8 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
           red[slot][1][wave] = sx;
         }
         __syncthreads();
-        sg = sum_slots(&red[slot][0][team * wpr], wpr);
-        sx = sum_slots(&red[slot][1][team * wpr], wpr);
+        sg = wave_sums<CH>(&red[slot][0][team * wpr], wpr);
+        sx = wave_sums<CH>(&red[slot][1][team * wpr], wpr);
         slot ^= 1;
       }
       sg *= inv_d;
@@ -337,7 +352,7 @@ __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_
 #pragma unroll
       for (int c = 0; c < CH; ++c) {
         const int col = col_of(c);
-        if (col >= d || row >= rows) continue;
+        if (col >= d || (!kOne && row >= rows)) continue;
         float g[8], x[8], o[8], w[8];
         if constexpr (D > 0) {
           opaque(ca[c]);
