@@ -1,6 +1,6 @@
 """What libtss.so holds for the GPU, read from the symbol tables of its own code
-objects: bytes of scratch memory that a kernel's lanes take (registers that do
-not fit)."""
+objects: kernels only where the host launches them, and the bytes of scratch
+memory that a kernel's lanes take (registers that do not fit)."""
 import os
 import struct
 
@@ -57,3 +57,20 @@ def test_wide_norms_keep_their_registers(objects):
         assert all(v == 0 for v in scratch(objects, "layer_norm_backward_kernel", chunks).values())
     assert all(v == 0 for v in scratch(objects, "layer_norm_kernel", "Li2ELi64E").values())
     assert all(v == 0 for v in scratch(objects, "layer_norm_backward_few_kernel").values())
+
+
+def kernels(objects):
+    return [n[:-3] for o in objects for n in o if n.endswith(".kd")]
+
+
+def test_a_headers_kernels_are_not_in_every_unit(objects):
+    """A kernel of a unit's own in a header is copied into whatever includes it, launched or not.  (Templates are made
+    where they are launched.)"""
+    names = [n for n in kernels(objects) if n.startswith("_ZN3tssL")]
+    assert not names, f"of internal linkage, from a header: {sorted(names)}"
+
+
+def test_the_host_knows_every_kernel(objects):
+    """A kernel without the handle that the host launches it by is one that nothing reaches."""
+    handles = {n for n, _ in symbols(open(LIB, "rb").read())}
+    assert sorted(set(kernels(objects)) - handles) == []

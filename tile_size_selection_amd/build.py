@@ -49,7 +49,8 @@ def sources():
     return ([os.path.join(CSRC, "planner.cpp"), os.path.join(CSRC, "api.cpp"), os.path.join(CSRC, "lds_probe.hip"),
              os.path.join(CSRC, "noalloc.cpp")]
             + [os.path.join(CSRC, f) for f in ("norm.hip", "quantize.hip", "gemm_fp8.hip", "gemm_grouped.hip",
-                                              "layer_norm.hip", "order.hip", "gemm_int8.hip", "clip.hip")]
+                                              "layer_norm.hip", "column_sums.hip", "order.hip", "gemm_int8.hip",
+                                              "clip.hip")]
             + sorted(glob.glob(os.path.join(CSRC, "inst", "*.hip"))))
 
 

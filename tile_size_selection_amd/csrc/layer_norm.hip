@@ -670,7 +670,7 @@ int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const vo
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows == 0) {
     for (float *out : {dweight, dbias})
-      if (out) hipLaunchKernelGGL(zero_f32_kernel, dim3(uint32_t((d + 255) / 256)), dim3(256), 0, s, int(d), out);
+      if (out) launch_zero_f32(d, out, s);
     return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
   }
   if (!dy || !h || !weight || !mean || !rstd || !dx) return TSS_E_ARG;

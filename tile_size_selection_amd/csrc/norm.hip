@@ -285,7 +285,7 @@ int32_t tss_rms_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void
   if (!dweight) return TSS_E_ARG;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (rows == 0) {
-    hipLaunchKernelGGL(zero_f32_kernel, dim3(uint32_t((d + 255) / 256)), dim3(256), 0, s, int(d), dweight);
+    launch_zero_f32(d, dweight, s);
     return hipGetLastError() == hipSuccess ? TSS_OK : TSS_E_HIP;
   }
   if (!dy || !h || !weight || !rstd || !dx) return TSS_E_ARG;
