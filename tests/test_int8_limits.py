@@ -50,3 +50,9 @@ def test_the_waves_of_a_launch(tmp_path):
 
 def test_two_groups_of_columns_are_tested(tmp_path):
     assert all(way[:2] == (16, 2) for way in run(tmp_path, TWO_GROUPS))
+
+
+def test_two_groups_where_one_would_take_a_second_round_of_cus(tmp_path):
+    want = {(16, 4096, 4096): 1, (16, 4097, 4096): 2, (1, 5120, 4096): 2, (16, 6143, 512): 2, (32, 2048, 4096): 1, (32, 2049, 4096): 2,
+            (64, 1024, 4096): 1, (64, 1025, 4096): 2}
+    assert [way[:2] for way in run(tmp_path, want)] == [(16, n) for n in want.values()]

@@ -252,8 +252,8 @@ __global__ __launch_bounds__(G::THREADS) void gemm_int8_rounds_kernel(Int8Args p
 // their sums are joined through LDS (whole numbers: any order).  A (read by
 // every workgroup) comes from L2; two column groups halve that.  U: blocks of K
 // whose loads a wave has in flight.  4 x 8192 x 8192, weights in no cache: 16.5
-// us, 4.1 TB/s of B (one group, U = 4: 18.8), 16 rows 19.2 (24.1); where two
-// groups leave CUs free, 16 x 4096 x 4096: 8.9 and with one 7.4.
+// us, 4.1 TB/s of B (one group, U = 4: 18.6), 16 rows 19.2 (23.8); where one
+// group gives no CU a second workgroup, 16 x 4096 x 4096, 7.8 and with two 9.4.
 template <typename O>
 __device__ __forceinline__ void put_int8_row(const Int8Args &p, int row, int col, const float (&v)[4]) {
   O *to = static_cast<O *>(p.C) + int64_t(row) * p.N + col;

@@ -61,9 +61,12 @@ inline void split_ranges(int64_t K, int splits, int32_t *n, int32_t *k_split) {
 }
 
 // Products of 8-bit integers.  Groups of 16 columns of a workgroup of the
-// kernel for few rows: two where that leaves no CU free (its measurements are
-// at the kernel).
-inline int int8_row_groups(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 31) / 32) >= 192 ? 2 : 1; }
+// kernel for few rows: two where workgroups of one would be more than the CUs,
+// which then take a second round (us with one group and with two, weights in no
+// cache; 16 rows, K = 4096: N = 4000 7.6 and 9.1, 4096 7.8 and 9.4, 4112 9.9 and
+// 9.1, 5120 11.0 and 9.3; K = 8192: 4096 12.7 and 16.9, 5120 21.7 and 17.8; 64
+// rows, K = 4096: 1024 7.3 and 9.0, 1040 10.1 and 9.0; K <= 1024 within 0.2).
+inline int int8_row_groups(int64_t M, int64_t N) { return (M + 15) / 16 * ((N + 15) / 16) > kCUs ? 2 : 1; }
 
 // The launch of the kernel for few rows: groups of 16 columns of a workgroup,
 // workgroups, and waves of each (as many as join a group each, at least).
