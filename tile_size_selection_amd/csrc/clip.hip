@@ -12,7 +12,13 @@
 // 226505854 elements in 60 tensors, fp32 and bf16: 352 us, 110 of it the norm's
 // pass (5.6 TB/s); the outputs pass the caches by (through them 379).
 // The tensors' addresses travel in the kernel's arguments, kTable at a time:
-// no copy from host memory, so a captured graph holds all that it needs.
+// no copy from host memory, so a captured graph holds all that it needs.  Every
+// workgroup that scales reads the sums of all tables, which costs more than the
+// elements where there are many tables: n tensors of 100000 bf16 elements, in
+// place, kernels only: n = 128 24 us, 256 50, 512 122, 1000 323, 2000 907, 4000
+// 2755 (their bytes at a large copy's rate: 15, 30, 60, 117, 234, 468).
+// Tensors off 16-byte borders are taken element by element: 2^26 bf16 elements
+// 140 us, on a border 84; fp32 166 and 135.
 #include <algorithm>
 #include <new>
 #include <vector>
@@ -197,7 +203,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_scale_kernel(ClipTable<K> t
   const double n = sqrt(total_squares(partial, sums, red));
   if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = float(n);
   const float factor = clip_factor(n, max_norm);
-  // The last elements first: the norm's pass has left them in the caches.
+  // The table's last elements first: of a single table, the norm's pass has left them in the caches.
   with_range(t, gridDim.x - 1 - blockIdx.x, gridDim.x, [&](auto v, int k, int64_t from, int64_t end) {
     using T = decltype(v);
     if (factor == 1.0f && t.out[k] == t.in[k]) return;

@@ -6,7 +6,8 @@
 //
 // Quantising is bound by memory: a row is read once and stays in registers
 // while its largest magnitude is found: 16384 x 4096, bf16: 39 us (5.2 TB/s),
-// 4 x 8192: 2.4.
+// 4 x 8192: 2.4.  Gated, which takes exp and a division for each value: 85 (3.9
+// TB/s) and 4.4.
 #include <atomic>
 
 #include "gemm_int8_kernel.h"

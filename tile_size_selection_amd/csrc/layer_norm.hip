@@ -13,8 +13,11 @@
 // summed about a first mean; the mean's own error, which that second sum
 // shows, is taken out again, so that a mean far from zero costs no digits.
 // 16384 x 4096, bf16: 50 us (5.3 TB/s; a large copy: 5.1), with residual 99 to 105,
-// backward 106, of which 4.5 add up dw and db; 300000 x 128, fp16: 29.5 us (5.2
-// TB/s); one row of 4096: 2.7 us, its backward 3.5.
+// to int8 60 and 91; backward with dh 107, of which 5 add up dw and db, without 84;
+// 300000 x 128, fp16: 29.5 us (5.2 TB/s), to int8 38; one row of 4096: 2.5 us,
+// its backward 4.2 (in a graph of such calls on the same operands 3.5).
+// 2000 x 32768, bf16: 69 us, to int8 66 (fp16 91: four chunks of a row in 128
+// registers, 16 of them spilled; fp32 to int8 115, 20 spilled), backward 364.
 #include "ranges.h"
 #include "row_launch.h"
 
@@ -243,7 +246,7 @@ constexpr int kTeamWaves = 8;  // of a workgroup of several teams
 // atomics, the same bits on every run).  D rows' loads are in flight while a
 // row is reduced and written; D == 0 (wide rows, whose registers are full with dw and db):
 // none are, and the row is read again, from the caches, for its output (8000 x 8200, fp16: 139 us, with
-// one row ahead, which spills, 190).
+// one row ahead, which spills, 190; with dh).
 template <typename T, int CH, int D, int L>
 __global__ __launch_bounds__(L == 64 ? kMaxThreads : kNarrowThreads) void layer_norm_backward_kernel(BackArgs p) {
   constexpr bool kNarrow = L < 64;
@@ -553,10 +556,10 @@ int64_t backward_teams(const Team &f) {
 // teams: one, whose loads are twice the bytes), but each adds 16 bytes a column
 // (its shares of dw and db, written and read) to the 8 a column that a row of
 // 16-bit elements moves, so no more than one for every 8 turns where that still
-// gives every CU one.  100000 x 512, bf16: 83 us, 60000 x 1024 100, by one
+// gives every CU one.  With dh: 100000 x 512, bf16: 83 us, 60000 x 1024 100, by one
 // workgroup a CU 80 and 104, by four 84 and 106, and by more of one row each,
 // without teams, 87 and 107; 200000 x 264 86 (128 without); fp32 100000 x 512
-// 152, by two workgroups 164.
+// 152, by two workgroups 164.  Without dh: 64, 77, 80 and 115.
 int64_t backward_blocks(int64_t rows, int64_t d, int64_t size) {
   constexpr int64_t cus = 256;
   const Team f = team_of(d, 1);
@@ -567,7 +570,7 @@ int64_t backward_blocks(int64_t rows, int64_t d, int64_t size) {
 }
 
 // The columns' workgroups take 4 us and 2 more for 1000 rows; rows of more bytes in all keep the CUs busy in
-// two launches too (us, one launch and two; bf16 256 x 4096: 5.3 and 10.9; 1000 x 1024 6.4 and 9.5, 8192 17.9
+// two launches too (us in a graph of such calls on the same operands, with dh, one launch and two; bf16 256 x 4096: 5.3 and 10.9; 1000 x 1024 6.4 and 9.5, 8192 17.9
 // and 21.0; 2000 x 128 8.6 and 8.1; fp32 1000 x 4096: 17.9 and 18.5, 8192 34 and 30; 500 x 16384 42.0 and 41.5).
 bool few(int64_t rows, int64_t d, int64_t size) {
   return rows <= 1024 && d <= kFewThreads * 16 && rows * d * size <= int64_t(1) << 24;
@@ -588,8 +591,8 @@ void launch_few(const BackArgs &a, float *dweight, float *dbias, hipStream_t s) 
 }
 
 // Columns of a workgroup: 128 bytes, which makes the most of the CUs; up to 64
-// rows 256 columns, fewer workgroups (64 x 16384, bf16: 5.1 us, fp32 1 x 16384
-// 4.8 and by 32 columns 11.5).
+// rows 256 columns, fewer workgroups (in a graph, as above: 64 x 16384, bf16: 4.7
+// us, fp32 1 x 16384 4.7 and by 32 columns 11.5).
 template <typename T>
 void launch_few(const BackArgs &a, float *dweight, float *dbias, hipStream_t s) {
   if (a.rows <= 64) launch_few<T, 32>(a, dweight, dbias, s);
@@ -600,7 +603,7 @@ template <typename T>
 void launch_backward(const BackArgs &a, hipStream_t s) {
   const Team f = team_of(a.d, 1);
   // One row ahead: two rows' registers leave room for fewer waves (300000 x 128,
-  // bf16: 63 us, two ahead 68; 16384 x 4096, fp32: 202 and 249; bf16 106 and 110).
+  // bf16, with dh: 65 us, two ahead 68; 16384 x 4096, fp32: 199 and 249; bf16 107 and 110).
   const dim3 grid(uint32_t(backward_blocks(a.rows, a.d, sizeof(T)))), block(f.lanes < 64 ? kNarrowThreads : backward_teams(f) * f.waves * 64);
   const int lds = f.lanes == 64 && backward_teams(f) > 1 ? int(block.x) * 32 : 0;  // to join the teams' sums
   auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, lds, s, a); };
