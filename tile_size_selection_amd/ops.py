@@ -496,6 +496,8 @@ def _refuse_list(grads, out):
     if out is not None and len(out) != len(grads):
         raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
     for t, o in zip(grads, grads if out is None else out):
+        if not (isinstance(t, torch.Tensor) and isinstance(o, torch.Tensor)):
+            raise ValueError(f"gradients and outputs must be tensors, not {type(o if isinstance(t, torch.Tensor) else t).__name__}")
         _name(t, "a gradient", ("f16", "bf16", "f32"))
         if o.shape != t.shape or o.dtype != t.dtype or o.stride() != t.stride():
             raise ValueError(f"an output must have its gradient's shape, type and strides, {t.dtype} {tuple(t.shape)} "
@@ -508,11 +510,11 @@ def _clip(grads, max_norm: float, out, norm, workspace):
         out = list(out)
     if not grads and norm is None:
         raise ValueError("without tensors norm must be given")
-    device = grads[0].device if grads else norm.device
     table = C.bind().table(grads, out, _CLIPPED)
     if table is None:
         _refuse_list(grads, out)
     at, sizes, types, to, index = table
+    device = grads[0].device if grads else norm.device
     norm = _out(norm, "norm", (), torch.float32, device)
     if grads and norm.get_device() != index:
         raise ValueError("every tensor must be on the same GPU")
