@@ -19,12 +19,15 @@ class Ranges {
 
   // Whether any written bytes are read, or written twice, in another way than that.
   bool clash() const {
-    for (int i = 0; i < n_; ++i)
+    for (int i = 0; i < n_; ++i) {
+      const Range &a = of_[i];
+      if (!a.written) continue;
       for (int j = 0; j < n_; ++j) {
-        const Range &a = of_[i], &b = of_[j];
-        if (i == j || !a.written || a.begin >= b.end || b.begin >= a.end) continue;
+        const Range &b = of_[j];
+        if (i == j || a.begin >= b.end || b.begin >= a.end) continue;
         if (b.written || a.begin != b.begin || !(a.over >> j & 1)) return true;
       }
+    }
     return false;
   }
 
