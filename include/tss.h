@@ -665,9 +665,9 @@ int32_t tss_layer_norm(int64_t rows, int64_t d, int32_t dtype, const void *x, co
  * (the gradient of x and of residual; dh, which may be NULL, is what arrives
  * through residual_out), dweight[d] (fp32) = sum over rows of dy xhat and
  * dbias[d] (fp32; may be NULL) = sum over rows of dy, added in a fixed order.
- * dx may be dy, h or dh; other overlaps are refused.  workspace: device memory of at least
- * tss_layer_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned,
- * scratch.  rows == 0: dweight and dbias are zero-filled.
+ * dx may be dy, h or dh; other overlaps are refused.  workspace: device memory
+ * of at least tss_layer_norm_backward_workspace_size(rows, d) bytes, 16-byte
+ * aligned, scratch.  rows == 0: dweight and dbias are zero-filled.
  * Errors: as tss_layer_norm; TSS_E_ARG for a missing or small workspace.
  */
 int32_t tss_layer_norm_backward(int64_t rows, int64_t d, int32_t dtype, const void *dy, const void *h,
@@ -699,7 +699,8 @@ int32_t tss_quantize_int8(int64_t rows, int64_t d, int32_t dtype, const void *x,
  * returns; what grads and out point to is device memory, each tensor without
  * gaps and aligned to its elements (to 16 bytes for the full rate), out[i] of
  * grads[i]'s type.  out[i] may be grads[i]; otherwise no output, nor *norm or
- * the workspace, may overlap another or an input.  Squares are added in 64 bits and a fixed order.
+ * the workspace, may overlap another or an input.  Squares are added in 64 bits
+ * and a fixed order.
  * A norm that is NaN makes every output NaN; an infinite one multiplies by 0.
  * max_norm >= 0 (not read when out is NULL).  At most 2^40 elements in all.
  * workspace: device memory of at least tss_clip_grad_norm_workspace_size(n,

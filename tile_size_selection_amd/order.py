@@ -46,9 +46,9 @@ def _order(order, tokens: Optional[int] = None) -> Tuple[int, int]:
 def sort_by_expert(expert, experts: int, sizes=None, row=None, choice=None, workspace=None) -> ExpertOrder:
     """ExpertOrder of expert (tokens, top), int32 or int64: the stable order of
     the choices by expert.  experts: 1 to 4096.  sizes, row, choice: outputs to
-    write into, else allocated (row may be an int32 expert itself); workspace: a device tensor of at least
-    tss_sort_by_expert_workspace_size bytes (allocated here when one is needed
-    and not given)."""
+    write into, else allocated (row may be an int32 expert itself); workspace: a
+    device tensor of at least tss_sort_by_expert_workspace_size bytes (allocated
+    here when one is needed and not given)."""
     if expert.dim() != 2 or expert.shape[1] < 1 or expert.dtype not in (torch.int32, torch.int64):
         raise ValueError("expert must be (tokens, top) int32 or int64")
     tokens, top = expert.shape
